@@ -529,6 +529,183 @@ rarn_status rarn_ipc_export(const void *ptr, void *handle);
 rarn_status rarn_ipc_import(const void *handle, void **ptr);
 rarn_status rarn_ipc_close(void *ptr);
 
+/*
+ * Attention side: per-head norm and position rotation, the 8-bit key / value
+ * cache, and attention of drafted tokens over it.  A model that calls the
+ * forms above on its residual stream projects y to queries, keys and values;
+ * these are the steps between that projection and the next residual add.
+ * The pages have no counterpart; the norm is "RMSNorm kernel", 1 Background,
+ * over one head's elements, and the codes and scales are those of the 8-bit
+ * output forms.
+ *
+ * A rarn_heads names a [T, heads, D] matrix inside a larger allocation: head h
+ * of token t starts at element t * token_stride + h * head_stride of `data`
+ * and its D elements are adjacent (q, k and v may be slices of one packed
+ * projection, in either order of tokens and heads).  Outputs' rows must not
+ * overlap one another (RARN_ERR_INVALID_ARG).
+ *
+ * A rarn_kv_cache is a pool of num_pages pages of page_size slots.  The codes
+ * of head h at slot s of page g are head_dim bytes at byte
+ *   g * page_stride + h * head_stride + s * slot_stride
+ * of `k` (keys) and `v` (values), in `format`.  RARN_SCALE_ROW: each has its
+ * own binary32 scale, at element g * scale_page_stride + h * scale_head_stride
+ * + s * scale_slot_stride of k_scale / v_scale, written with the codes;
+ * RARN_SCALE_TENSOR: k_scale[0] and v_scale[0] are read (scale strides are
+ * ignored).  A code stands for its value times its scale.  head_dim must be a
+ * multiple of 16 up to 256, `k`, `v` 16-byte aligned and the code strides
+ * multiples of 16 (else RARN_ERR_UNSUPPORTED); rows that share memory:
+ * RARN_ERR_INVALID_ARG.  Keys and values may lie interleaved by pages in one
+ * allocation.
+ *
+ * Indices in device memory (positions, slots, page tables, lengths) cannot be
+ * checked before the launch.  What lies outside its table is left out, never
+ * read or written, and sets bit 4 of the watchdog word (rarn_watchdog).
+ */
+typedef struct rarn_heads {
+    void *data;
+    int64_t token_stride, head_stride;  /* elements */
+    int32_t heads;
+    rarn_dtype dtype;
+} rarn_heads;
+
+typedef struct rarn_kv_cache {
+    void *k, *v;                                     /* codes */
+    float *k_scale, *v_scale;
+    int64_t page_stride, head_stride, slot_stride;   /* bytes, of k and of v */
+    int64_t scale_page_stride, scale_head_stride, scale_slot_stride;  /* elements */
+    int64_t num_pages;
+    int32_t page_size;
+    int32_t heads;
+    int32_t head_dim;
+    rarn_fp8_format format;
+    rarn_scale_mode scale_mode;
+} rarn_kv_cache;
+
+/* The rotation: row `position` of cos_sin [table_rows, rot_dim] (dense
+ * binary32) holds rot_dim / 2 cosines, then rot_dim / 2 sines.  The first
+ * rot_dim elements of a head turn in pairs (a, b) -> (a cos - b sin,
+ * b cos + a sin): elements (i, i + rot_dim / 2) in the HALF style, (2i, 2i + 1)
+ * INTERLEAVED; the others stay.  positions: T values, one per token. */
+typedef enum rarn_rotation_style {
+    RARN_ROTATE_HALF = 0,
+    RARN_ROTATE_INTERLEAVED = 1
+} rarn_rotation_style;
+
+typedef struct rarn_rotation {
+    const float *cos_sin;
+    const int64_t *positions;
+    int64_t table_rows;
+    int32_t rot_dim;  /* even, 2 .. D */
+    rarn_rotation_style style;
+} rarn_rotation;
+
+#define RARN_MAX_HEADS 4096
+#define RARN_MAX_HEAD_DIM 1024
+#define RARN_MAX_PAGE_SIZE (1 << 20)
+#define RARN_MAX_SEQUENCES (1 << 20)
+#define RARN_MAX_MASK_WORDS (1 << 16)
+#define RARN_MAX_STRIDE ((int64_t)1 << 40)
+
+/*
+ * q_out = rotate(norm(q) * q_gamma), k_out = rotate(norm(k) * k_gamma), head by
+ * head: norm(x) = x * rsqrt(mean(x^2) + eps) over the head's D elements,
+ * binary32 throughout, one rounding to the storage type at the end.  A NULL
+ * gamma leaves out that tensor's norm, a NULL rotation the rotation.  q_out may
+ * equal q and k_out k (same data and strides); every other overlap of an
+ * output with another buffer returns RARN_ERR_ALIAS, except that matrices of
+ * one token stride may lie side by side within it.  A token whose position is
+ * outside 0 .. table_rows - 1 keeps its output rows as they were.
+ *
+ * All matrices have one storage type.  D is 1 .. RARN_MAX_HEAD_DIM; with D and
+ * rot_dim multiples of 32 bytes, D at most 1024 bytes and every base and
+ * stride a multiple of 16 bytes, a kernel with 16-byte accesses runs,
+ * otherwise one that goes element by element.  T * heads (of q, k and v
+ * together) must stay below 2^31.
+ */
+rarn_status rarn_qk_norm_rope(rarn_heads q_out, rarn_heads k_out, rarn_heads q, rarn_heads k,
+                              const void *q_gamma, const void *k_gamma,
+                              const rarn_rotation *rotation, int64_t T, int64_t D, float eps,
+                              void *stream);
+
+/*
+ * Token t's keys and values into slot slots[t] of the cache (page
+ * slots[t] / page_size).  Row scales: s = max|x| / maxf over the head's
+ * elements (1 for zeros), code = x / s rounded to nearest even; tensor
+ * scales: code = x / scale[0], saturated.  A negative slot leaves the token
+ * out (padding).  The non-negative slots of one call must differ from one
+ * another: two tokens written to one slot race, and it may end up with the
+ * codes of one and the scale of the other.
+ */
+rarn_status rarn_kv_cache_write(const rarn_kv_cache *cache, rarn_heads k, rarn_heads v,
+                                const int64_t *slots, int64_t T, void *stream);
+
+/*
+ * Both in one pass: q_out as in rarn_qk_norm_rope, and the normalised, rotated
+ * keys and the values into the cache.  Keys are quantised from their binary32
+ * values, without a rounding to the storage type in between.  A token whose
+ * position is out of range is left out altogether; a negative slot leaves
+ * out its cache rows only.
+ */
+rarn_status rarn_qk_norm_rope_kv_write(rarn_heads q_out, const rarn_kv_cache *cache, rarn_heads q,
+                                       rarn_heads k, rarn_heads v, const void *q_gamma,
+                                       const void *k_gamma, const rarn_rotation *rotation,
+                                       const int64_t *slots, int64_t T, float eps, void *stream);
+
+/*
+ * The cache read back: sequence b's tokens j = 0, 1, ... go to output rows
+ * starts[b] .. starts[b + 1] - 1 (starts: B + 1 non-decreasing values in device
+ * memory), each code times its scale in binary32, rounded to the outputs'
+ * type.  Token j of sequence b lies at slot j % page_size of page
+ * page_table[b * table_stride + j / page_size]; table_width entries per
+ * sequence.  Rows before starts[0] and from starts[B] on stay as they were; a
+ * row whose page is missing becomes zeros.  k_out, v_out: [rows, heads, D] of
+ * one type (any of the three).
+ */
+rarn_status rarn_kv_cache_read(rarn_heads k_out, rarn_heads v_out, const rarn_kv_cache *cache,
+                               const int32_t *page_table, int64_t table_stride,
+                               int64_t table_width, const int32_t *starts, int64_t B,
+                               int64_t rows, void *stream);
+
+/*
+ * Attention of drafted tokens over the cache.  Sequence b has context_lens[b]
+ * cached tokens and n = starts[b + 1] - starts[b] drafted ones, whose keys and
+ * values lie behind them at cache tokens context_lens[b] + 0 .. n - 1 (written
+ * by rarn_qk_norm_rope_kv_write before this call) and whose queries are rows
+ * starts[b] .. starts[b + 1] - 1 of q.  Each drafted token sees the whole
+ * context, and drafted token d of its sequence where bit d % 32 of word d / 32
+ * of its mask row is set (mask: [tokens, mask_words] dense; bits past the row
+ * are not set).  Without a mask token i sees drafted tokens 0 .. i: a chain, and
+ * with n = 1 the ordinary decode step.  For query head h with key head
+ * h / (q_heads / kv_heads):
+ *   out = sum_j p_j V_j,  p = softmax_j(scale * q . K_j)   over what it sees;
+ * a token that sees nothing gets zeros.  Values of hidden tokens do not enter,
+ * NaN and infinities among them.  Rows of q outside starts[0] .. starts[B] - 1
+ * keep their `out` rows as they were; tokens past the page table's width or on
+ * a missing page are hidden.  starts must not fall (B + 1 values from 0 to
+ * `tokens`): a sequence whose pair does is taken as empty, and nothing is
+ * computed (bit 4) where they name more rows than there are.
+ *
+ * q, out: one 16-bit type; softmax statistics and sums in binary32, the
+ * softmax weights rounded to binary16 (11 bits) for the second product.
+ * head_dim 64, 96, 128, 192 or 256; q 16-byte aligned with strides multiples
+ * of 8 elements (else RARN_ERR_UNSUPPORTED).  `workspace`:
+ * rarn_tree_attention_workspace_bytes bytes of device memory, 16-byte aligned,
+ * scratch for this call alone: calls that may overlap on the GPU need one
+ * each.  The lengths are read on the device, so one captured call serves every
+ * later length within its page table's width.  Results are the same bits on
+ * every call with the same inputs.
+ */
+rarn_status rarn_tree_attention(rarn_heads out, rarn_heads q, const rarn_kv_cache *cache,
+                                const int32_t *page_table, int64_t table_stride,
+                                int64_t table_width, const int32_t *context_lens,
+                                const int32_t *starts, const int32_t *mask, int64_t mask_words,
+                                int64_t B, int64_t tokens, float scale, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of a call with these sizes; -1 if they are not supported. */
+int64_t rarn_tree_attention_workspace_bytes(int64_t tokens, int64_t B, int64_t q_heads,
+                                            int64_t kv_heads, int64_t D);
+
 /* Rows that one launch sequence of rarn_gemm_add_rms_norm_noalloc covers for
  * a row length H: floor(floor((2^20 - 16) / (H / 128 + 1)) / 128) * 128
  * (16128 at H = 8192, 8064 at H = 16384); -1 if H is not supported. */
@@ -660,7 +837,9 @@ rarn_status rarn_plan_fp8(rarn_op op, int64_t T, int64_t H, int32_t R, rarn_dtyp
  * return without hanging; their outputs are then not valid.  Bit 0: a
  * stream-kernel consumer wait timed out; bit 1: a stream-kernel producer
  * wait; bit 2: a wait in a GEMM-form kernel; bit 3: a wait of the
- * tensor-parallel form's barrier between ranks.  Synchronises the device.  If
+ * tensor-parallel form's barrier between ranks.  Bit 4 is no timeout: an index
+ * in device memory lay outside its table (see the attention side), and what it
+ * named was left out.  Synchronises the device.  If
  * `clear` is nonzero the word is reset to 0 after reading.
  */
 rarn_status rarn_watchdog(uint32_t *flags, int clear);

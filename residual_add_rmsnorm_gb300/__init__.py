@@ -12,6 +12,16 @@ library is missing or fails to load, every call raises.
     y = fused_add_rms_norm(x, residual, gamma, eps)     # residual updated in place
     y = reduce_add_rms_norm(partials, residual, gamma, eps)   # partials: [R, ..., H]
 
+Attention side (per-head norm and rotation, an 8-bit paged key / value cache,
+attention of drafted tokens over it):
+
+    qk_norm_rope(q, k, q_gamma, k_gamma, eps, cos_sin, positions)
+    cache = KVCache.empty(pages, page_size, heads, head_dim)
+    qk_norm_rope_kv_write(q, k, v, q_gamma, k_gamma, eps, cos_sin, positions, cache, slots)
+    kv_cache_write(k, v, cache, slots)
+    kv_cache_read(cache, page_table, starts, k_out, v_out)
+    tree_attention(q, cache, page_table, context_lens, starts, mask=mask)
+
 8-bit output (e4m3 / e5m2 codes with a per-tensor or per-row scale):
 
     rms_norm_fp8(x, gamma, eps, out, scale, fmt="e4m3", scale_mode="tensor")
@@ -33,7 +43,9 @@ __all__ = ["rms_norm", "fused_add_rms_norm", "reduce_add_rms_norm", "rms_norm_ho
            "TUNING", "set_tuning", "get_tuning", "reset_tuning", "tuning", "gemm_noalloc_rows",
            "launch_floor", "tp_rows", "tp_reduce_add_rms_norm", "tp_reduce_add_rms_norm_world",
            "ipc_export", "ipc_import", "ipc_close", "TP_MAX_RANKS", "TP_SIGNAL_BYTES",
-           "IPC_HANDLE_BYTES"]
+           "IPC_HANDLE_BYTES", "qk_norm_rope", "KVCache", "kv_cache_write",
+           "qk_norm_rope_kv_write", "kv_cache_read", "tree_attention",
+           "tree_attention_workspace_bytes", "ROTATION_STYLES"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "librarn.so")
@@ -43,6 +55,7 @@ OP_CODES = {"rms_norm": 0, "fused_add_rms_norm": 1, "reduce_add_rms_norm": 2}
 PATHS = {"auto": 0, "rows": 1, "stream": 2, "cluster": 3}
 FP8_FORMATS = {"e4m3": 0, "e5m2": 1}
 SCALE_MODES = {"tensor": 0, "row": 1}
+ROTATION_STYLES = {"half": 0, "interleaved": 1}
 # rarn_tuning knobs (planner overrides; -1 is the planner's own choice)
 TUNING = {"rows_per_thread": 0, "rows_grid": 1, "rows_pipeline": 2, "l2_rows": 3,
           "stream_packs": 4, "stream_groups": 5, "gemm_cols": 6, "gemm_slab": 7,
@@ -90,6 +103,33 @@ class Fp8Rows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
                 ("format", ctypes.c_int), ("scale_mode", ctypes.c_int),
                 ("scale", ctypes.c_void_p)]
+
+
+class Heads(ctypes.Structure):
+    """``rarn_heads``: data pointer, token and head strides in elements, heads,
+    storage type."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("dtype", ctypes.c_int)]
+
+
+class Rotation(ctypes.Structure):
+    """``rarn_rotation``: table, positions, table rows, rotated elements, style."""
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("table_rows", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
+                ("style", ctypes.c_int)]
+
+
+class KvCacheDesc(ctypes.Structure):
+    """``rarn_kv_cache``."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("scale_page_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64),
+                ("scale_slot_stride", ctypes.c_int64), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("format", ctypes.c_int),
+                ("scale_mode", ctypes.c_int)]
 
 
 _lib = None
@@ -202,6 +242,19 @@ def library() -> ctypes.CDLL:
     lib.rarn_launch_floor.restype = c_int
     lib.rarn_gemm_noalloc_rows.argtypes = [i64]
     lib.rarn_gemm_noalloc_rows.restype = i64
+    rot, kc = ctypes.POINTER(Rotation), ctypes.POINTER(KvCacheDesc)
+    lib.rarn_qk_norm_rope.argtypes = [Heads, Heads, Heads, Heads, vp, vp, rot, i64, i64, f32, vp]
+    lib.rarn_kv_cache_write.argtypes = [kc, Heads, Heads, vp, i64, vp]
+    lib.rarn_qk_norm_rope_kv_write.argtypes = [Heads, kc, Heads, Heads, Heads, vp, vp, rot, vp,
+                                               i64, f32, vp]
+    lib.rarn_kv_cache_read.argtypes = [Heads, Heads, kc, vp, i64, i64, vp, i64, i64, vp]
+    lib.rarn_tree_attention.argtypes = [Heads, Heads, kc, vp, i64, i64, vp, vp, vp, i64, i64, i64,
+                                        f32, vp, ctypes.c_size_t, vp]
+    for f in (lib.rarn_qk_norm_rope, lib.rarn_kv_cache_write, lib.rarn_qk_norm_rope_kv_write,
+              lib.rarn_kv_cache_read, lib.rarn_tree_attention):
+        f.restype = c_int
+    lib.rarn_tree_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    lib.rarn_tree_attention_workspace_bytes.restype = i64
     _lib = lib
     return lib
 
@@ -686,6 +739,275 @@ def plan_gemm(T: int, H: int, K: int, dtype: str = "bf16", num_sms: int = 152) -
     if st not in (0, 2):
         _check(st, "rarn_plan_gemm")
     return buf.value.decode()
+
+
+def _heads(name, t, shape, dtype, device):
+    """A [T, heads, D] CUDA tensor with unit stride inside a head as a
+    rarn_heads."""
+    if t.dim() != 3 or t.shape[0] != shape[0] or t.shape[2] != shape[2] or \
+            (shape[1] is not None and t.shape[1] != shape[1]):
+        raise ValueError(f"{name} must be {['heads' if x is None else x for x in shape]}, got "
+                         f"{list(t.shape)}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.stride(2) != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name} must have unit stride inside a head")
+    return Heads(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1], _dtype_code(t))
+
+
+def _indices(name, t, dtype, n, device):
+    """A contiguous CUDA index tensor of n values."""
+    if t.dtype != dtype or t.device != device or not t.is_cuda:
+        raise TypeError(f"{name} must be a {dtype} CUDA tensor on {device}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {n} values")
+    return t.data_ptr()
+
+
+def _gamma(name, g, D, dtype, device):
+    if g is None:
+        return None
+    _check_tensor(name, g, dtype, device)
+    if g.numel() != D:
+        raise ValueError(f"{name} has {g.numel()} elements, expected {D}")
+    return g.data_ptr()
+
+
+def _rotation(cos_sin, positions, style, T, device):
+    """The rarn_rotation of a call, or None without a table."""
+    import torch
+    if style not in ROTATION_STYLES:
+        raise ValueError(f"style must be one of {sorted(ROTATION_STYLES)}")
+    if cos_sin is None:
+        return None
+    _check_tensor("cos_sin", cos_sin, torch.float32, device)
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [positions, rot_dim]")
+    if positions is None:
+        raise ValueError("cos_sin needs positions")
+    return ctypes.byref(Rotation(cos_sin.data_ptr(),
+                                 _indices("positions", positions, torch.int64, T, device),
+                                 cos_sin.shape[0], cos_sin.shape[1], ROTATION_STYLES[style]))
+
+
+def qk_norm_rope(q, k, q_gamma, k_gamma, eps: float, cos_sin=None, positions=None,
+                 style: str = "half", q_out=None, k_out=None):
+    """RMSNorm of every query and key head over its D elements, times gamma,
+    then the position rotation; returns (q_out, k_out).
+
+    q [T, Hq, D], k [T, Hk, D]: CUDA tensors of one type (float32 / float16 /
+    bfloat16) with unit stride inside a head and any other strides (slices of a
+    packed projection); q_gamma, k_gamma: [D], or None to leave that norm out;
+    cos_sin: [positions, rot_dim] float32, rot_dim / 2 cosines then sines, or
+    None for no rotation; positions: [T] int64; style: "half" rotates elements
+    (i, i + rot_dim / 2), "interleaved" (2i, 2i + 1).  q_out may be q, k_out k.
+    A token whose position is outside the table keeps its output rows and sets
+    watchdog bit 4."""
+    import torch
+    dev, dt = q.device, q.dtype
+    if q.dim() != 3:
+        raise ValueError("q must be [T, heads, D]")
+    T, D = q.shape[0], q.shape[2]
+    hq = _heads("q", q, (T, None, D), dt, dev)
+    hk = _heads("k", k, (T, None, D), dt, dev)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=dt, device=dev)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=dt, device=dev)
+    with torch.cuda.device(dev):
+        _check(library().rarn_qk_norm_rope(
+            _heads("q_out", q_out, q.shape, dt, dev), _heads("k_out", k_out, k.shape, dt, dev),
+            hq, hk, _gamma("q_gamma", q_gamma, D, dt, dev), _gamma("k_gamma", k_gamma, D, dt, dev),
+            _rotation(cos_sin, positions, style, T, dev), T, D, float(eps), _stream(dev)),
+            "rarn_qk_norm_rope")
+    return q_out, k_out
+
+
+class KVCache:
+    """A paged cache of keys and values held as e4m3 / e5m2 codes with binary32
+    scales.  The tensors are the caller's; this object only describes them.
+
+    k, v: [pages, heads, page_size, head_dim] uint8 (or float8 of the format)
+    with unit stride along head_dim and the same strides (views of any layout:
+    a pool that keeps tokens before heads is passed permuted); k_scale, v_scale:
+    float32 [pages, heads, page_size] with equal strides (scale_mode "row": a
+    scale per token and head, written with the codes) or one value each
+    ("tensor": read)."""
+
+    def __init__(self, k, v, k_scale, v_scale, fmt: str = "e4m3", scale_mode: str = "row"):
+        import torch
+        if fmt not in FP8_FORMATS or scale_mode not in SCALE_MODES:
+            raise ValueError(f"fmt must be one of {sorted(FP8_FORMATS)}, scale_mode one of "
+                             f"{sorted(SCALE_MODES)}")
+        codes = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+        if k.dim() != 4:
+            raise ValueError("k must be [pages, heads, page_size, head_dim]")
+        for n, t in (("k", k), ("v", v)):
+            if t.dtype not in (torch.uint8, codes[fmt]):
+                raise TypeError(f"{n} must be uint8 or {codes[fmt]}")
+            if not t.is_cuda or t.device != k.device:
+                raise ValueError(f"{n} must be a CUDA tensor on {k.device}")
+            if t.shape != k.shape or t.stride() != k.stride() or t.stride(3) != 1:
+                raise ValueError("k and v must have one shape and layout, unit stride along "
+                                 "head_dim")
+        for n, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t.dtype != torch.float32 or not t.is_cuda or t.device != k.device:
+                raise TypeError(f"{n} must be a float32 CUDA tensor on {k.device}")
+            if scale_mode == "row":
+                if t.shape != k.shape[:3] or t.stride() != k_scale.stride():
+                    raise ValueError(f"{n} must be {list(k.shape[:3])}, k_scale and v_scale of "
+                                     f"one layout")
+            elif t.numel() != 1:
+                raise ValueError(f"{n} must hold one value")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.fmt, self.scale_mode = fmt, scale_mode
+        self.device = k.device
+        self.num_pages, self.heads, self.page_size, self.head_dim = k.shape
+        ps, hs, ss = k.stride()[:3]
+        sp, sh, s1 = k_scale.stride() if scale_mode == "row" else (0, 0, 0)
+        self._desc = KvCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                                 v_scale.data_ptr(), ps, hs, ss, sp, sh, s1, self.num_pages,
+                                 self.page_size, self.heads, self.head_dim, FP8_FORMATS[fmt],
+                                 SCALE_MODES[scale_mode])
+        self._ref = ctypes.byref(self._desc)
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, heads: int, head_dim: int, fmt: str = "e4m3",
+              scale_mode: str = "row", device="cuda", k_scale: float = 1.0, v_scale: float = 1.0):
+        """A cache of zero codes with tensors of its own (``k_scale``,
+        ``v_scale``: the two scales of mode "tensor")."""
+        import torch
+        shape = (pages, heads, page_size, head_dim)
+        k, v = (torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2))
+        if scale_mode == "row":
+            ks, vs = (torch.ones(shape[:3], dtype=torch.float32, device=device) for _ in range(2))
+        else:
+            ks, vs = (torch.full((1,), float(x), dtype=torch.float32, device=device)
+                      for x in (k_scale, v_scale))
+        return cls(k, v, ks, vs, fmt, scale_mode)
+
+
+def kv_cache_write(k, v, cache: KVCache, slots) -> None:
+    """Keys and values k, v [T, heads, D] (one type, any strides) quantised into
+    the cache: token t into slot slots[t] (int64; page * page_size + slot of the
+    page; negative: left out; the others distinct)."""
+    import torch
+    dev, dt = cache.device, k.dtype
+    if k.dim() != 3:
+        raise ValueError("k must be [T, heads, D]")
+    shape = (k.shape[0], cache.heads, cache.head_dim)
+    hk, hv = _heads("k", k, shape, dt, dev), _heads("v", v, shape, dt, dev)
+    ps = _indices("slots", slots, torch.int64, shape[0], dev)
+    with torch.cuda.device(dev):
+        _check(library().rarn_kv_cache_write(cache._ref, hk, hv, ps, shape[0], _stream(dev)),
+               "rarn_kv_cache_write")
+
+
+def qk_norm_rope_kv_write(q, k, v, q_gamma, k_gamma, eps: float, cos_sin, positions,
+                          cache: KVCache, slots, style: str = "half", q_out=None):
+    """qk_norm_rope and kv_cache_write in one pass: returns the normalised,
+    rotated queries; the keys (quantised from their binary32 values) and values
+    go to the cache."""
+    import torch
+    dev, dt = cache.device, q.dtype
+    if q.dim() != 3:
+        raise ValueError("q must be [T, heads, D]")
+    T, D = q.shape[0], cache.head_dim
+    hq = _heads("q", q, (T, None, D), dt, dev)
+    hk = _heads("k", k, (T, cache.heads, D), dt, dev)
+    hv = _heads("v", v, (T, cache.heads, D), dt, dev)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=dt, device=dev)
+    with torch.cuda.device(dev):
+        _check(library().rarn_qk_norm_rope_kv_write(
+            _heads("q_out", q_out, q.shape, dt, dev), cache._ref, hq, hk, hv,
+            _gamma("q_gamma", q_gamma, D, dt, dev), _gamma("k_gamma", k_gamma, D, dt, dev),
+            _rotation(cos_sin, positions, style, T, dev),
+            _indices("slots", slots, torch.int64, T, dev), T, float(eps), _stream(dev)),
+            "rarn_qk_norm_rope_kv_write")
+    return q_out
+
+
+def _page_table(t, device):
+    import torch
+    if t.dtype != torch.int32 or not t.is_cuda or t.device != device:
+        raise TypeError(f"page_table must be an int32 CUDA tensor on {device}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("page_table must be [sequences, pages] with unit stride along a row")
+    return t.data_ptr(), t.stride(0), t.shape[1]
+
+
+def kv_cache_read(cache: KVCache, page_table, starts, k_out, v_out):
+    """The cached tokens of every sequence, dequantised: sequence b's go to rows
+    starts[b] .. starts[b + 1] - 1 of k_out and v_out ([rows, heads, D], one
+    type); page_table: [B, width] int32, starts: [B + 1] int32.  Rows past the
+    last sequence stay as they were.  Returns (k_out, v_out)."""
+    import torch
+    dev = cache.device
+    if k_out.dim() != 3:
+        raise ValueError("k_out must be [rows, heads, D]")
+    shape = (k_out.shape[0], cache.heads, cache.head_dim)
+    hk, hv = (_heads(n, t, shape, k_out.dtype, dev) for n, t in (("k_out", k_out),
+                                                                 ("v_out", v_out)))
+    table = _page_table(page_table, dev)
+    B = page_table.shape[0]
+    ps = _indices("starts", starts, torch.int32, B + 1, dev)
+    with torch.cuda.device(dev):
+        _check(library().rarn_kv_cache_read(hk, hv, cache._ref, *table, ps, B, shape[0],
+                                            _stream(dev)), "rarn_kv_cache_read")
+    return k_out, v_out
+
+
+def tree_attention_workspace_bytes(tokens: int, sequences: int, q_heads: int, kv_heads: int,
+                                   head_dim: int) -> int:
+    """Workspace bytes tree_attention needs for these sizes (-1: unsupported)."""
+    return int(library().rarn_tree_attention_workspace_bytes(tokens, sequences, q_heads, kv_heads,
+                                                             head_dim))
+
+
+def tree_attention(q, cache: KVCache, page_table, context_lens, starts, mask=None,
+                   scale: float | None = None, out=None, workspace=None):
+    """Attention of drafted tokens over the cache: sequence b's drafted tokens
+    are rows starts[b] .. starts[b + 1] - 1 of q [tokens, q_heads, D], their
+    keys and values lie in the cache behind its context_lens[b] tokens.  Each
+    sees the context and the drafted tokens whose bits are set in its row of
+    ``mask`` ([tokens, words] int32, bit d % 32 of word d / 32 for drafted token
+    d); without a mask itself and those before it (one token: the decode step).
+    ``scale``: of the scores, 1 / sqrt(D) by default.  ``workspace``: a CUDA
+    tensor of at least tree_attention_workspace_bytes bytes (allocated if None);
+    calls that may overlap need one each.  Returns out (like q)."""
+    import torch
+    dev, dt = cache.device, q.dtype
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, D]")
+    N, D = q.shape[0], cache.head_dim
+    hq = _heads("q", q, (N, None, D), dt, dev)
+    if out is None:
+        out = torch.empty(q.shape, dtype=dt, device=dev)
+    ho = _heads("out", out, q.shape, dt, dev)
+    table = _page_table(page_table, dev)
+    B = page_table.shape[0]
+    ctx = _indices("context_lens", context_lens, torch.int32, B, dev)
+    st = _indices("starts", starts, torch.int32, B + 1, dev)
+    pm, words = None, 0
+    if mask is not None:
+        if mask.dim() != 2 or mask.shape[0] != N:
+            raise ValueError(f"mask must be [{N}, words]")
+        words = mask.shape[1]
+        pm = _indices("mask", mask, torch.int32, N * words, dev)
+    if workspace is None:
+        n = max(tree_attention_workspace_bytes(N, B, q.shape[1], cache.heads, D), 16)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
+    with torch.cuda.device(dev):
+        _check(library().rarn_tree_attention(
+            ho, hq, cache._ref, *table, ctx, st, pm, words, B, N,
+            float(D ** -0.5 if scale is None else scale), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream(dev)), "rarn_tree_attention")
+    return out
 
 
 def launch_floor(grid: int, block: int, rows=None, row_bytes: int = 0) -> None:

@@ -18,6 +18,7 @@
 
 #include "../../include/rarn.h"
 #include "gemm_plan.h"
+#include "host.h"
 #include "plan.h"
 #include "q8in.cuh"
 #include "tp.cuh"
@@ -681,6 +682,24 @@ rarn_status run(int op, void *y, const void *src, int32_t R, void *residual, con
 }
 
 }  // namespace
+
+namespace rarn {
+namespace host {
+
+rarn_status current_device(Device *out) {
+    DeviceInfo *d = nullptr;
+    const rarn_status st = device_info(&d);
+    if (st != RARN_OK) return st;
+    *out = Device{d->num_sms, d->max_smem_optin, d->watchdog};
+    return RARN_OK;
+}
+
+rarn_status cuda_failed(cudaError_t e) { return cuda_fail(e); }
+
+bool pdl_enabled() { return g_pdl.load() != 0; }
+
+}  // namespace host
+}  // namespace rarn
 
 extern "C" {
 

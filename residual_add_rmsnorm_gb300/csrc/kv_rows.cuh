@@ -1,0 +1,520 @@
+// kv_rows.cuh -- per-head RMSNorm of queries and keys with the position
+// rotation, and the 8-bit cache's write and read.
+//
+//   n = x * rsqrt(mean(x^2) + eps) * gamma       over one head's D elements
+//   (a, b) -> (a cos - b sin, b cos + a sin)     for the first `rot` elements,
+//                                                pairs (i, i + rot / 2) or (2i, 2i + 1)
+//   code = RN(n / s)                             s given, or max|n| / maxf per row
+//
+// All of it is one pass: a head is 128 to 512 bytes, so the row's elements
+// stay in registers between the sum of squares, the rotation and the row's
+// largest magnitude, and memory is touched once per byte.
+//
+// Vector kernel.  A lane owns two 16-byte packs that hold both halves of its
+// rotation pairs (pack p and pack rot / 2 + p for "half" pairs, two
+// neighbouring packs otherwise), so the rotation needs no exchange; a group
+// of D / (2 packs) lanes, rounded up to a power of two, owns a head and
+// reduces by shuffles inside itself.  The group takes kHeads heads of one
+// token with the same cos / sin registers (the table is binary32: for one
+// head its 8 D bytes would be four times the head's own).
+#pragma once
+
+#include "kv.cuh"
+
+namespace rarn {
+namespace kv {
+
+struct RowParams {
+    Heads q, k, v;          // inputs; heads == 0: none
+    Heads q_out, k_out;     // k_out.data == nullptr: keys go to the cache only
+    const void *q_gamma, *k_gamma;  // [D] or nullptr: no norm
+    const float *table;     // [table_rows, rot]: cos then sin; nullptr: no rotation
+    const int64_t *positions;
+    int64_t table_rows;
+    int rot;
+    int interleaved;
+    const int64_t *slots;   // cache slot of each token, < 0: not written
+    Cache cache;            // cache.k == nullptr: none
+    int64_t T;
+    int D;
+    float eps;
+    unsigned int *watchdog;
+};
+
+// What becomes of head `h` of the concatenation q, k, v.
+struct HeadRole {
+    const char *src;
+    char *dst;              // 16- or 32-bit output, or nullptr
+    const void *gamma;
+    int64_t src_off, dst_off;  // elements
+    uint8_t *codes;         // the cache's codes of this head at slot 0 of page 0, or nullptr
+    float *scales;
+    bool rotate;
+    int head;               // in the cache
+};
+
+__device__ __forceinline__ HeadRole role_of(const RowParams &p, int64_t t, int h) {
+    HeadRole r{};
+    const bool cached = p.cache.k != nullptr;
+    if (h < p.q.heads) {
+        r.src = static_cast<const char *>(p.q.data);
+        r.src_off = t * p.q.ts + h * p.q.hs;
+        r.dst = static_cast<char *>(p.q_out.data);
+        r.dst_off = t * p.q_out.ts + h * p.q_out.hs;
+        r.gamma = p.q_gamma;
+        r.rotate = p.table != nullptr;
+        return r;
+    }
+    h -= p.q.heads;
+    if (h < p.k.heads) {
+        r.src = static_cast<const char *>(p.k.data);
+        r.src_off = t * p.k.ts + h * p.k.hs;
+        r.dst = static_cast<char *>(p.k_out.data);
+        r.dst_off = t * p.k_out.ts + h * p.k_out.hs;
+        r.gamma = p.k_gamma;
+        r.rotate = p.table != nullptr;
+        r.codes = cached ? p.cache.k : nullptr;
+        r.scales = p.cache.k_scale;
+        r.head = h;
+        return r;
+    }
+    h -= p.k.heads;
+    r.src = static_cast<const char *>(p.v.data);
+    r.src_off = t * p.v.ts + h * p.v.hs;
+    r.codes = p.cache.v;
+    r.scales = p.cache.v_scale;
+    r.head = h;
+    return r;
+}
+
+// A token's place in the cache: page and slot inside it; page < 0: none.
+struct Place {
+    int64_t page;
+    int at;
+};
+
+__device__ __forceinline__ Place place_of(const RowParams &p, int64_t t, bool reporter) {
+    Place pl{-1, 0};
+    if (!p.cache.k) return pl;
+    const int64_t slot = p.slots[t];
+    if (slot < 0) return pl;
+    const int64_t page = slot / p.cache.page_size;
+    if (page >= p.cache.pages) {
+        if (reporter) atomicOr(p.watchdog, kWatchIndex);
+        return pl;
+    }
+    pl.page = page;
+    pl.at = static_cast<int>(slot - page * p.cache.page_size);
+    return pl;
+}
+
+// The row of the rotation table for token t; nullptr with *ok = false when its
+// position lies outside the table (the token's rows are then left as they are).
+__device__ __forceinline__ const float *table_row(const RowParams &p, int64_t t, bool reporter,
+                                                  bool *ok) {
+    *ok = true;
+    if (!p.table) return nullptr;
+    const int64_t pos = p.positions[t];
+    if (pos < 0 || pos >= p.table_rows) {
+        if (reporter) atomicOr(p.watchdog, kWatchIndex);
+        *ok = false;
+        return nullptr;
+    }
+    return p.table + pos * p.rot;
+}
+
+template <int LG>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int m = LG / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+}
+
+template <int LG>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int m = LG / 2; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
+    return v;
+}
+
+// A row's multipliers and scale from its largest magnitude: the 8-bit output
+// forms' rule (quant_row).
+__device__ __forceinline__ QMul row_mul(float amax, int fmt, float *scale) {
+    const float maxf = q_maxf(fmt);
+    *scale = amax > 0.f ? amax / maxf : 1.f;
+    if (!(amax > 0.f)) return QMul{1.f, 1.f};
+    const float k = amax < 1.17549435e-38f ? 16777216.f : 1.f;
+    return QMul{1.f / (amax * k), maxf * k};
+}
+
+// A warp: kHeads heads per group of LG lanes, one token.
+template <typename T, int LG, int kHeads>
+__global__ void __launch_bounds__(128) k_head_rows(const RowParams p, int chunks) {
+    constexpr int E = DT<T>::EPV;  // elements per pack
+    constexpr int GPW = 32 / LG;   // groups per warp
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int64_t t = item / chunks;
+    if (t >= p.T) return;  // whole warps
+    const int lane = threadIdx.x & 31, group = lane / LG, l = lane % LG;
+    const int h0 = static_cast<int>(item - t * chunks) * (GPW * kHeads) + group;
+    const int heads = p.q.heads + p.k.heads + p.v.heads;
+
+    // this lane's two packs
+    const int turned = p.table ? p.rot / (2 * E) : 0;  // lanes whose packs rotate
+    const bool owns = l < p.D / (2 * E);
+    const bool turns = l < turned;
+    int ea, eb;
+    if (turns && !p.interleaved) {
+        ea = l * E;
+        eb = p.rot / 2 + l * E;
+    } else {
+        ea = 2 * E * l;  // past the rotated lanes this is rot + 2 E (l - turned) too
+        eb = ea + E;
+    }
+
+    uint4 xa[kHeads], xb[kHeads];
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        xa[i] = xb[i] = make_uint4(0, 0, 0, 0);
+        const int h = h0 + i * GPW;
+        if (owns && h < heads) {
+            const HeadRole r = role_of(p, t, h);
+            const T *s = reinterpret_cast<const T *>(r.src) + r.src_off;
+            xa[i] = ld_stream(s + ea);
+            xb[i] = ld_stream(s + eb);
+        }
+    }
+    bool ok;
+    const float *tr = table_row(p, t, lane == 0, &ok);
+    if (!ok) return;  // the whole warp: one token
+    const Place pl = place_of(p, t, lane == 0);
+    float c[E], s[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        c[j] = 1.f;
+        s[j] = 0.f;
+    }
+    if (tr && turns) {
+#pragma unroll
+        for (int j = 0; j < E; j += 4) {
+            const float4 cv = __ldg(reinterpret_cast<const float4 *>(tr + l * E + j));
+            const float4 sv = __ldg(reinterpret_cast<const float4 *>(tr + p.rot / 2 + l * E + j));
+            c[j] = cv.x; c[j + 1] = cv.y; c[j + 2] = cv.z; c[j + 3] = cv.w;
+            s[j] = sv.x; s[j + 1] = sv.y; s[j + 2] = sv.z; s[j + 3] = sv.w;
+        }
+    }
+    const float inv_d = 1.f / static_cast<float>(p.D);
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        const int h = h0 + i * GPW;
+        const bool live = owns && h < heads;
+        const HeadRole r = role_of(p, t, h < heads ? h : 0);
+        float f[2 * E];
+        {
+            float a[E], b[E];
+            DT<T>::unpack(xa[i], a);
+            DT<T>::unpack(xb[i], b);
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                f[j] = a[j];
+                f[E + j] = b[j];
+            }
+        }
+        if (p.q_gamma || p.k_gamma) {  // uniform; a row without gamma keeps factor 1
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < 2 * E; ++j) ss = fmaf(f[j], f[j], ss);
+            ss = group_sum<LG>(ss);
+            if (live && r.gamma) {
+                const float inv = rsqrtf(fmaf(ss, inv_d, p.eps));
+                float a[E], b[E];
+                DT<T>::unpack(ld_keep(static_cast<const T *>(r.gamma) + ea), a);
+                DT<T>::unpack(ld_keep(static_cast<const T *>(r.gamma) + eb), b);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    f[j] = f[j] * inv * a[j];
+                    f[E + j] = f[E + j] * inv * b[j];
+                }
+            }
+        }
+        if (turns && r.rotate) {
+            if (p.interleaved) {
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const float x = f[2 * j], y = f[2 * j + 1];
+                    f[2 * j] = x * c[j] - y * s[j];
+                    f[2 * j + 1] = y * c[j] + x * s[j];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const float x = f[j], y = f[E + j];
+                    f[j] = x * c[j] - y * s[j];
+                    f[E + j] = y * c[j] + x * s[j];
+                }
+            }
+        }
+        float fa[E], fb[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            fa[j] = f[j];
+            fb[j] = f[E + j];
+        }
+        if (live && r.dst) {
+            T *d = reinterpret_cast<T *>(r.dst) + r.dst_off;
+            st_global(d + ea, DT<T>::pack(fa));
+            st_global(d + eb, DT<T>::pack(fb));
+        }
+        if (p.cache.k) {  // uniform
+            float amax = 0.f;
+#pragma unroll
+            for (int j = 0; j < 2 * E; ++j) amax = fmaxf(amax, fabsf(f[j]));
+            amax = group_max<LG>(amax);
+            if (live && r.codes && pl.page >= 0) {
+                QMul m;
+                if (p.cache.mode == Q_ROW) {
+                    float scale;
+                    m = row_mul(amax, p.cache.fmt, &scale);
+                    if (l == 0)
+                        r.scales[pl.page * p.cache.s_page + r.head * p.cache.s_head +
+                                 pl.at * p.cache.s_slot] = scale;
+                } else {
+                    m = QMul{1.f / __ldg(r.scales), 1.f};
+                }
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    fa[j] = (fa[j] * m.m1) * m.m2;
+                    fb[j] = (fb[j] * m.m1) * m.m2;
+                }
+                uint8_t *d = r.codes + pl.page * p.cache.page_stride +
+                             r.head * p.cache.head_stride + pl.at * p.cache.slot_stride;
+                st_codes<E>(d + ea, fa, p.cache.fmt);
+                st_codes<E>(d + eb, fb, p.cache.fmt);
+            }
+        }
+    }
+}
+
+// Any head size, rotation width, stride and alignment: a warp per head, a
+// lane per rotation pair (then per unrotated element), the row re-read from
+// L1 for each of its passes.
+template <typename T>
+__global__ void __launch_bounds__(128) k_head_rows_any(const RowParams p, int heads) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int64_t t = item / heads;
+    if (t >= p.T) return;
+    const int lane = threadIdx.x & 31;
+    const HeadRole r = role_of(p, t, static_cast<int>(item - t * heads));
+    bool ok;
+    const float *tr = table_row(p, t, lane == 0, &ok);
+    if (!ok) return;
+    const Place pl = place_of(p, t, lane == 0);
+    const T *src = reinterpret_cast<const T *>(r.src) + r.src_off;
+    float inv = 1.f;
+    if (r.gamma) {
+        float ss = 0.f;
+        for (int e = lane; e < p.D; e += 32) {
+            const float x = DT<T>::to_f(src[e]);
+            ss = fmaf(x, x, ss);
+        }
+        inv = rsqrtf(fmaf(warp_sum(ss), 1.f / static_cast<float>(p.D), p.eps));
+    }
+    const bool turn = r.rotate && tr;
+    const int half = turn ? p.rot / 2 : 0;
+    const int work = half + (p.D - 2 * half);  // pairs, then single elements
+    auto normed = [&](int e) {
+        const float x = DT<T>::to_f(src[e]);
+        return r.gamma ? x * inv * ld_elem<T>(r.gamma, e) : x;
+    };
+    // element(s) of work item i: one rotated pair or one element
+    auto value = [&](int i, int &e0, int &e1, float &a, float &b) {
+        if (i < half) {
+            e0 = p.interleaved ? 2 * i : i;
+            e1 = p.interleaved ? 2 * i + 1 : half + i;
+            const float x = normed(e0), y = normed(e1);
+            const float c = __ldg(tr + i), s = __ldg(tr + half + i);
+            a = x * c - y * s;
+            b = y * c + x * s;
+        } else {
+            e0 = half + i;
+            e1 = -1;
+            a = normed(e0);
+            b = 0.f;
+        }
+    };
+    QMul m{1.f, 1.f};
+    const bool store_codes = r.codes && pl.page >= 0;
+    if (store_codes) {
+        if (p.cache.mode == Q_ROW) {
+            float amax = 0.f;
+            for (int i = lane; i < work; i += 32) {
+                int e0, e1;
+                float a, b;
+                value(i, e0, e1, a, b);
+                amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(b)));
+            }
+            amax = warp_max(amax);
+            float scale;
+            m = row_mul(amax, p.cache.fmt, &scale);
+            if (lane == 0)
+                r.scales[pl.page * p.cache.s_page + r.head * p.cache.s_head +
+                         pl.at * p.cache.s_slot] = scale;
+        } else {
+            m.m1 = 1.f / __ldg(r.scales);
+        }
+    }
+    uint8_t *codes = store_codes ? r.codes + pl.page * p.cache.page_stride +
+                                       r.head * p.cache.head_stride + pl.at * p.cache.slot_stride
+                                 : nullptr;
+    for (int i = lane; i < work; i += 32) {
+        int e0, e1;
+        float a, b;
+        value(i, e0, e1, a, b);
+        if (r.dst) {
+            T *d = reinterpret_cast<T *>(r.dst) + r.dst_off;
+            d[e0] = DT<T>::from_f(a);
+            if (e1 >= 0) d[e1] = DT<T>::from_f(b);
+        }
+        if (codes) {
+            codes[e0] = fp8x1((a * m.m1) * m.m2, p.cache.fmt);
+            if (e1 >= 0) codes[e1] = fp8x1((b * m.m1) * m.m2, p.cache.fmt);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The cache read back: x = RN(code * s), sequences packed one after another.
+// ---------------------------------------------------------------------------
+struct ReadParams {
+    Heads k_out, v_out;      // [rows, heads, D]
+    Cache cache;
+    const int32_t *table;    // [B, width] pages of each sequence
+    int64_t table_stride;
+    int table_width;
+    const int32_t *starts;   // [B + 1]: first output row of each sequence
+    int B;
+    int64_t rows;
+    int D;
+    unsigned int *watchdog;
+};
+
+constexpr int kReadRows = 16;  // output rows per CTA
+
+// Each CTA finds the cache place of its kReadRows rows once (a binary search
+// over the sequences' starts), then streams their codes: 16 codes per load.
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(256) k_cache_read(const ReadParams p) {
+    __shared__ int64_t s_code[kReadRows], s_scale[kReadRows];  // offsets; code < 0: nothing
+    __shared__ int s_state[kReadRows];                         // 0: leave, 1: read, 2: zeros
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t r0 = (int64_t)blockIdx.x * kReadRows;
+    if (threadIdx.x < kReadRows) {
+        const int64_t r = r0 + threadIdx.x;
+        int state = 0;
+        int64_t code = 0, scale = 0;
+        // the last sequence that starts at or before row r
+        int lo = 0, hi = p.B;  // starts[lo] <= r < starts[hi]
+        if (r < p.rows && r >= p.starts[0] && r < p.starts[p.B]) {
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (p.starts[mid] <= r) lo = mid;
+                else hi = mid;
+            }
+            const int64_t j = r - p.starts[lo];
+            const int64_t pg = j / p.cache.page_size;
+            const int at = static_cast<int>(j - pg * p.cache.page_size);
+            state = 2;
+            if (pg < p.table_width) {
+                const int64_t page = p.table[lo * p.table_stride + pg];
+                if (page >= 0 && page < p.cache.pages) {
+                    state = 1;
+                    code = page * p.cache.page_stride + at * p.cache.slot_stride;
+                    scale = page * p.cache.s_page + at * p.cache.s_slot;
+                }
+            }
+            if (state == 2) atomicOr(p.watchdog, kWatchIndex);
+        }
+        s_code[threadIdx.x] = code;
+        s_scale[threadIdx.x] = scale;
+        s_state[threadIdx.x] = state;
+    }
+    __syncthreads();
+    const int per_head = p.D / 16;
+    const int per_row = 2 * p.cache.heads * per_head;
+    const int total = kReadRows * per_row;
+    constexpr int U = 4;
+    for (int base = threadIdx.x; base < total; base += 256 * U) {
+        uint4 w[U];
+        float sc[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = base + u * 256;
+            w[u] = make_uint4(0, 0, 0, 0);
+            sc[u] = 0.f;
+            if (i < total) {
+                const int row = i / per_row, x = i - row * per_row;
+                const int hh = x / per_head, piece = x - hh * per_head;
+                const bool val = hh >= p.cache.heads;
+                const int h = val ? hh - p.cache.heads : hh;
+                if (s_state[row] == 1) {
+                    const uint8_t *src = (val ? p.cache.v : p.cache.k) + s_code[row] +
+                                         h * p.cache.head_stride + piece * 16;
+                    w[u] = ld_stream(src);
+                    const float *ss = val ? p.cache.v_scale : p.cache.k_scale;
+                    sc[u] = p.cache.mode == Q_ROW ? ss[s_scale[row] + h * p.cache.s_head] : *ss;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = base + u * 256;
+            if (i >= total) break;
+            const int row = i / per_row, x = i - row * per_row;
+            if (s_state[row] == 0) continue;
+            const int hh = x / per_head, piece = x - hh * per_head;
+            const bool val = hh >= p.cache.heads;
+            const int h = val ? hh - p.cache.heads : hh;
+            const Heads &o = val ? p.v_out : p.k_out;
+            T *d = static_cast<T *>(o.data) + (r0 + row) * o.ts + h * o.hs + piece * 16;
+            float f[16];
+            const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 a = codes2_to_f2(ws[j] & 0xffffu, p.cache.fmt);
+                const float2 b = codes2_to_f2(ws[j] >> 16, p.cache.fmt);
+                f[4 * j] = a.x * sc[u];
+                f[4 * j + 1] = a.y * sc[u];
+                f[4 * j + 2] = b.x * sc[u];
+                f[4 * j + 3] = b.y * sc[u];
+            }
+            if constexpr (kVec) {
+                constexpr int E = DT<T>::EPV;
+#pragma unroll
+                for (int j = 0; j < 16 / E; ++j) {
+                    float g[E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) g[e] = f[j * E + e];
+                    st_global(d + j * E, DT<T>::pack(g));
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) d[e] = DT<T>::from_f(f[e]);
+            }
+        }
+    }
+}
+
+// Host launchers (instantiated per storage type).
+template <typename T>
+cudaError_t launch_head_rows(const RowParams &p, bool vec, int num_sms, bool pdl,
+                             cudaStream_t st);
+template <typename T>
+cudaError_t launch_cache_read(const ReadParams &p, bool vec, bool pdl, cudaStream_t st);
+
+}  // namespace kv
+}  // namespace rarn
