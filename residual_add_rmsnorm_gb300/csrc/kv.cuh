@@ -32,12 +32,29 @@ struct Cache {
     int mode;  // QMode
 };
 
-// Two codes to binary16, exactly (both formats are subsets of it).
+// Four codes to two pairs of binary16, exactly (both formats are subsets of
+// it).  One instruction per pair; the header's intrinsic, which returns the
+// halves apart, measured three times that.
+template <bool kE5M2>
+__device__ __forceinline__ void codes4_to_h2(uint32_t four, uint32_t &lo, uint32_t &hi) {
+    if constexpr (kE5M2) {
+        asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\n"
+            "cvt.rn.f16x2.e5m2x2 %0, a;\ncvt.rn.f16x2.e5m2x2 %1, b;\n}\n"
+            : "=r"(lo), "=r"(hi)
+            : "r"(four));
+    } else {
+        asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\n"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+            : "=r"(lo), "=r"(hi)
+            : "r"(four));
+    }
+}
+
 template <bool kE5M2>
 __device__ __forceinline__ uint32_t codes2_to_h2(uint32_t two) {
-    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two),
-                                                     kE5M2 ? __NV_E5M2 : __NV_E4M3);
-    return static_cast<uint32_t>(r.x) | (static_cast<uint32_t>(r.y) << 16);
+    uint32_t lo, hi;
+    codes4_to_h2<kE5M2>(two, lo, hi);
+    return lo;
 }
 
 __device__ __forceinline__ float2 codes2_to_f2(uint32_t two, int fmt) {

@@ -542,10 +542,21 @@ rarn_status rarn_tree_attention(rarn_heads out, rarn_heads q, const rarn_kv_cach
     p.D = (int)D;
     p.G = q.heads / cache->heads;
     p.bf16 = q.dtype == RARN_BF16;
+    p.out_aligned = on(out.data, 8) && out.token_stride % 4 == 0 && out.head_stride % 4 == 0;
     p.scale_log2 = scale * 1.44269504088896340736f;
+    const int ps = cache->page_size;
+    p.whole_steps =
+        ps % tree::kStep == 0 &&
+        (cache->scale_mode == RARN_SCALE_TENSOR ||
+         (on(cache->k_scale, 16) && on(cache->v_scale, 16) && cache->scale_slot_stride == 1 &&
+          (cache->heads == 1 || cache->scale_head_stride % 4 == 0) &&
+          (cache->num_pages == 1 || cache->scale_page_stride % 4 == 0)));
+    p.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (ps == 1 << i) p.page_shift = i;
     char *ws = static_cast<char *>(workspace);
     p.count = reinterpret_cast<int *>(ws);
-    p.joins = reinterpret_cast<int4 *>(ws + pl.joins_off);
+    p.joins = reinterpret_cast<tree::Join *>(ws + pl.joins_off);
     p.ml = reinterpret_cast<float2 *>(ws + pl.ml_off);
     p.part = reinterpret_cast<float *>(ws + pl.part_off);
     p.max_segs = (int)pl.segments;

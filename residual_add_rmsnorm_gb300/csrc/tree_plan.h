@@ -10,6 +10,7 @@ namespace tree {
 struct Plan {
     int rows;          // rows (drafted token x query head of the group) of a segment
     int64_t segments;  // at most
+    int64_t expected;  // segments where all sequences draft alike
     int64_t joins_off, ml_off, part_off, bytes;
 };
 
@@ -24,9 +25,10 @@ inline Plan plan(int64_t tokens, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
     p.rows = per > 8 && D <= 128 ? 16 : 8;
     // every sequence ends in at most one block that is not full
     p.segments = Hk * (tokens * G / p.rows + B);
+    p.expected = Hk * B * ((per + p.rows - 1) / p.rows);
     auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
     p.joins_off = 256;
-    p.ml_off = p.joins_off + up(16 * p.segments);
+    p.ml_off = p.joins_off + up(32 * p.segments);
     p.part_off = p.ml_off + up(2 * kCtas * p.rows * 8);
     p.bytes = p.part_off + 2 * kCtas * p.rows * D * 4;
     return p;
