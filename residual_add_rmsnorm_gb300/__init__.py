@@ -741,25 +741,54 @@ def plan_gemm(T: int, H: int, K: int, dtype: str = "bf16", num_sms: int = 152) -
     return buf.value.decode()
 
 
-def _heads(name, t, shape, dtype, device):
+# What the attention side's calls keep at hand: a decode step makes several of
+# them per layer, and Python is most of a short call's time.
+_codes = {}       # torch dtype -> rarn_dtype
+_get_device = _raw_stream = None
+
+
+def _on(device, what, fn, *args):
+    """fn(*args, stream) on ``device`` and its current stream; raises on a
+    status other than OK."""
+    global _get_device, _raw_stream
+    import torch
+    if _get_device is None:
+        _get_device = torch.cuda.current_device
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda i: torch.cuda.current_stream(i).cuda_stream)
+    i = device.index
+    if _get_device() == i:
+        status = fn(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            status = fn(*args, _raw_stream(i))
+    if status:
+        _check(status, what)
+
+
+def _heads(name, t, T, heads, D, dtype, device):
     """A [T, heads, D] CUDA tensor with unit stride inside a head as a
-    rarn_heads."""
-    if t.dim() != 3 or t.shape[0] != shape[0] or t.shape[2] != shape[2] or \
-            (shape[1] is not None and t.shape[1] != shape[1]):
-        raise ValueError(f"{name} must be {['heads' if x is None else x for x in shape]}, got "
-                         f"{list(t.shape)}")
+    rarn_heads (heads None: any number)."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != T or shape[2] != D or \
+            (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [{T}, {'heads' if heads is None else heads}, {D}], got "
+                         f"{list(shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.device != device or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.stride(2) != 1 and t.shape[2] > 1:
+    if stride[2] != 1 and D > 1:
         raise ValueError(f"{name} must have unit stride inside a head")
-    return Heads(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1], _dtype_code(t))
+    code = _codes.get(dtype)
+    if code is None:
+        code = _codes[dtype] = _dtype_code(t)
+    return Heads(t.data_ptr(), stride[0], stride[1], shape[1], code)
 
 
 def _indices(name, t, dtype, n, device):
     """A contiguous CUDA index tensor of n values."""
-    if t.dtype != dtype or t.device != device or not t.is_cuda:
+    if t.dtype is not dtype or t.device != device or not t.is_cuda:
         raise TypeError(f"{name} must be a {dtype} CUDA tensor on {device}")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {n} values")
@@ -769,7 +798,8 @@ def _indices(name, t, dtype, n, device):
 def _gamma(name, g, D, dtype, device):
     if g is None:
         return None
-    _check_tensor(name, g, dtype, device)
+    if g.dtype is not dtype or g.device != device or not g.is_contiguous():
+        _check_tensor(name, g, dtype, device)
     if g.numel() != D:
         raise ValueError(f"{name} has {g.numel()} elements, expected {D}")
     return g.data_ptr()
@@ -778,18 +808,21 @@ def _gamma(name, g, D, dtype, device):
 def _rotation(cos_sin, positions, style, T, device):
     """The rarn_rotation of a call, or None without a table."""
     import torch
-    if style not in ROTATION_STYLES:
+    code = ROTATION_STYLES.get(style)
+    if code is None:
         raise ValueError(f"style must be one of {sorted(ROTATION_STYLES)}")
     if cos_sin is None:
         return None
-    _check_tensor("cos_sin", cos_sin, torch.float32, device)
-    if cos_sin.dim() != 2:
+    if cos_sin.dtype is not torch.float32 or cos_sin.device != device or \
+            not cos_sin.is_contiguous():
+        _check_tensor("cos_sin", cos_sin, torch.float32, device)
+    shape = cos_sin.shape
+    if len(shape) != 2:
         raise ValueError("cos_sin must be [positions, rot_dim]")
     if positions is None:
         raise ValueError("cos_sin needs positions")
-    return ctypes.byref(Rotation(cos_sin.data_ptr(),
-                                 _indices("positions", positions, torch.int64, T, device),
-                                 cos_sin.shape[0], cos_sin.shape[1], ROTATION_STYLES[style]))
+    return Rotation(cos_sin.data_ptr(), _indices("positions", positions, torch.int64, T, device),
+                    shape[0], shape[1], code)
 
 
 def qk_norm_rope(q, k, q_gamma, k_gamma, eps: float, cos_sin=None, positions=None,
@@ -809,19 +842,17 @@ def qk_norm_rope(q, k, q_gamma, k_gamma, eps: float, cos_sin=None, positions=Non
     dev, dt = q.device, q.dtype
     if q.dim() != 3:
         raise ValueError("q must be [T, heads, D]")
-    T, D = q.shape[0], q.shape[2]
-    hq = _heads("q", q, (T, None, D), dt, dev)
-    hk = _heads("k", k, (T, None, D), dt, dev)
+    T, Hq, D = q.shape
+    hq = _heads("q", q, T, Hq, D, dt, dev)
+    hk = _heads("k", k, T, None, D, dt, dev)
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=dt, device=dev)
     if k_out is None:
         k_out = torch.empty(k.shape, dtype=dt, device=dev)
-    with torch.cuda.device(dev):
-        _check(library().rarn_qk_norm_rope(
-            _heads("q_out", q_out, q.shape, dt, dev), _heads("k_out", k_out, k.shape, dt, dev),
-            hq, hk, _gamma("q_gamma", q_gamma, D, dt, dev), _gamma("k_gamma", k_gamma, D, dt, dev),
-            _rotation(cos_sin, positions, style, T, dev), T, D, float(eps), _stream(dev)),
-            "rarn_qk_norm_rope")
+    _on(dev, "rarn_qk_norm_rope", library().rarn_qk_norm_rope,
+        _heads("q_out", q_out, T, Hq, D, dt, dev), _heads("k_out", k_out, T, hk.heads, D, dt, dev),
+        hq, hk, _gamma("q_gamma", q_gamma, D, dt, dev), _gamma("k_gamma", k_gamma, D, dt, dev),
+        _rotation(cos_sin, positions, style, T, dev), T, D, eps)
     return q_out, k_out
 
 
@@ -895,14 +926,11 @@ def kv_cache_write(k, v, cache: KVCache, slots) -> None:
     page; negative: left out; the others distinct)."""
     import torch
     dev, dt = cache.device, k.dtype
-    if k.dim() != 3:
-        raise ValueError("k must be [T, heads, D]")
-    shape = (k.shape[0], cache.heads, cache.head_dim)
-    hk, hv = _heads("k", k, shape, dt, dev), _heads("v", v, shape, dt, dev)
-    ps = _indices("slots", slots, torch.int64, shape[0], dev)
-    with torch.cuda.device(dev):
-        _check(library().rarn_kv_cache_write(cache._ref, hk, hv, ps, shape[0], _stream(dev)),
-               "rarn_kv_cache_write")
+    T = k.shape[0]
+    _on(dev, "rarn_kv_cache_write", library().rarn_kv_cache_write, cache._ref,
+        _heads("k", k, T, cache.heads, cache.head_dim, dt, dev),
+        _heads("v", v, T, cache.heads, cache.head_dim, dt, dev),
+        _indices("slots", slots, torch.int64, T, dev), T)
 
 
 def qk_norm_rope_kv_write(q, k, v, q_gamma, k_gamma, eps: float, cos_sin, positions,
@@ -911,32 +939,29 @@ def qk_norm_rope_kv_write(q, k, v, q_gamma, k_gamma, eps: float, cos_sin, positi
     rotated queries; the keys (quantised from their binary32 values) and values
     go to the cache."""
     import torch
-    dev, dt = cache.device, q.dtype
-    if q.dim() != 3:
-        raise ValueError("q must be [T, heads, D]")
-    T, D = q.shape[0], cache.head_dim
-    hq = _heads("q", q, (T, None, D), dt, dev)
-    hk = _heads("k", k, (T, cache.heads, D), dt, dev)
-    hv = _heads("v", v, (T, cache.heads, D), dt, dev)
+    dev, dt, H, D = cache.device, q.dtype, cache.heads, cache.head_dim
+    T = q.shape[0]
+    hq = _heads("q", q, T, None, D, dt, dev)
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=dt, device=dev)
-    with torch.cuda.device(dev):
-        _check(library().rarn_qk_norm_rope_kv_write(
-            _heads("q_out", q_out, q.shape, dt, dev), cache._ref, hq, hk, hv,
-            _gamma("q_gamma", q_gamma, D, dt, dev), _gamma("k_gamma", k_gamma, D, dt, dev),
-            _rotation(cos_sin, positions, style, T, dev),
-            _indices("slots", slots, torch.int64, T, dev), T, float(eps), _stream(dev)),
-            "rarn_qk_norm_rope_kv_write")
+    _on(dev, "rarn_qk_norm_rope_kv_write", library().rarn_qk_norm_rope_kv_write,
+        _heads("q_out", q_out, T, hq.heads, D, dt, dev), cache._ref, hq,
+        _heads("k", k, T, H, D, dt, dev), _heads("v", v, T, H, D, dt, dev),
+        _gamma("q_gamma", q_gamma, D, dt, dev), _gamma("k_gamma", k_gamma, D, dt, dev),
+        _rotation(cos_sin, positions, style, T, dev),
+        _indices("slots", slots, torch.int64, T, dev), T, eps)
     return q_out
 
 
 def _page_table(t, device):
+    """Address, row stride, sequences and width of a page table."""
     import torch
-    if t.dtype != torch.int32 or not t.is_cuda or t.device != device:
+    if t.dtype is not torch.int32 or t.device != device or not t.is_cuda:
         raise TypeError(f"page_table must be an int32 CUDA tensor on {device}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
         raise ValueError("page_table must be [sequences, pages] with unit stride along a row")
-    return t.data_ptr(), t.stride(0), t.shape[1]
+    return t.data_ptr(), stride[0], shape[0], shape[1]
 
 
 def kv_cache_read(cache: KVCache, page_table, starts, k_out, v_out):
@@ -945,18 +970,13 @@ def kv_cache_read(cache: KVCache, page_table, starts, k_out, v_out):
     type); page_table: [B, width] int32, starts: [B + 1] int32.  Rows past the
     last sequence stay as they were.  Returns (k_out, v_out)."""
     import torch
-    dev = cache.device
-    if k_out.dim() != 3:
-        raise ValueError("k_out must be [rows, heads, D]")
-    shape = (k_out.shape[0], cache.heads, cache.head_dim)
-    hk, hv = (_heads(n, t, shape, k_out.dtype, dev) for n, t in (("k_out", k_out),
-                                                                 ("v_out", v_out)))
-    table = _page_table(page_table, dev)
-    B = page_table.shape[0]
-    ps = _indices("starts", starts, torch.int32, B + 1, dev)
-    with torch.cuda.device(dev):
-        _check(library().rarn_kv_cache_read(hk, hv, cache._ref, *table, ps, B, shape[0],
-                                            _stream(dev)), "rarn_kv_cache_read")
+    dev, dt, H, D = cache.device, k_out.dtype, cache.heads, cache.head_dim
+    rows = k_out.shape[0]
+    hk = _heads("k_out", k_out, rows, H, D, dt, dev)
+    hv = _heads("v_out", v_out, rows, H, D, dt, dev)
+    table, stride, B, width = _page_table(page_table, dev)
+    _on(dev, "rarn_kv_cache_read", library().rarn_kv_cache_read, hk, hv, cache._ref, table, stride,
+        width, _indices("starts", starts, torch.int32, B + 1, dev), B, rows)
     return k_out, v_out
 
 
@@ -979,16 +999,13 @@ def tree_attention(q, cache: KVCache, page_table, context_lens, starts, mask=Non
     tensor of at least tree_attention_workspace_bytes bytes (allocated if None);
     calls that may overlap need one each.  Returns out (like q)."""
     import torch
-    dev, dt = cache.device, q.dtype
-    if q.dim() != 3:
-        raise ValueError("q must be [tokens, heads, D]")
-    N, D = q.shape[0], cache.head_dim
-    hq = _heads("q", q, (N, None, D), dt, dev)
+    dev, dt, D = cache.device, q.dtype, cache.head_dim
+    N = q.shape[0]
+    hq = _heads("q", q, N, None, D, dt, dev)
     if out is None:
         out = torch.empty(q.shape, dtype=dt, device=dev)
-    ho = _heads("out", out, q.shape, dt, dev)
-    table = _page_table(page_table, dev)
-    B = page_table.shape[0]
+    ho = _heads("out", out, N, hq.heads, D, dt, dev)
+    table, stride, B, width = _page_table(page_table, dev)
     ctx = _indices("context_lens", context_lens, torch.int32, B, dev)
     st = _indices("starts", starts, torch.int32, B + 1, dev)
     pm, words = None, 0
@@ -998,15 +1015,13 @@ def tree_attention(q, cache: KVCache, page_table, context_lens, starts, mask=Non
         words = mask.shape[1]
         pm = _indices("mask", mask, torch.int32, N * words, dev)
     if workspace is None:
-        n = max(tree_attention_workspace_bytes(N, B, q.shape[1], cache.heads, D), 16)
+        n = max(tree_attention_workspace_bytes(N, B, hq.heads, cache.heads, D), 16)
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+    elif workspace.device != dev or not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
-    with torch.cuda.device(dev):
-        _check(library().rarn_tree_attention(
-            ho, hq, cache._ref, *table, ctx, st, pm, words, B, N,
-            float(D ** -0.5 if scale is None else scale), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream(dev)), "rarn_tree_attention")
+    _on(dev, "rarn_tree_attention", library().rarn_tree_attention, ho, hq, cache._ref, table,
+        stride, width, ctx, st, pm, words, B, N, D ** -0.5 if scale is None else scale,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
 
 
