@@ -14,9 +14,12 @@
 // rotation pairs (pack p and pack rot / 2 + p for "half" pairs, two
 // neighbouring packs otherwise), so the rotation needs no exchange; a group
 // of D / (2 packs) lanes, rounded up to a power of two, owns a head and
-// reduces by shuffles inside itself.  The group takes kHeads heads of one
-// token with the same cos / sin registers (the table is binary32: for one
-// head its 8 D bytes would be four times the head's own).
+// reduces by shuffles inside itself.  A warp walks over heads of one tensor
+// and token, loading the next two heads of each group while it works on two:
+// the products of gamma with the token's cosines and sines, which every head
+// shares, stay in registers, and a head costs six multiply-adds per pair
+// (packed two to an instruction they measured no faster; the table is binary32: read per head its 8 D bytes
+// would be four times the head's own).
 #pragma once
 
 #include "kv.cuh"
@@ -41,49 +44,38 @@ struct RowParams {
     unsigned int *watchdog;
 };
 
-// What becomes of head `h` of the concatenation q, k, v.
-struct HeadRole {
-    const char *src;
+// What becomes of one tensor's heads of a token.
+struct Role {
+    const char *src;        // the token's first head
     char *dst;              // 16- or 32-bit output, or nullptr
     const void *gamma;
-    int64_t src_off, dst_off;  // elements
-    uint8_t *codes;         // the cache's codes of this head at slot 0 of page 0, or nullptr
+    int64_t src_hs, dst_hs; // elements between heads
+    uint8_t *codes;         // the cache's codes at head 0 of slot 0 of page 0, or nullptr
     float *scales;
+    int heads;
     bool rotate;
-    int head;               // in the cache
 };
 
-__device__ __forceinline__ HeadRole role_of(const RowParams &p, int64_t t, int h) {
-    HeadRole r{};
-    const bool cached = p.cache.k != nullptr;
-    if (h < p.q.heads) {
-        r.src = static_cast<const char *>(p.q.data);
-        r.src_off = t * p.q.ts + h * p.q.hs;
-        r.dst = static_cast<char *>(p.q_out.data);
-        r.dst_off = t * p.q_out.ts + h * p.q_out.hs;
-        r.gamma = p.q_gamma;
+enum Tensor : int { T_Q = 0, T_K = 1, T_V = 2 };
+
+template <typename T>
+__device__ __forceinline__ Role role_of(const RowParams &p, int64_t t, int which) {
+    Role r{};
+    const Heads &in = which == T_Q ? p.q : which == T_K ? p.k : p.v;
+    r.src = static_cast<const char *>(in.data) + t * in.ts * (int64_t)sizeof(T);
+    r.src_hs = in.hs;
+    r.heads = in.heads;
+    if (which != T_V) {
+        const Heads &out = which == T_Q ? p.q_out : p.k_out;
+        if (out.data) r.dst = static_cast<char *>(out.data) + t * out.ts * (int64_t)sizeof(T);
+        r.dst_hs = out.hs;
+        r.gamma = which == T_Q ? p.q_gamma : p.k_gamma;
         r.rotate = p.table != nullptr;
-        return r;
     }
-    h -= p.q.heads;
-    if (h < p.k.heads) {
-        r.src = static_cast<const char *>(p.k.data);
-        r.src_off = t * p.k.ts + h * p.k.hs;
-        r.dst = static_cast<char *>(p.k_out.data);
-        r.dst_off = t * p.k_out.ts + h * p.k_out.hs;
-        r.gamma = p.k_gamma;
-        r.rotate = p.table != nullptr;
-        r.codes = cached ? p.cache.k : nullptr;
-        r.scales = p.cache.k_scale;
-        r.head = h;
-        return r;
+    if (which != T_Q && p.cache.k) {
+        r.codes = which == T_K ? p.cache.k : p.cache.v;
+        r.scales = which == T_K ? p.cache.k_scale : p.cache.v_scale;
     }
-    h -= p.k.heads;
-    r.src = static_cast<const char *>(p.v.data);
-    r.src_off = t * p.v.ts + h * p.v.hs;
-    r.codes = p.cache.v;
-    r.scales = p.cache.v_scale;
-    r.head = h;
     return r;
 }
 
@@ -93,10 +85,8 @@ struct Place {
     int at;
 };
 
-__device__ __forceinline__ Place place_of(const RowParams &p, int64_t t, bool reporter) {
+__device__ __forceinline__ Place place_of(const RowParams &p, int64_t slot, bool reporter) {
     Place pl{-1, 0};
-    if (!p.cache.k) return pl;
-    const int64_t slot = p.slots[t];
     if (slot < 0) return pl;
     const int64_t page = slot / p.cache.page_size;
     if (page >= p.cache.pages) {
@@ -108,13 +98,12 @@ __device__ __forceinline__ Place place_of(const RowParams &p, int64_t t, bool re
     return pl;
 }
 
-// The row of the rotation table for token t; nullptr with *ok = false when its
+// The row of the rotation table for a position; nullptr with *ok = false when its
 // position lies outside the table (the token's rows are then left as they are).
-__device__ __forceinline__ const float *table_row(const RowParams &p, int64_t t, bool reporter,
+__device__ __forceinline__ const float *table_row(const RowParams &p, int64_t pos, bool reporter,
                                                   bool *ok) {
     *ok = true;
     if (!p.table) return nullptr;
-    const int64_t pos = p.positions[t];
     if (pos < 0 || pos >= p.table_rows) {
         if (reporter) atomicOr(p.watchdog, kWatchIndex);
         *ok = false;
@@ -147,152 +136,207 @@ __device__ __forceinline__ QMul row_mul(float amax, int fmt, float *scale) {
     return QMul{1.f / (amax * k), maxf * k};
 }
 
-// A warp: kHeads heads per group of LG lanes, one token.
-template <typename T, int LG, int kHeads>
-__global__ void __launch_bounds__(128) k_head_rows(const RowParams p, int chunks) {
+// A lane's 2 E elements as the first and second members of its E pairs: half
+// style, pack a against pack b; interleaved, even elements against odd ones.
+template <typename T, bool kInter>
+struct Pairs {
+    static constexpr int E = DT<T>::EPV;
+    float a[E], b[E];
+
+    __device__ __forceinline__ void unpack(const uint4 &pa, const uint4 &pb) {
+        float x[E], y[E];
+        DT<T>::unpack(pa, x);
+        DT<T>::unpack(pb, y);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            if constexpr (kInter) {
+                const float *z = 2 * j < E ? x + 2 * j : y + (2 * j - E);
+                a[j] = z[0];
+                b[j] = z[1];
+            } else {
+                a[j] = x[j];
+                b[j] = y[j];
+            }
+        }
+    }
+
+    // The elements in memory order.
+    __device__ __forceinline__ void elements(float (&x)[E], float (&y)[E]) const {
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            if constexpr (kInter) {
+                float *z = 2 * j < E ? x + 2 * j : y + (2 * j - E);
+                z[0] = a[j];
+                z[1] = b[j];
+            } else {
+                x[j] = a[j];
+                y[j] = b[j];
+            }
+        }
+    }
+};
+
+// Heads of a group that are loaded at a time, ahead of as many being worked
+// on, and CTAs per SM (at most 102 registers a thread).  Measured, bfloat16,
+// 8192 tokens of 64 + 8 heads of 128: 57.9 us; one head at a time 63.6 (60.3
+// with six CTAs), four CTAs 61.2.
+constexpr int kAtATime = 2;
+constexpr int kRowCtas = 5;
+
+// A warp: one token, `per` heads of one tensor for each group of LG lanes.
+// The work items of a token are its tensors' chunks of per * 32 / LG heads,
+// `chunks` in all (nq of q, then nk of k, then those of v).
+template <typename T, int LG, bool kInter>
+__global__ void __launch_bounds__(128, kRowCtas) k_head_rows(const RowParams p, int per, int nq, int nk,
+                                                   int chunks) {
     constexpr int E = DT<T>::EPV;  // elements per pack
     constexpr int GPW = 32 / LG;   // groups per warp
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int64_t t = item / chunks;
+    // a CTA's warps take the same chunk of four tokens, so they end together
+    const unsigned block = blockIdx.x / (unsigned)chunks;
+    const int64_t t = (int64_t)block * 4 + (threadIdx.x >> 5);
     if (t >= p.T) return;  // whole warps
-    const int lane = threadIdx.x & 31, group = lane / LG, l = lane % LG;
-    const int h0 = static_cast<int>(item - t * chunks) * (GPW * kHeads) + group;
-    const int heads = p.q.heads + p.k.heads + p.v.heads;
+    const int lane = threadIdx.x & 31, l = lane % LG;
+    int chunk = static_cast<int>(blockIdx.x - block * chunks);
+    const int which = chunk < nq ? T_Q : chunk < nq + nk ? T_K : T_V;
+    chunk -= which == T_Q ? 0 : which == T_K ? nq : nq + nk;
+    const Role r = role_of<T>(p, t, which);
+    const int h0 = chunk * (per * GPW) + lane / LG;
+    const int end = min(r.heads, (chunk + 1) * (per * GPW));
 
     // this lane's two packs
-    const int turned = p.table ? p.rot / (2 * E) : 0;  // lanes whose packs rotate
     const bool owns = l < p.D / (2 * E);
-    const bool turns = l < turned;
-    int ea, eb;
-    if (turns && !p.interleaved) {
-        ea = l * E;
-        eb = p.rot / 2 + l * E;
-    } else {
-        ea = 2 * E * l;  // past the rotated lanes this is rot + 2 E (l - turned) too
-        eb = ea + E;
-    }
+    const bool turns = r.rotate && l < p.rot / (2 * E);
+    // past the rotated lanes neighbouring packs in either style
+    const int ea = turns && !kInter ? l * E : 2 * E * l;
+    const int eb = turns && !kInter ? p.rot / 2 + l * E : ea + E;
 
-    uint4 xa[kHeads], xb[kHeads];
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        xa[i] = xb[i] = make_uint4(0, 0, 0, 0);
-        const int h = h0 + i * GPW;
-        if (owns && h < heads) {
-            const HeadRole r = role_of(p, t, h);
-            const T *s = reinterpret_cast<const T *>(r.src) + r.src_off;
-            xa[i] = ld_stream(s + ea);
-            xb[i] = ld_stream(s + eb);
+    // first what the other loads wait for
+    const int64_t pos = p.table ? p.positions[t] : 0;
+    const int64_t slot = r.codes ? p.slots[t] : -1;
+    const T *src = reinterpret_cast<const T *>(r.src);
+    auto load = [&](int h, uint4 &a, uint4 &b) {
+        a = b = make_uint4(0, 0, 0, 0);
+        if (owns && h < end) {
+            const T *s = src + h * r.src_hs;
+            a = ld_stream(s + ea);
+            b = ld_stream(s + eb);
         }
-    }
+    };
+    constexpr int U = kAtATime;
+    uint4 xa[U], xb[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(h0 + u * GPW, xa[u], xb[u]);
+
     bool ok;
-    const float *tr = table_row(p, t, lane == 0, &ok);
+    const float *tr = table_row(p, pos, lane == 0, &ok);
     if (!ok) return;  // the whole warp: one token
-    const Place pl = place_of(p, t, lane == 0);
-    float c[E], s[E];
+    const Place pl = place_of(p, slot, lane == 0);
+    // gamma, and its products with the cosines and sines
+    Pairs<T, kInter> g;
+    float bs[E], as[E];  // -gamma_b sin, gamma_a sin; times cos they stay in g
+    {
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-        c[j] = 1.f;
-        s[j] = 0.f;
-    }
-    if (tr && turns) {
+        for (int j = 0; j < E; ++j) g.a[j] = g.b[j] = 1.f;
+        if (r.gamma && owns)
+            g.unpack(ld_keep(static_cast<const T *>(r.gamma) + ea),
+                     ld_keep(static_cast<const T *>(r.gamma) + eb));
+        if (turns) {
 #pragma unroll
-        for (int j = 0; j < E; j += 4) {
-            const float4 cv = __ldg(reinterpret_cast<const float4 *>(tr + l * E + j));
-            const float4 sv = __ldg(reinterpret_cast<const float4 *>(tr + p.rot / 2 + l * E + j));
-            c[j] = cv.x; c[j + 1] = cv.y; c[j + 2] = cv.z; c[j + 3] = cv.w;
-            s[j] = sv.x; s[j + 1] = sv.y; s[j + 2] = sv.z; s[j + 3] = sv.w;
+            for (int j = 0; j < E; j += 4) {
+                const float4 c = __ldg(reinterpret_cast<const float4 *>(tr + l * E + j));
+                const float4 s =
+                    __ldg(reinterpret_cast<const float4 *>(tr + p.rot / 2 + l * E + j));
+                const float cj[4] = {c.x, c.y, c.z, c.w}, sj[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    bs[j + u] = -g.b[j + u] * sj[u];
+                    as[j + u] = g.a[j + u] * sj[u];
+                    g.a[j + u] *= cj[u];
+                    g.b[j + u] *= cj[u];
+                }
+            }
         }
     }
     const float inv_d = 1.f / static_cast<float>(p.D);
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        const int h = h0 + i * GPW;
-        const bool live = owns && h < heads;
-        const HeadRole r = role_of(p, t, h < heads ? h : 0);
-        float f[2 * E];
-        {
-            float a[E], b[E];
-            DT<T>::unpack(xa[i], a);
-            DT<T>::unpack(xb[i], b);
-#pragma unroll
-            for (int j = 0; j < E; ++j) {
-                f[j] = a[j];
-                f[E + j] = b[j];
-            }
-        }
-        if (p.q_gamma || p.k_gamma) {  // uniform; a row without gamma keeps factor 1
+    const QMul given = r.codes && p.cache.mode == Q_TENSOR ? QMul{1.f / __ldg(r.scales), 1.f}
+                                                           : QMul{1.f, 1.f};
+    uint8_t *codes = nullptr;
+    float *scales = nullptr;
+    if (pl.page >= 0) {
+        codes = r.codes + pl.page * p.cache.page_stride + pl.at * p.cache.slot_stride;
+        scales = r.scales + pl.page * p.cache.s_page + pl.at * p.cache.s_slot;
+    }
+
+    auto head = [&](int h, const uint4 &pa, const uint4 &pb) {
+        const bool live = owns && h < end;
+        Pairs<T, kInter> x;
+        x.unpack(pa, pb);
+        float inv = 1.f;
+        if (r.gamma) {  // uniform
             float ss = 0.f;
 #pragma unroll
-            for (int j = 0; j < 2 * E; ++j) ss = fmaf(f[j], f[j], ss);
-            ss = group_sum<LG>(ss);
-            if (live && r.gamma) {
-                const float inv = rsqrtf(fmaf(ss, inv_d, p.eps));
-                float a[E], b[E];
-                DT<T>::unpack(ld_keep(static_cast<const T *>(r.gamma) + ea), a);
-                DT<T>::unpack(ld_keep(static_cast<const T *>(r.gamma) + eb), b);
-#pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    f[j] = f[j] * inv * a[j];
-                    f[E + j] = f[E + j] * inv * b[j];
-                }
-            }
+            for (int j = 0; j < E; ++j) ss = fmaf(x.b[j], x.b[j], fmaf(x.a[j], x.a[j], ss));
+            inv = rsqrtf(fmaf(group_sum<LG>(ss), inv_d, p.eps));
         }
-        if (turns && r.rotate) {
-            if (p.interleaved) {
+        if (turns) {
 #pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    const float x = f[2 * j], y = f[2 * j + 1];
-                    f[2 * j] = x * c[j] - y * s[j];
-                    f[2 * j + 1] = y * c[j] + x * s[j];
-                }
-            } else {
+            for (int j = 0; j < E; ++j) {
+                const float a = fmaf(x.b[j], bs[j], x.a[j] * g.a[j]);
+                const float b = fmaf(x.a[j], as[j], x.b[j] * g.b[j]);
+                x.a[j] = a * inv;
+                x.b[j] = b * inv;
+            }
+        } else if (r.gamma) {
 #pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    const float x = f[j], y = f[E + j];
-                    f[j] = x * c[j] - y * s[j];
-                    f[E + j] = y * c[j] + x * s[j];
-                }
+            for (int j = 0; j < E; ++j) {
+                x.a[j] = x.a[j] * inv * g.a[j];
+                x.b[j] = x.b[j] * inv * g.b[j];
             }
         }
         float fa[E], fb[E];
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            fa[j] = f[j];
-            fb[j] = f[E + j];
-        }
+        x.elements(fa, fb);
         if (live && r.dst) {
-            T *d = reinterpret_cast<T *>(r.dst) + r.dst_off;
+            T *d = reinterpret_cast<T *>(r.dst) + h * r.dst_hs;
             st_global(d + ea, DT<T>::pack(fa));
             st_global(d + eb, DT<T>::pack(fb));
         }
-        if (p.cache.k) {  // uniform
-            float amax = 0.f;
+        if (codes) {  // uniform
+            QMul m = given;
+            if (p.cache.mode == Q_ROW) {
+                float amax = 0.f;
 #pragma unroll
-            for (int j = 0; j < 2 * E; ++j) amax = fmaxf(amax, fabsf(f[j]));
-            amax = group_max<LG>(amax);
-            if (live && r.codes && pl.page >= 0) {
-                QMul m;
-                if (p.cache.mode == Q_ROW) {
-                    float scale;
-                    m = row_mul(amax, p.cache.fmt, &scale);
-                    if (l == 0)
-                        r.scales[pl.page * p.cache.s_page + r.head * p.cache.s_head +
-                                 pl.at * p.cache.s_slot] = scale;
-                } else {
-                    m = QMul{1.f / __ldg(r.scales), 1.f};
-                }
+                for (int j = 0; j < E; ++j) amax = fmaxf(amax, fmaxf(fabsf(fa[j]), fabsf(fb[j])));
+                amax = group_max<LG>(amax);
+                float scale;
+                m = row_mul(amax, p.cache.fmt, &scale);
+                if (l == 0 && live) scales[h * p.cache.s_head] = scale;
+            }
 #pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    fa[j] = (fa[j] * m.m1) * m.m2;
-                    fb[j] = (fb[j] * m.m1) * m.m2;
-                }
-                uint8_t *d = r.codes + pl.page * p.cache.page_stride +
-                             r.head * p.cache.head_stride + pl.at * p.cache.slot_stride;
+            for (int j = 0; j < E; ++j) {
+                fa[j] = (fa[j] * m.m1) * m.m2;
+                fb[j] = (fb[j] * m.m1) * m.m2;
+            }
+            if (live) {
+                uint8_t *d = codes + h * p.cache.head_stride;
                 st_codes<E>(d + ea, fa, p.cache.fmt);
                 st_codes<E>(d + eb, fb, p.cache.fmt);
             }
+        }
+    };
+    // groups whose heads have run out go along with the warp's reductions
+    const int first = chunk * (per * GPW);
+#pragma unroll 1
+    for (int i = 0; first + i < end; i += U * GPW) {
+        uint4 na[U], nb[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) load(h0 + i + (U + u) * GPW, na[u], nb[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (first + i + u * GPW < end) head(h0 + i + u * GPW, xa[u], xb[u]);  // uniform
+            xa[u] = na[u];
+            xb[u] = nb[u];
         }
     }
 }
@@ -308,12 +352,22 @@ __global__ void __launch_bounds__(128) k_head_rows_any(const RowParams p, int he
     const int64_t t = item / heads;
     if (t >= p.T) return;
     const int lane = threadIdx.x & 31;
-    const HeadRole r = role_of(p, t, static_cast<int>(item - t * heads));
+    int h = static_cast<int>(item - t * heads);
+    int which = T_Q;
+    if (h >= p.q.heads) {
+        h -= p.q.heads;
+        which = T_K;
+        if (h >= p.k.heads) {
+            h -= p.k.heads;
+            which = T_V;
+        }
+    }
+    const Role r = role_of<T>(p, t, which);
     bool ok;
-    const float *tr = table_row(p, t, lane == 0, &ok);
+    const float *tr = table_row(p, p.table ? p.positions[t] : 0, lane == 0, &ok);
     if (!ok) return;
-    const Place pl = place_of(p, t, lane == 0);
-    const T *src = reinterpret_cast<const T *>(r.src) + r.src_off;
+    const Place pl = place_of(p, r.codes ? p.slots[t] : -1, lane == 0);
+    const T *src = reinterpret_cast<const T *>(r.src) + h * r.src_hs;
     float inv = 1.f;
     if (r.gamma) {
         float ss = 0.f;
@@ -347,7 +401,7 @@ __global__ void __launch_bounds__(128) k_head_rows_any(const RowParams p, int he
         }
     };
     QMul m{1.f, 1.f};
-    const bool store_codes = r.codes && pl.page >= 0;
+    const bool store_codes = pl.page >= 0;
     if (store_codes) {
         if (p.cache.mode == Q_ROW) {
             float amax = 0.f;
@@ -361,21 +415,21 @@ __global__ void __launch_bounds__(128) k_head_rows_any(const RowParams p, int he
             float scale;
             m = row_mul(amax, p.cache.fmt, &scale);
             if (lane == 0)
-                r.scales[pl.page * p.cache.s_page + r.head * p.cache.s_head +
+                r.scales[pl.page * p.cache.s_page + h * p.cache.s_head +
                          pl.at * p.cache.s_slot] = scale;
         } else {
             m.m1 = 1.f / __ldg(r.scales);
         }
     }
     uint8_t *codes = store_codes ? r.codes + pl.page * p.cache.page_stride +
-                                       r.head * p.cache.head_stride + pl.at * p.cache.slot_stride
+                                       h * p.cache.head_stride + pl.at * p.cache.slot_stride
                                  : nullptr;
     for (int i = lane; i < work; i += 32) {
         int e0, e1;
         float a, b;
         value(i, e0, e1, a, b);
         if (r.dst) {
-            T *d = reinterpret_cast<T *>(r.dst) + r.dst_off;
+            T *d = reinterpret_cast<T *>(r.dst) + h * r.dst_hs;
             d[e0] = DT<T>::from_f(a);
             if (e1 >= 0) d[e1] = DT<T>::from_f(b);
         }

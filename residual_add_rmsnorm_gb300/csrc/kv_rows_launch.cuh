@@ -6,18 +6,36 @@
 namespace rarn {
 namespace kv {
 
-template <typename T, int LG>
+// Heads per group at most, and warps per SM below which a call's heads are
+// spread over more warps (8192 tokens of 64 + 8 heads: 57.9 us with 8 heads,
+// 62.6 with 4, 61 with 16; 517 tokens of 40 + 8: 8.3 us with 16 warps, 10.3
+// with 32 or 64, which leave a warp two loads).
+constexpr int kRowHeads = 8;
+constexpr int kRowWarps = 16;
+
+template <typename T, int LG, bool kInter>
 inline cudaError_t launch_head_group(const RowParams &p, int num_sms, bool pdl, cudaStream_t st) {
-    const int heads = p.q.heads + p.k.heads + p.v.heads;
     constexpr int gpw = 32 / LG;
-    // Several heads per group share the table's registers and keep more loads
-    // in flight; one head per group gives a short call more warps.
-    const int many = (heads + gpw * 4 - 1) / (gpw * 4);
-    const bool wide = p.T * many >= (int64_t)num_sms * 16;
-    const int chunks = wide ? many : (heads + gpw - 1) / gpw;
-    const dim3 grid((unsigned)((p.T * chunks + 3) / 4));
-    return wide ? launch_kernel(k_head_rows<T, LG, 4>, grid, dim3(128), 0, st, pdl, 1, p, chunks)
-                : launch_kernel(k_head_rows<T, LG, 1>, grid, dim3(128), 0, st, pdl, 1, p, chunks);
+    auto chunks_of = [](int heads, int per) { return (heads + per * gpw - 1) / (per * gpw); };
+    // Heads per group: as many as leave every SM its warps; the table's
+    // products are formed once per warp.
+    int per = kRowHeads;
+    int nq, nk, nv;
+    for (;; per /= 2) {
+        nq = chunks_of(p.q.heads, per);
+        nk = chunks_of(p.k.heads, per);
+        nv = chunks_of(p.v.heads, per);
+        if (per == 1 || p.T * (nq + nk + nv) >= (int64_t)num_sms * kRowWarps) break;
+    }
+    const int chunks = nq + nk + nv;
+    return launch_kernel(k_head_rows<T, LG, kInter>, dim3((unsigned)((p.T + 3) / 4 * chunks)),
+                         dim3(128), 0, st, pdl, 1, p, per, nq, nk, chunks);
+}
+
+template <typename T, int LG>
+inline cudaError_t launch_head_style(const RowParams &p, int num_sms, bool pdl, cudaStream_t st) {
+    return p.interleaved ? launch_head_group<T, LG, true>(p, num_sms, pdl, st)
+                         : launch_head_group<T, LG, false>(p, num_sms, pdl, st);
 }
 
 template <typename T>
@@ -29,10 +47,10 @@ cudaError_t launch_head_rows(const RowParams &p, bool vec, int num_sms, bool pdl
                              dim3(128), 0, st, pdl, 1, p, heads);
     }
     const int lanes = p.D / (2 * DT<T>::EPV);
-    if (lanes <= 4) return launch_head_group<T, 4>(p, num_sms, pdl, st);
-    if (lanes <= 8) return launch_head_group<T, 8>(p, num_sms, pdl, st);
-    if (lanes <= 16) return launch_head_group<T, 16>(p, num_sms, pdl, st);
-    return launch_head_group<T, 32>(p, num_sms, pdl, st);
+    if (lanes <= 4) return launch_head_style<T, 4>(p, num_sms, pdl, st);
+    if (lanes <= 8) return launch_head_style<T, 8>(p, num_sms, pdl, st);
+    if (lanes <= 16) return launch_head_style<T, 16>(p, num_sms, pdl, st);
+    return launch_head_style<T, 32>(p, num_sms, pdl, st);
 }
 
 template <typename T>
