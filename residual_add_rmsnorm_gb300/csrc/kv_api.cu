@@ -20,11 +20,11 @@ extern template cudaError_t launch_head_rows<__half>(const RowParams &, bool, in
                                                      cudaStream_t);
 extern template cudaError_t launch_head_rows<float>(const RowParams &, bool, int, bool,
                                                     cudaStream_t);
-extern template cudaError_t launch_cache_read<__nv_bfloat16>(const ReadParams &, bool, bool,
+extern template cudaError_t launch_cache_read<__nv_bfloat16>(const ReadParams &, int, int, bool,
                                                              cudaStream_t);
-extern template cudaError_t launch_cache_read<__half>(const ReadParams &, bool, bool,
+extern template cudaError_t launch_cache_read<__half>(const ReadParams &, int, int, bool,
                                                       cudaStream_t);
-extern template cudaError_t launch_cache_read<float>(const ReadParams &, bool, bool,
+extern template cudaError_t launch_cache_read<float>(const ReadParams &, int, int, bool,
                                                      cudaStream_t);
 }  // namespace kv
 namespace tree {
@@ -109,9 +109,10 @@ rarn_status check_heads(const rarn_heads &h, int64_t T, int64_t D, bool output) 
     return RARN_OK;
 }
 
-bool packs_ok(const rarn_heads &h) {
+// Whether every head begins on an `a`-byte boundary.
+bool packs_ok(const rarn_heads &h, int a = 16) {
     const int64_t s = size_of(h.dtype);
-    return on(h.data, 16) && h.token_stride * s % 16 == 0 && h.head_stride * s % 16 == 0;
+    return on(h.data, a) && h.token_stride * s % a == 0 && h.head_stride * s % a == 0;
 }
 
 // Whether the (stride, count) dimensions with `inner` units innermost address
@@ -463,14 +464,15 @@ rarn_status rarn_kv_cache_read(rarn_heads k_out, rarn_heads v_out, const rarn_kv
     p.rows = rows;
     p.D = (int)D;
     p.watchdog = dev.watchdog;
-    const bool vec = packs_ok(k_out) && packs_ok(v_out);
+    const bool vec = packs_ok(k_out, 16) && packs_ok(v_out, 16);
+    const int store = !vec ? 0 : packs_ok(k_out, 32) && packs_ok(v_out, 32) ? 32 : 16;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const bool pdl = host::pdl_enabled();
     cudaError_t e;
     switch (k_out.dtype) {
-    case RARN_BF16: e = kv::launch_cache_read<__nv_bfloat16>(p, vec, pdl, cs); break;
-    case RARN_F16: e = kv::launch_cache_read<__half>(p, vec, pdl, cs); break;
-    default: e = kv::launch_cache_read<float>(p, vec, pdl, cs); break;
+    case RARN_BF16: e = kv::launch_cache_read<__nv_bfloat16>(p, store, dev.num_sms, pdl, cs); break;
+    case RARN_F16: e = kv::launch_cache_read<__half>(p, store, dev.num_sms, pdl, cs); break;
+    default: e = kv::launch_cache_read<float>(p, store, dev.num_sms, pdl, cs); break;
     }
     return e == cudaSuccess ? RARN_OK : host::cuda_failed(e);
 }

@@ -4,6 +4,6 @@
 namespace rarn {
 namespace kv {
 template cudaError_t launch_head_rows<__nv_bfloat16>(const RowParams &, bool, int, bool, cudaStream_t);
-template cudaError_t launch_cache_read<__nv_bfloat16>(const ReadParams &, bool, bool, cudaStream_t);
+template cudaError_t launch_cache_read<__nv_bfloat16>(const ReadParams &, int, int, bool, cudaStream_t);
 }  // namespace kv
 }  // namespace rarn

@@ -4,6 +4,6 @@
 namespace rarn {
 namespace kv {
 template cudaError_t launch_head_rows<float>(const RowParams &, bool, int, bool, cudaStream_t);
-template cudaError_t launch_cache_read<float>(const ReadParams &, bool, bool, cudaStream_t);
+template cudaError_t launch_cache_read<float>(const ReadParams &, int, int, bool, cudaStream_t);
 }  // namespace kv
 }  // namespace rarn
