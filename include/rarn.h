@@ -689,7 +689,7 @@ rarn_status rarn_kv_cache_read(rarn_heads k_out, rarn_heads v_out, const rarn_kv
  * softmax weights rounded to binary16 (11 bits) for the second product.
  * head_dim 64, 96, 128, 192 or 256; q 16-byte aligned with strides multiples
  * of 8 elements (else RARN_ERR_UNSUPPORTED).  `workspace`:
- * rarn_tree_attention_workspace_bytes bytes of device memory, 16-byte aligned,
+ * rarn_tree_attention_workspace_bytes bytes of device memory, 32-byte aligned,
  * scratch for this call alone: calls that may overlap on the GPU need one
  * each.  The lengths are read on the device, so one captured call serves every
  * later length within its page table's width.  Results are the same bits on

@@ -514,7 +514,7 @@ rarn_status rarn_tree_attention(rarn_heads out, rarn_heads q, const rarn_kv_cach
     if (tokens >= kMaxItems / q.heads || !packs_ok(q)) return RARN_ERR_UNSUPPORTED;
     const tree::Plan pl = tree::plan(tokens, B, q.heads, cache->heads, D);
     if (pl.segments >= kMaxItems) return RARN_ERR_UNSUPPORTED;
-    if (!workspace || !on(workspace, 16) || (int64_t)workspace_bytes < pl.bytes)
+    if (!workspace || !on(workspace, 32) || (int64_t)workspace_bytes < pl.bytes)
         return RARN_ERR_INVALID_ARG;
     const Range outs[2] = {range_of(out, tokens, D), solid(workspace, pl.bytes)};
     const Range ins[8] = {range_of(q, tokens, D), cr.k, cr.v, cr.ks, cr.vs,

@@ -6,6 +6,7 @@
 #include "gemm_norm_launch.cuh"  // tensor_map_encoder
 #include "tree_attn.cuh"
 #include "tree_plan.h"
+#include "tree_tile.cuh"
 
 namespace rarn {
 namespace tree {
@@ -13,8 +14,8 @@ namespace tree {
 // CTAs of a kernel that the current device holds at once; the kernel's shared
 // memory is allowed for and the question asked once per device.
 template <typename K>
-inline cudaError_t resident(K kernel, int threads, int smem, int num_sms, std::atomic<int> *known,
-                            int *ctas) {
+inline cudaError_t resident(K kernel, int threads, int smem, int num_sms, int most,
+                            std::atomic<int> *known, int *ctas) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -28,7 +29,7 @@ inline cudaError_t resident(K kernel, int threads, int smem, int num_sms, std::a
         if (per < 1) return cudaErrorInvalidConfiguration;
         slot.store(per, std::memory_order_relaxed);
     }
-    *ctas = per * num_sms < kMaxCtas ? per * num_sms : kMaxCtas;
+    *ctas = per * num_sms < most ? per * num_sms : most;
     return cudaSuccess;
 }
 
@@ -77,7 +78,7 @@ inline cudaError_t launch_rows(const Params &p, const Plan &pl, int num_sms, boo
                   encode_codes<D>(&vm, p.cache.v, p.cache)))
         return cudaErrorInvalidValue;
     int ctas = 0;
-    cudaError_t e = resident(kernel, kThreads, S::kBytes, num_sms, known, &ctas);
+    cudaError_t e = resident(kernel, kThreads, S::kBytes, num_sms, kMaxCtas, known, &ctas);
     if (e != cudaSuccess) return e;
     if ((e = launch_kernel(kernel, dim3(ctas), dim3(kThreads), S::kBytes, st, pdl, 1, p, km,
                            vm)) != cudaSuccess)
@@ -110,8 +111,30 @@ inline cudaError_t launch_type(const Params &p, const Plan &pl, int num_sms, boo
     return launch_copies<D, kE5M2, false>(p, pl, num_sms, pdl, st);
 }
 
+template <int D, bool kE5M2, bool kTwo>
+inline cudaError_t launch_tiles(const Params &p, const Plan &pl, int num_sms, bool pdl,
+                                cudaStream_t st) {
+    static std::atomic<int> known[64];
+    auto kernel = k_tree_tile<D, kE5M2, kTwo>;
+    constexpr int smem = TileSmem<D>::kBytes;
+    int ctas = 0;
+    cudaError_t e = resident(kernel, kTileThreads, smem, num_sms, kMaxTileCtas, known, &ctas);
+    if (e != cudaSuccess) return e;
+    if ((e = launch_kernel(kernel, dim3(ctas), dim3(kTileThreads), smem, st, pdl, 1, p)) !=
+        cudaSuccess)
+        return e;
+    return launch_join<D>(p, pl.rows, ctas >= 4 * pl.expected, pdl, st);
+}
+
 template <bool kE5M2>
 cudaError_t launch_tree(const Params &p, const Plan &pl, int num_sms, bool pdl, cudaStream_t st) {
+    if (pl.tiles) {
+        if (p.D == 64)
+            return pl.rows == 256 ? launch_tiles<64, kE5M2, true>(p, pl, num_sms, pdl, st)
+                                  : launch_tiles<64, kE5M2, false>(p, pl, num_sms, pdl, st);
+        return pl.rows == 256 ? launch_tiles<128, kE5M2, true>(p, pl, num_sms, pdl, st)
+                              : launch_tiles<128, kE5M2, false>(p, pl, num_sms, pdl, st);
+    }
     switch (p.D) {
     case 64: return launch_type<64, kE5M2>(p, pl, num_sms, pdl, st);
     case 96: return launch_type<96, kE5M2>(p, pl, num_sms, pdl, st);

@@ -9,6 +9,7 @@ namespace tree {
 
 struct Plan {
     int rows;          // rows (drafted token x query head of the group) of a segment
+    bool tiles;        // the tensor-memory kernel (tree_tile.cuh)
     int64_t segments;  // at most
     int64_t expected;  // segments where all sequences draft alike
     int64_t joins_off, ml_off, part_off, bytes;
@@ -18,19 +19,20 @@ inline bool dim_ok(int64_t D) { return D == 64 || D == 96 || D == 128 || D == 19
 
 // tokens drafted tokens in all, of B sequences.
 inline Plan plan(int64_t tokens, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
-    constexpr int64_t kCtas = 608;
     Plan p{};
     const int64_t G = Hq / Hk;
     const int64_t per = ((tokens + B - 1) / B) * G;  // rows of an average sequence
-    p.rows = per > 8 && D <= 128 ? 16 : 8;
+    p.tiles = (D == 64 || D == 128) && per > 16;
+    p.rows = p.tiles ? (per > 128 ? 256 : 128) : per > 8 && D <= 128 ? 16 : 8;
+    const int64_t ctas = p.tiles ? 160 : 608;
     // every sequence ends in at most one block that is not full
     p.segments = Hk * (tokens * G / p.rows + B);
     p.expected = Hk * B * ((per + p.rows - 1) / p.rows);
     auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
     p.joins_off = 256;
     p.ml_off = p.joins_off + up(32 * p.segments);
-    p.part_off = p.ml_off + up(2 * kCtas * p.rows * 8);
-    p.bytes = p.part_off + 2 * kCtas * p.rows * D * 4;
+    p.part_off = p.ml_off + up(2 * ctas * p.rows * 8);
+    p.bytes = p.part_off + 2 * ctas * p.rows * D * 4;
     return p;
 }
 
