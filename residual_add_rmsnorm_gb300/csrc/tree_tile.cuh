@@ -13,12 +13,14 @@
 //   * eight converter warps load two tiles ahead into registers, convert the
 //     codes (exactly) and store keys and values in 128-byte-swizzled rows,
 //     and the tile's scales beside them;
-//   * one thread issues tcgen05.mma: S into one of two 128-column
-//     accumulators, and O += P V with P read from tensor memory and V from
-//     the same row layout as K (as the transposed, N-major operand);
 //   * two pipelines of four softmax warps, a thread per row: scores from
 //     tensor memory, running maximum with slack, weights rounded to binary16
-//     over the scores' columns.
+//     over the scores' columns; one thread of each issues its tcgen05.mma: S
+//     into the pipeline's 128 columns, and O += P V with P read from tensor
+//     memory and V from the same row layout as K (as the N-major operand).
+// Sixteen warps in all: with a seventeenth for the products a thread has 96
+// registers instead of 128, and what spills goes through the little L1 that
+// shared memory leaves (three times the time).
 // With up to 128 rows the pipelines take alternate tiles of the same rows, and
 // their states are joined at the end; with up to 256 rows each has its own
 // 128. While one pipeline is at its softmax the other's products run.
@@ -35,8 +37,8 @@ namespace tree {
 constexpr int kTileKeys = 128;   // keys of a tile
 constexpr int kTileRows = 128;   // rows of a pipeline
 constexpr int kSoftWarps = 8;
-constexpr int kConvWarps = 8;
-constexpr int kTileThreads = 32 * (kSoftWarps + kConvWarps + 1);
+constexpr int kConvWarps = 8;       // 16 keys of a tile each
+constexpr int kTileThreads = 32 * (kSoftWarps + kConvWarps);
 constexpr int kMaxTileCtas = 160;
 
 // What the softmax needs of a tile besides its scores.
@@ -60,7 +62,8 @@ struct TileSmem {
 // Barriers, in one array.
 enum Bar : int {
     B_KFULL = 0, B_KEMPTY = 2, B_VFULL = 4, B_VEMPTY = 6, B_SFULL = 8, B_PFULL = 10, B_ODONE = 12,
-    B_INFO = 14, B_QMAX = 18, B_QREADY = 19, B_MERGE = 20, B_DRAIN = 21, B_COUNT = 22
+    B_INFO = 14, B_QMAX = 18, B_QREADY = 19, B_MERGE = 20, B_DRAIN = 21, B_QDONE = 22, B_NEXT = 23,
+    B_COUNT = 24
 };
 
 // A CTA's share of the line, segment by segment.  Every role walks it alike.
@@ -251,6 +254,64 @@ __device__ __forceinline__ void add_nonfinite(const Params &p, const Segment &sg
     }
 }
 
+// A row's largest score of a tile: columns of S at `ts` times the keys'
+// factors.  kEdge: only where bits of vis are set.
+template <bool kEdge>
+__device__ __forceinline__ float row_top(uint32_t ts, const TileInfo &ti,
+                                         const uint32_t (&vis)[4]) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        float s[32];
+        gemm::tmem_ld32(ts + 32 * c, s);
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            const float4 kk = *reinterpret_cast<const float4 *>(ti.kk + 32 * c + j);
+            float a[4] = {s[j] * kk.x, s[j + 1] * kk.y, s[j + 2] * kk.z, s[j + 3] * kk.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (kEdge && !((vis[c] >> (j + u)) & 1u)) a[u] = -INFINITY;
+            top = fmaxf(top, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])));
+        }
+    }
+    return top;
+}
+
+// A row's weights of a tile, 2^(score - off) times the value scales, in
+// binary16 over the scores' columns; returns the sum of 2^(score - off).
+template <bool kEdge>
+__device__ __forceinline__ float row_weights(uint32_t ts, const TileInfo &ti,
+                                             const uint32_t (&vis)[4], float off) {
+    float l = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        float s[32];
+        gemm::tmem_ld32(ts + 32 * c, s);
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            const float4 kk = *reinterpret_cast<const float4 *>(ti.kk + 32 * c + j);
+            const float4 vs = *reinterpret_cast<const float4 *>(ti.vs + 32 * c + j);
+            const float k4[4] = {kk.x, kk.y, kk.z, kk.w}, v4[4] = {vs.x, vs.y, vs.z, vs.w};
+            float q[4], x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool hid = kEdge && !((vis[c] >> (j + u)) & 1u);
+                q[u] = fmaf(s[j + u], k4[u], -off);
+                if (hid) q[u] = -INFINITY;
+                q[u] = exp2_fast(q[u]);
+                x[u] = q[u] * v4[u];
+                if (hid) x[u] = 0.f;
+            }
+            l += (q[0] + q[1]) + (q[2] + q[3]);
+            w[j / 2] = pack_h2(x[0], x[1]);
+            w[j / 2 + 1] = pack_h2(x[2], x[3]);
+        }
+        tmem_st16(ts + 16 * c, w);
+    }
+    return l;
+}
+
 // The k of an offset m - k.
 __device__ __forceinline__ int k_of(float off, float m) {
     return __float2int_rn((m == -INFINITY ? 0.f : m) - off);
@@ -260,70 +321,52 @@ __device__ __forceinline__ int k_of(float off, float m) {
 // Converters
 // ---------------------------------------------------------------------------
 
-// A tile as a converter thread knows it: its keys' codes on the way, and what
-// it needs for the values'.
-template <int D>
-struct Fetch {
-    static constexpr int kLoads = D / 32;  // of each of K and V: 256 threads, 16 codes a load
-    uint4 k[kLoads];
-    int64_t code;   // where the codes of key (lane & 15) of the warp's 16 lie, < 0: nowhere
-    float sc;       // lanes 0 .. 15: key scale, 16 .. 31: value scale of key (lane & 15)
-    uint32_t ok;    // the warp's 16 keys that exist
-    bool past;      // the tile reaches behind the context
-    bool first;     // of its segment
+// A tile as a converter lane knows it: key (lane & 15) of the warp's 16.
+struct Look {
+    int64_t code;     // where the key's codes lie, < 0: nowhere
+    float sc;         // lanes 0 .. 15: its key scale, 16 .. 31: its value scale
+    bool past;        // the tile reaches behind the context
+    bool first;       // of its segment
 };
 
-// Where a converter thread's i-th load belongs: row of the tile, chunk of 16
-// codes.  Eight neighbouring lanes store two rows' neighbouring chunks, which
-// the swizzle keeps in different banks.
+// Loads of each of K and V by a converter thread: 256 threads, 16 codes a load.
 template <int D>
-__device__ __forceinline__ void conv_place(int warp, int lane, int i, int &row, int &x) {
+constexpr int kConvLoads = D / 32;
+
+// Where a converter thread's i-th load belongs: row of the warp's 16, chunk of
+// 16 codes.  Eight neighbouring lanes store two rows' neighbouring chunks,
+// which the swizzle keeps in different banks.
+template <int D>
+__device__ __forceinline__ void conv_place(int lane, int i, int &row, int &x) {
     if constexpr (D == 128) {
-        row = warp * 16 + ((lane >> 2) & 3) + 4 * i;
+        row = ((lane >> 2) & 3) + 4 * i;
         x = (lane & 3) | ((lane >> 4) << 2);
     } else {
-        row = warp * 16 + (lane >> 2) + 8 * i;
+        row = (lane >> 2) + 8 * i;
         x = lane & 3;
     }
 }
 
+// A converter thread's share of a tile's codes.
 template <int D>
-__device__ __forceinline__ void load_codes(const uint8_t *from, int64_t code,
-                                           uint4 (&w)[Fetch<D>::kLoads]) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < Fetch<D>::kLoads; ++i) {
-        int row, x;
-        conv_place<D>(0, lane, i, row, x);
-        const int64_t at = __shfl_sync(0xffffffffu, code, row);
-        w[i] = make_uint4(0, 0, 0, 0);
-        if (at >= 0) w[i] = ld_stream(from + at + x * 16);
-    }
-}
+struct Codes {
+    uint4 k[kConvLoads<D>], v[kConvLoads<D>];
 
-template <int D>
-__device__ __forceinline__ void fetch_tile(const Params &p, const Segment &sg, int tile, int t0,
-                                           int warp, Fetch<D> &f) {
-    const int lane = threadIdx.x & 31;
-    const int j0 = tile * kTileKeys;
-    const int j = j0 + warp * 16 + (lane & 15);
-    KeyAt mine{-1, 0};
-    if (j < sg.s.len) {
-        const int pg = p.page_of(j);
-        const int64_t page = p.table[sg.b * p.table_stride + pg];
-        if (page >= 0 && page < p.cache.pages)
-            mine = place(p, page, j - pg * p.cache.page_size, sg.head);
-        else
-            atomicOr(p.watchdog, kv::kWatchIndex);
+    __device__ __forceinline__ void load(const Cache &c, int64_t code) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < kConvLoads<D>; ++i) {
+            int row, x;
+            conv_place<D>(lane, i, row, x);
+            const int64_t at = __shfl_sync(0xffffffffu, code, row);
+            k[i] = v[i] = make_uint4(0, 0, 0, 0);
+            if (at >= 0) {
+                k[i] = ld_stream(c.k + at + x * 16);
+                v[i] = ld_stream(c.v + at + x * 16);
+            }
+        }
     }
-    f.ok = __ballot_sync(0xffffffffu, mine.code >= 0) & 0xffffu;
-    f.past = j0 + kTileKeys > sg.s.ctx;
-    f.first = tile == t0;
-    f.code = mine.code;
-    f.sc = 0.f;
-    if (mine.code >= 0) f.sc = (lane < 16 ? p.cache.k_scale : p.cache.v_scale)[mine.scale];
-    load_codes<D>(p.cache.k, mine.code, f.k);
-}
+};
 
 // 16 codes to binary16 into a tile of an operand.
 template <int D, bool kE5M2>
@@ -365,9 +408,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             gemm::mbar_init(bar(B_KFULL + i), kConvWarps);
-            gemm::mbar_init(bar(B_KEMPTY + i), 1);
+            gemm::mbar_init(bar(B_KEMPTY + i), kTwo ? 2 : 1);
             gemm::mbar_init(bar(B_VFULL + i), kConvWarps);
-            gemm::mbar_init(bar(B_VEMPTY + i), 1);
+            gemm::mbar_init(bar(B_VEMPTY + i), kTwo ? 2 : 1);
             gemm::mbar_init(bar(B_SFULL + i), 1);
             gemm::mbar_init(bar(B_PFULL + i), 4);
             gemm::mbar_init(bar(B_ODONE + i), 1);
@@ -376,13 +419,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
         gemm::mbar_init(bar(B_QMAX), kTwo ? 8 : 4);
         gemm::mbar_init(bar(B_QREADY), kTwo ? 8 : 4);
         gemm::mbar_init(bar(B_MERGE), 4);
-        gemm::mbar_init(bar(B_DRAIN), 1);
+        gemm::mbar_init(bar(B_DRAIN), 2);
+        gemm::mbar_init(bar(B_QDONE), 1);
+        gemm::mbar_init(bar(B_NEXT), 4);
         gemm::fence_async_shared();
         sh_abort = 0;
         sh_nonfinite = 0;
         sh_amax[0] = sh_amax[1] = 0;
     }
-    if (warp == kSoftWarps + kConvWarps) {
+    if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&sh_tmem)),
                      "r"(512)
@@ -398,161 +443,151 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
     const Cursor cur = find_part<128>(p, kRows, kTileKeys, sh_part);
     Walk walk(p, kRows, cur);
 
-    if (warp >= kSoftWarps && warp < kSoftWarps + kConvWarps) {
+    if (warp >= kSoftWarps) {
         // ---------------- converters ----------------
         const int cw = warp - kSoftWarps;
-        // the stream of tiles over all segments: keys two ahead, values one
-        Fetch<D> f[2];
-        uint4 v[Fetch<D>::kLoads];
+        // The stream of tiles over all segments.  While tile n is converted,
+        // the codes of n + 1 and n + 2 are on their way and the pages of
+        // n + 3 are looked up.
         int tile = 0;
         bool more = walk.next();
         if (more) tile = walk.t0;
-        int segments = 0;  // begun by the tiles stored
-        auto fetch = [&](Fetch<D> &x) {
-            if (!more) return false;
-            fetch_tile<D>(p, walk.sg, tile, walk.t0, cw, x);
+        struct Ahead {
+            int j, head;
+            int page;    // -1: none, -2: behind the sequence
+            bool past, first, there;
+        } ah;
+        auto look_up = [&]() {  // begins the look-up of the stream's next tile
+            ah.there = more;
+            if (!more) return;
+            const Segment &sg = walk.sg;
+            ah.j = tile * kTileKeys + cw * 16 + (lane & 15);
+            ah.head = sg.head;
+            ah.past = (tile + 1) * kTileKeys > sg.s.ctx;
+            ah.first = tile == walk.t0;
+            ah.page = -2;
+            if (ah.j < sg.s.len) ah.page = max(-1, p.table[sg.b * p.table_stride + p.page_of(ah.j)]);
             if (++tile >= walk.t1) {
                 more = walk.next();
                 tile = walk.t0;
             }
+        };
+        auto found = [&](Look &x) {  // ends it
+            x.code = -1;
+            x.sc = 0.f;
+            if (!ah.there) return false;
+            x.past = ah.past;
+            x.first = ah.first;
+            if (ah.page >= 0 && ah.page < p.cache.pages) {
+                const KeyAt at = place(p, ah.page, p.offset_in_page(ah.j), ah.head);
+                x.code = at.code;
+                x.sc = (lane < 16 ? p.cache.k_scale : p.cache.v_scale)[at.scale];
+            } else if (ah.page != -2) {
+                atomicOr(p.watchdog, kv::kWatchIndex);
+            }
             return true;
         };
+        int segments = 0;  // begun by the tiles stored
+        int n = 0;         // tiles stored
         bool alive = true;
-        int n = 0;  // tiles stored
-        auto store = [&](Fetch<D> &x) {
+        auto store = [&](Codes<D> &c, const Look &now) {
             const int stage = n & 1;
             const uint32_t parity = ((n >> 1) & 1) ^ 1;
             TileInfo &ti = info[n & 3];
             const uint32_t kbase = sbase + S::kK + stage * S::kOperand;
             const uint32_t vbase = sbase + S::kV + stage * S::kOperand;
-            alive = alive && tile_wait(p, bar(B_KEMPTY + stage), parity, &sh_abort);
-            if (x.first) {
+            alive = tile_wait(p, bar(B_KEMPTY + stage), parity, &sh_abort);
+            if (now.first) {
                 // the scaling of this segment's queries goes into the key scales
                 alive = alive && tile_wait(p, bar(B_QREADY), segments & 1, &sh_abort);
                 ++segments;
             }
             alive = __all_sync(0xffffffffu, alive);
             if (!alive) return;
+#pragma unroll
+            for (int i = 0; i < kConvLoads<D>; ++i) {
+                int row, ch;
+                conv_place<D>(lane, i, row, ch);
+                store_codes<D, kE5M2>(kbase, cw * 16 + row, ch, c.k[i]);
+            }
             const float undo =
                 power_of_two(query_exponent(sh_amax[(segments - 1) & 1]) - 13) * p.scale_log2;
-            const float vabs = fabsf(x.sc);
+            const float vabs = fabsf(now.sc);
             const float vmax = warp_max(lane >= 16 && vabs < INFINITY ? vabs : 0.f);
-            if (lane < 16) ti.kk[cw * 16 + lane] = x.sc * undo;
-            else ti.vs[cw * 16 + lane - 16] = x.sc;
+            const uint32_t ok = __ballot_sync(0xffffffffu, now.code >= 0);
+            if (lane < 16) ti.kk[cw * 16 + lane] = now.sc * undo;
+            else ti.vs[cw * 16 + lane - 16] = now.sc;
             if (lane == 0) {
                 ti.vmax[cw] = vmax;
-                ti.ok[cw] = (uint16_t)x.ok;
+                ti.ok[cw] = (uint16_t)ok;
             }
-#pragma unroll
-            for (int i = 0; i < Fetch<D>::kLoads; ++i) {
-                int row, ch;
-                conv_place<D>(cw, lane, i, row, ch);
-                store_codes<D, kE5M2>(kbase, row, ch, x.k[i]);
-            }
-            gemm::fence_async_shared();
-            __syncwarp();
-            if (lane == 0) gemm::mbar_arrive(bar(B_KFULL + stage));
             // Behind the context a value may be hidden from some rows, and 0
             // times NaN or infinity would reach them: such elements become
             // zero here and are added at the end to the rows that see them.
-            if (x.past) {
+            if (now.past) {
                 bool any = false;
 #pragma unroll
-                for (int i = 0; i < Fetch<D>::kLoads; ++i) {
-                    const uint4 c = v[i];
-                    v[i] = make_uint4(finite_codes<kE5M2>(c.x), finite_codes<kE5M2>(c.y),
-                                      finite_codes<kE5M2>(c.z), finite_codes<kE5M2>(c.w));
-                    any |= c.x != v[i].x || c.y != v[i].y || c.z != v[i].z || c.w != v[i].w;
+                for (int i = 0; i < kConvLoads<D>; ++i) {
+                    const uint4 w = c.v[i];
+                    c.v[i] = make_uint4(finite_codes<kE5M2>(w.x), finite_codes<kE5M2>(w.y),
+                                        finite_codes<kE5M2>(w.z), finite_codes<kE5M2>(w.w));
+                    any |= w.x != c.v[i].x || w.y != c.v[i].y || w.z != c.v[i].z ||
+                           w.w != c.v[i].w;
                 }
                 if (any) sh_nonfinite = 1;
             }
+            gemm::fence_async_shared();
             __syncwarp();
-            if (lane == 0) gemm::mbar_arrive(bar(B_INFO + (n & 3)));
+            if (lane == 0) {
+                gemm::mbar_arrive(bar(B_KFULL + stage));
+                gemm::mbar_arrive(bar(B_INFO + (n & 3)));
+            }
             alive = tile_wait(p, bar(B_VEMPTY + stage), parity, &sh_abort);
             alive = __all_sync(0xffffffffu, alive);
             if (!alive) return;
 #pragma unroll
-            for (int i = 0; i < Fetch<D>::kLoads; ++i) {
+            for (int i = 0; i < kConvLoads<D>; ++i) {
                 int row, ch;
-                conv_place<D>(cw, lane, i, row, ch);
-                store_codes<D, kE5M2>(vbase, row, ch, v[i]);
+                conv_place<D>(lane, i, row, ch);
+                store_codes<D, kE5M2>(vbase, cw * 16 + row, ch, c.v[i]);
             }
             gemm::fence_async_shared();
             __syncwarp();
             if (lane == 0) gemm::mbar_arrive(bar(B_VFULL + stage));
             ++n;
         };
-        bool h0 = fetch(f[0]), h1 = fetch(f[1]);
-        if (h0) load_codes<D>(p.cache.v, f[0].code, v);
-        while (alive && h0) {
-            store(f[0]);
-            if (h1) load_codes<D>(p.cache.v, f[1].code, v);
-            h0 = fetch(f[0]);
-            if (!h1 || !alive) break;
-            store(f[1]);
-            if (h0) load_codes<D>(p.cache.v, f[0].code, v);
-            h1 = fetch(f[1]);
+        // looks of tiles n, n + 1 and n + 2; codes of n and n + 1
+        Codes<D> c0, c1;
+        Look l0, l1, l2;
+        look_up();
+        bool h0 = found(l0);
+        look_up();
+        c0.load(p.cache, l0.code);
+        bool h1 = found(l1);
+        look_up();
+        c1.load(p.cache, l1.code);
+        bool h2 = found(l2);
+        while (h0) {
+            look_up();
+            store(c0, l0);
+            if (!alive) break;
+            c0.load(p.cache, l2.code);
+            l0 = l1;
+            h0 = h1;
+            l1 = l2;
+            h1 = h2;
+            h2 = found(l2);
+            if (!h0) break;
+            look_up();
+            store(c1, l0);
+            if (!alive) break;
+            c1.load(p.cache, l2.code);
+            l0 = l1;
+            h0 = h1;
+            l1 = l2;
+            h1 = h2;
+            h2 = found(l2);
         }
-    } else if (warp == kSoftWarps + kConvWarps) {
-        // ---------------- products ----------------
-        if (lane == 0) {
-            int n = 0;            // tiles of finished segments
-            int items[2] = {0, 0};  // of each pipeline, in all
-            int segment = 0;
-            bool alive = true;
-            while (alive && walk.next()) {
-                const int T = walk.t1 - walk.t0, U = kTwo ? 2 * T : T;
-                alive = tile_wait(p, bar(B_QREADY), segment & 1, &sh_abort);
-                auto scores = [&](int u) {
-                    const int t = kTwo ? u >> 1 : u, i = u & 1, stage = (n + t) & 1;
-                    if (!kTwo || i == 0)
-                        alive = alive && tile_wait(p, bar(B_KFULL + stage), ((n + t) >> 1) & 1,
-                                                   &sh_abort);
-                    if (!alive) return;
-                    gemm::tmem_fence_after();
-                    const uint32_t qb = sbase + S::kQ + (kTwo ? i * S::kOperand : 0);
-                    const uint32_t kb = sbase + S::kK + stage * S::kOperand;
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (k >> 2) * (kTileKeys * 128) + (k & 3) * 32;
-                        gemm::mma_f16(tmem + i * 128, gemm::smem_desc(qb + off, 128),
-                                      gemm::smem_desc(kb + off, 128),
-                                      tile_desc<kTileKeys, false>(), k > 0);
-                    }
-                    gemm::mma_commit(bar(B_SFULL + i));
-                    if (!kTwo || i == 1) gemm::mma_commit(bar(B_KEMPTY + stage));
-                };
-                for (int u = 0; u < 2 && u < U; ++u) scores(u);
-                for (int u = 0; alive && u < U; ++u) {
-                    const int t = kTwo ? u >> 1 : u, i = u & 1, stage = (n + t) & 1;
-                    alive = tile_wait(p, bar(B_PFULL + i), items[i] & 1, &sh_abort);
-                    if (!kTwo || i == 0)
-                        alive = alive && tile_wait(p, bar(B_VFULL + stage), ((n + t) >> 1) & 1,
-                                                   &sh_abort);
-                    if (!alive) break;
-                    ++items[i];
-                    gemm::tmem_fence_after();
-                    const uint32_t vb = sbase + S::kV + stage * S::kOperand;
-                    const bool started = kTwo ? t > 0 : u > 1;
-#pragma unroll
-                    for (int k = 0; k < kTileKeys / 16; ++k)
-                        mma_f16_ts(tmem + kTmemO + i * 128, tmem + i * 128 + 8 * k,
-                                   value_desc(vb + k * 2048), tile_desc<D, true>(),
-                                   started || k > 0);
-                    if (!kTwo || i == 1) gemm::mma_commit(bar(B_VEMPTY + stage));
-                    if (u + 2 >= U) gemm::mma_commit(bar(B_ODONE + i));
-                    if (u + 2 < U) scores(u + 2);
-                }
-                n += T;
-                ++segment;
-            }
-            // nothing may be in flight when the tensor memory goes
-            gemm::mma_commit(bar(B_DRAIN));
-            const unsigned long long t0 = gemm::now_ns();
-            while (!gemm::mbar_try_wait(bar(B_DRAIN), 0))
-                if (gemm::now_ns() - t0 > kWaitLimitNs) break;
-        }
-        __syncwarp();
     } else {
         // ---------------- softmax ----------------
         const int pipe = warp >> 2;
@@ -562,6 +597,40 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
         int n = 0;                            // tiles of finished segments
         int items = 0, segment = 0, merges = 0, rounds = 0;
         bool alive = true;
+        // The pipeline's products, issued by one thread: item t of a segment
+        // that began at tile n is key tile n + t.
+        const bool issuer = (threadIdx.x & 127) == 0;
+        auto scores = [&](int t, bool last) {
+            const int stage = (n + t) & 1;
+            if (!tile_wait(p, bar(B_KFULL + stage), ((n + t) >> 1) & 1, &sh_abort)) return false;
+            gemm::tmem_fence_after();
+            const uint32_t qb = sbase + S::kQ + (kTwo ? pipe * S::kOperand : 0);
+            const uint32_t kb = sbase + S::kK + stage * S::kOperand;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k >> 2) * (kTileKeys * 128) + (k & 3) * 32;
+                gemm::mma_f16(tmem + pipe * 128, gemm::smem_desc(qb + off, 128),
+                              gemm::smem_desc(kb + off, 128), tile_desc<kTileKeys, false>(),
+                              k > 0);
+            }
+            gemm::mma_commit(bar(B_SFULL + pipe));
+            gemm::mma_commit(bar(B_KEMPTY + stage));
+            if (!kTwo && last && pipe == 0) gemm::mma_commit(bar(B_QDONE));
+            return true;
+        };
+        auto products = [&](int t, bool started, bool last) {
+            const int stage = (n + t) & 1;
+            if (!tile_wait(p, bar(B_VFULL + stage), ((n + t) >> 1) & 1, &sh_abort)) return false;
+            gemm::tmem_fence_after();
+            const uint32_t vb = sbase + S::kV + stage * S::kOperand;
+#pragma unroll
+            for (int k = 0; k < kTileKeys / 16; ++k)
+                mma_f16_ts(tmem + kTmemO + pipe * 128, tmem + pipe * 128 + 8 * k,
+                           value_desc(vb + k * 2048), tile_desc<D, true>(), started || k > 0);
+            gemm::mma_commit(bar(B_VEMPTY + stage));
+            if (last) gemm::mma_commit(bar(B_ODONE + pipe));
+            return true;
+        };
         auto wait = [&](int b, int parity) {
             alive = tile_wait(p, bar(b), parity & 1, &sh_abort);
             alive = __all_sync(0xffffffffu, alive);
@@ -627,16 +696,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
             int k = 100;
             float off = -100.f;
             int done = 0;  // items of this segment
-            for (int t = kTwo ? 0 : pipe; t < T; t += kTwo ? 1 : 2) {
+            constexpr int kEach = kTwo ? 1 : 2;
+            const int t_first = kTwo ? 0 : pipe;
+            if (t_first < T) {
+                if (issuer)
+                    alive = tile_wait(p, bar(B_QREADY), segment & 1, &sh_abort) &&
+                            scores(t_first, t_first + kEach >= T);
+                alive = __all_sync(0xffffffffu, alive);
+                if (!alive) break;
+            }
+            for (int t = t_first; t < T; t += kEach) {
                 if (!wait(B_SFULL + pipe, items)) break;
                 if (!wait(B_INFO + ((n + t) & 3), (n + t) >> 2)) break;
                 gemm::tmem_fence_after();
                 const TileInfo &ti = info[(n + t) & 3];
                 const int j0 = (walk.t0 + t) * kTileKeys;
-                const float4 va = *reinterpret_cast<const float4 *>(ti.vmax),
-                             vb = *reinterpret_cast<const float4 *>(ti.vmax + 4);
-                const float vm = fmaxf(fmaxf(fmaxf(va.x, va.y), fmaxf(va.z, va.w)),
-                                       fmaxf(fmaxf(vb.x, vb.y), fmaxf(vb.z, vb.w)));
+                const float4 va = *reinterpret_cast<const float4 *>(ti.vmax);
+                const float vm = fmaxf(fmaxf(va.x, va.y), fmaxf(va.z, va.w));
                 const uint4 okw = *reinterpret_cast<const uint4 *>(ti.ok);
                 uint32_t vis[4] = {okw.x, okw.y, okw.z, okw.w};
                 const bool edge = (okw.x & okw.y & okw.z & okw.w) != 0xffffffffu ||
@@ -651,25 +727,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
                     }
                 }
                 // the row's largest score
-                float top = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float s[32];
-                    gemm::tmem_ld32(ts + 32 * c, s);
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 kk = *reinterpret_cast<const float4 *>(ti.kk + 32 * c + j);
-                        float a0 = s[j] * kk.x, a1 = s[j + 1] * kk.y, a2 = s[j + 2] * kk.z,
-                              a3 = s[j + 3] * kk.w;
-                        if (edge) {
-                            if (!((vis[c] >> j) & 1u)) a0 = -INFINITY;
-                            if (!((vis[c] >> (j + 1)) & 1u)) a1 = -INFINITY;
-                            if (!((vis[c] >> (j + 2)) & 1u)) a2 = -INFINITY;
-                            if (!((vis[c] >> (j + 3)) & 1u)) a3 = -INFINITY;
-                        }
-                        top = fmaxf(top, fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)));
-                    }
-                }
+                const float top = edge ? row_top<true>(ts, ti, vis) : row_top<false>(ts, ti, vis);
                 const bool lower = vm > 0.f && vm * power_of_two(k) > kWeightScale;  // uniform
                 if (__any_sync(0xffffffffu, lower || top > m + kSlack)) {
                     if (lower) k = min(k, 11 - (int)((__float_as_uint(vm) >> 23) & 0xff) + 127);
@@ -684,48 +742,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
                         for (int c = 0; c < D / 32; ++c) tmem_scale32(to + 32 * c, by);
                     }
                 }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float s[32];
-                    gemm::tmem_ld32(ts + 32 * c, s);
-                    uint32_t w[16];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 kk = *reinterpret_cast<const float4 *>(ti.kk + 32 * c + j);
-                        const float4 vs = *reinterpret_cast<const float4 *>(ti.vs + 32 * c + j);
-                        float q0 = fmaf(s[j], kk.x, -off), q1 = fmaf(s[j + 1], kk.y, -off),
-                              q2 = fmaf(s[j + 2], kk.z, -off), q3 = fmaf(s[j + 3], kk.w, -off);
-                        const uint32_t v4 = edge ? vis[c] >> j : 0xfu;
-                        if (edge) {
-                            if (!(v4 & 1u)) q0 = -INFINITY;
-                            if (!(v4 & 2u)) q1 = -INFINITY;
-                            if (!(v4 & 4u)) q2 = -INFINITY;
-                            if (!(v4 & 8u)) q3 = -INFINITY;
-                        }
-                        q0 = exp2_fast(q0);
-                        q1 = exp2_fast(q1);
-                        q2 = exp2_fast(q2);
-                        q3 = exp2_fast(q3);
-                        l += (q0 + q1) + (q2 + q3);
-                        q0 *= vs.x;
-                        q1 *= vs.y;
-                        q2 *= vs.z;
-                        q3 *= vs.w;
-                        if (edge) {
-                            if (!(v4 & 1u)) q0 = 0.f;
-                            if (!(v4 & 2u)) q1 = 0.f;
-                            if (!(v4 & 4u)) q2 = 0.f;
-                            if (!(v4 & 8u)) q3 = 0.f;
-                        }
-                        w[j / 2] = pack_h2(q0, q1);
-                        w[j / 2 + 1] = pack_h2(q2, q3);
-                    }
-                    tmem_st16(ts + 16 * c, w);
-                }
+                l += edge ? row_weights<true>(ts, ti, vis, off)
+                          : row_weights<false>(ts, ti, vis, off);
                 tmem_st_wait();
                 gemm::tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) gemm::mbar_arrive(bar(B_PFULL + pipe));
+                if (issuer) {
+                    alive = tile_wait(p, bar(B_PFULL + pipe), items & 1, &sh_abort) &&
+                            products(t, done > 0, t + kEach >= T);
+                    if (alive && t + kEach < T) alive = scores(t + kEach, t + 2 * kEach >= T);
+                }
+                alive = __all_sync(0xffffffffu, alive);
+                if (!alive) break;
                 ++items;
                 ++done;
             }
@@ -739,8 +768,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
             float *buf = reinterpret_cast<float *>(smem + S::kQ);  // [column][row]
             const bool joined = !kTwo && T > 1;
             if (joined && pipe == 1) {
-                // this pipeline's state, over the queries (every product of
-                // the segment is done)
+                // this pipeline's state, over the queries once the other
+                // pipeline's last scores are done as well
+                if (!wait(B_QDONE, segment)) break;
                 sh_ml[r] = make_float2(l, off);
                 sh_m[r] = m;
 #pragma unroll 1
@@ -812,13 +842,32 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
                              (int)sg.row0, sg.s.n, sg.head, sg.block, 0, 0};
             }
             gemm::tmem_fence_before();  // O is read before the next segment's products
+            if (!kTwo) {
+                // The pipelines begin a segment together: one that skipped
+                // segments of a single tile could take an old phase of a
+                // barrier for its own.
+                __syncwarp();
+                if (pipe == 0) {
+                    if (lane == 0) gemm::mbar_arrive(bar(B_NEXT));
+                } else if (!wait(B_NEXT, segment)) {
+                    break;
+                }
+            }
             n += T;
             ++segment;
         }
+        // nothing may be in flight when the tensor memory goes
+        if (issuer) {
+            gemm::mma_commit(bar(B_DRAIN));
+            const unsigned long long t0 = gemm::now_ns();
+            while (!gemm::mbar_try_wait(bar(B_DRAIN), 0))
+                if (gemm::now_ns() - t0 > kWaitLimitNs) break;
+        }
+        __syncwarp();
     }
     gemm::tmem_fence_before();
     __syncthreads();
-    if (warp == kSoftWarps + kConvWarps)
+    if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                      : "memory");
 }

@@ -133,6 +133,14 @@ CASES = {
                  Hk=2, D=64),
     "long": dict(ctx=[9000], new=[4], Hq=4, Hk=2, D=64),
     "group of 64": dict(ctx=[210], new=[3], Hq=64, Hk=1, D=64),
+    # segments of one tile among segments of several, several to a CTA
+    "short and long": dict(ctx=[(37 * i) % 390 for i in range(250)],
+                           new=[9 + i % 4 for i in range(250)], Hq=4, Hk=2, D=64),
+    "256 rows": dict(ctx=[700, 10, 0, 129], new=[40, 33, 64, 1], Hq=16, Hk=2, D=128),
+    "more than 256 rows": dict(ctx=[260], new=[90], Hq=8, Hk=1, D=64, fmt="e5m2"),
+    "spread scales, many rows": dict(ctx=[600], new=[20], Hq=8, Hk=2, D=128, spread=4.0),
+    "sharp, many rows": dict(ctx=[900], new=[40], Hq=16, Hk=2, D=128, gain=6.0, mode="tensor"),
+    "f16, many rows": dict(ctx=[300, 44], new=[30, 17], Hq=8, Hk=4, D=128, dt="f16", page=24),
     "group of 3": dict(ctx=[45, 600], new=[11, 23], Hq=9, Hk=3, D=192, dt="f16"),
 }
 
