@@ -254,27 +254,100 @@ __device__ __forceinline__ void add_nonfinite(const Params &p, const Segment &sg
     }
 }
 
+// 16 columns of tensor memory on their way to registers, and their arrival.
+__device__ __forceinline__ void tmem_ld16_begin(uint32_t taddr, float (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+          "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]),
+          "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld16_end(float (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]),
+                   "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]),
+                   "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+}
+
+// Two binary32 values in one 64-bit register, and packed arithmetic on them.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float2 apart(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // A row's largest score of a tile: columns of S at `ts` times the keys'
 // factors.  kEdge: only where bits of vis are set.
 template <bool kEdge>
 __device__ __forceinline__ float row_top(uint32_t ts, const TileInfo &ti,
                                          const uint32_t (&vis)[4]) {
-    float top = -INFINITY;
+    float t0 = -INFINITY, t1 = -INFINITY;
+    float buf[2][16];
+    tmem_ld16_begin(ts, buf[0]);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        float s[32];
-        gemm::tmem_ld32(ts + 32 * c, s);
+    for (int c = 0; c < 8; ++c) {
+        float(&s)[16] = buf[c & 1];
+        tmem_ld16_end(s);
+        if (c < 7) tmem_ld16_begin(ts + 16 * (c + 1), buf[(c + 1) & 1]);
+        const uint32_t v16 = kEdge ? vis[c >> 1] >> (16 * (c & 1)) : 0u;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            const float4 kk = *reinterpret_cast<const float4 *>(ti.kk + 32 * c + j);
-            float a[4] = {s[j] * kk.x, s[j + 1] * kk.y, s[j + 2] * kk.z, s[j + 3] * kk.w};
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (kEdge && !((vis[c] >> (j + u)) & 1u)) a[u] = -INFINITY;
-            top = fmaxf(top, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])));
+        for (int j = 0; j < 16; j += 4) {
+            const ulonglong2 kk = *reinterpret_cast<const ulonglong2 *>(ti.kk + 16 * c + j);
+            float2 a = apart(mul2(two(s[j], s[j + 1]), kk.x));
+            float2 b = apart(mul2(two(s[j + 2], s[j + 3]), kk.y));
+            if (kEdge) {
+                if (!((v16 >> j) & 1u)) a.x = -INFINITY;
+                if (!((v16 >> (j + 1)) & 1u)) a.y = -INFINITY;
+                if (!((v16 >> (j + 2)) & 1u)) b.x = -INFINITY;
+                if (!((v16 >> (j + 3)) & 1u)) b.y = -INFINITY;
+            }
+            t0 = max3(t0, a.x, a.y);
+            t1 = max3(t1, b.x, b.y);
         }
     }
-    return top;
+    return fmaxf(t0, t1);
 }
 
 // A row's weights of a tile, 2^(score - off) times the value scales, in
@@ -282,34 +355,49 @@ __device__ __forceinline__ float row_top(uint32_t ts, const TileInfo &ti,
 template <bool kEdge>
 __device__ __forceinline__ float row_weights(uint32_t ts, const TileInfo &ti,
                                              const uint32_t (&vis)[4], float off) {
-    float l = 0.f;
+    uint64_t l0 = two(0.f, 0.f), l1 = l0;
+    const uint64_t shift = two(-off, -off);
+    float buf[2][16];
+    tmem_ld16_begin(ts, buf[0]);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        float s[32];
-        gemm::tmem_ld32(ts + 32 * c, s);
-        uint32_t w[16];
+    for (int c = 0; c < 8; ++c) {
+        float(&s)[16] = buf[c & 1];
+        tmem_ld16_end(s);
+        if (c < 7) tmem_ld16_begin(ts + 16 * (c + 1), buf[(c + 1) & 1]);
+        const uint32_t v16 = kEdge ? vis[c >> 1] >> (16 * (c & 1)) : 0u;
+        uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            const float4 kk = *reinterpret_cast<const float4 *>(ti.kk + 32 * c + j);
-            const float4 vs = *reinterpret_cast<const float4 *>(ti.vs + 32 * c + j);
-            const float k4[4] = {kk.x, kk.y, kk.z, kk.w}, v4[4] = {vs.x, vs.y, vs.z, vs.w};
-            float q[4], x[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const bool hid = kEdge && !((vis[c] >> (j + u)) & 1u);
-                q[u] = fmaf(s[j + u], k4[u], -off);
-                if (hid) q[u] = -INFINITY;
-                q[u] = exp2_fast(q[u]);
-                x[u] = q[u] * v4[u];
-                if (hid) x[u] = 0.f;
+        for (int j = 0; j < 16; j += 4) {
+            const ulonglong2 kk = *reinterpret_cast<const ulonglong2 *>(ti.kk + 16 * c + j);
+            const ulonglong2 vs = *reinterpret_cast<const ulonglong2 *>(ti.vs + 16 * c + j);
+            float2 a = apart(fma2(two(s[j], s[j + 1]), kk.x, shift));
+            float2 b = apart(fma2(two(s[j + 2], s[j + 3]), kk.y, shift));
+            const uint32_t v4 = v16 >> j;
+            if (kEdge) {
+                if (!(v4 & 1u)) a.x = -INFINITY;
+                if (!(v4 & 2u)) a.y = -INFINITY;
+                if (!(v4 & 4u)) b.x = -INFINITY;
+                if (!(v4 & 8u)) b.y = -INFINITY;
             }
-            l += (q[0] + q[1]) + (q[2] + q[3]);
-            w[j / 2] = pack_h2(x[0], x[1]);
-            w[j / 2 + 1] = pack_h2(x[2], x[3]);
+            const uint64_t pa = two(exp2_fast(a.x), exp2_fast(a.y));
+            const uint64_t pb = two(exp2_fast(b.x), exp2_fast(b.y));
+            l0 = add2(l0, pa);
+            l1 = add2(l1, pb);
+            a = apart(mul2(pa, vs.x));
+            b = apart(mul2(pb, vs.y));
+            if (kEdge) {
+                if (!(v4 & 1u)) a.x = 0.f;
+                if (!(v4 & 2u)) a.y = 0.f;
+                if (!(v4 & 4u)) b.x = 0.f;
+                if (!(v4 & 8u)) b.y = 0.f;
+            }
+            w[j / 2] = pack_h2(a.x, a.y);
+            w[j / 2 + 1] = pack_h2(b.x, b.y);
         }
-        tmem_st16(ts + 16 * c, w);
+        tmem_st8(ts + 8 * c, w);  // behind every load that is under way
     }
-    return l;
+    const float2 x = apart(add2(l0, l1));
+    return x.x + x.y;
 }
 
 // The k of an offset m - k.
@@ -347,6 +435,14 @@ __device__ __forceinline__ void conv_place(int lane, int i, int &row, int &x) {
     }
 }
 
+__device__ __forceinline__ uint4 ld_past_l1(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 // A converter thread's share of a tile's codes.
 template <int D>
 struct Codes {
@@ -361,8 +457,8 @@ struct Codes {
             const int64_t at = __shfl_sync(0xffffffffu, code, row);
             k[i] = v[i] = make_uint4(0, 0, 0, 0);
             if (at >= 0) {
-                k[i] = ld_stream(c.k + at + x * 16);
-                v[i] = ld_stream(c.v + at + x * 16);
+                k[i] = ld_past_l1(c.k + at + x * 16);
+                v[i] = ld_past_l1(c.v + at + x * 16);
             }
         }
     }
@@ -642,31 +738,41 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
             const int R = sg.block * kRows + (kTwo ? pipe * kTileRows : 0) + r;
             const int tok = R / p.G, hq = sg.head * p.G + (R - tok * p.G);
             const bool live = tok < sg.s.n;
+            const bool warp_live = __any_sync(0xffffffffu, live);
             if (kTwo || pipe == 0) {
                 // Q in binary16, scaled by one power of two for the block: a
-                // row that is not finite is left out of that and becomes NaN
-                const uint16_t *src = static_cast<const uint16_t *>(p.q.data) +
-                                      (sg.row0 + tok) * p.q.ts + (int64_t)hq * p.q.hs;
-                auto q8 = [&](int e, float (&x)[8]) {
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (live) w = ld_stream(src + e);
-                    if (p.bf16) DT<__nv_bfloat16>::unpack(w, x);
-                    else DT<__half>::unpack(w, x);
-                };
-                float amax = 0.f;
-                bool finite = true;
-#pragma unroll 4
-                for (int e = 0; e < D; e += 8) {
-                    float x[8];
-                    q8(e, x);
+                // row that is not finite is left out of that and becomes NaN.
+                // D / 8 lanes read a row, all of the warp's 32 at once.
+                constexpr int kLanes = D / 8, kSide = 32 / kLanes, kN = 32 / kSide;
+                const uint16_t *src = static_cast<const uint16_t *>(p.q.data);
+                const int64_t own =
+                    live ? (sg.row0 + tok) * p.q.ts + (int64_t)hq * p.q.hs : -1;
+                const int chunk = lane % kLanes, side = lane / kLanes;
+                uint4 w[kN];
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        amax = fmaxf(amax, fabsf(x[u]));
-                        finite = finite && fabsf(x[u]) < INFINITY;
-                    }
+                for (int i = 0; i < kN; ++i) {
+                    const int64_t at = __shfl_sync(0xffffffffu, own, i * kSide + side);
+                    w[i] = make_uint4(0, 0, 0, 0);
+                    if (at >= 0) w[i] = ld_past_l1(src + at + chunk * 8);
                 }
-                amax = warp_max(finite ? amax : 0.f);
+                // magnitudes as the integers they sort as
+                const uint32_t inf = p.bf16 ? 0x7f80u : 0x7c00u;
+                uint32_t most = 0, bad = 0;  // bad: this lane's rows that are not finite, by i
+#pragma unroll
+                for (int i = 0; i < kN; ++i) {
+                    const uint32_t m2 =
+                        __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                 __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+                    const uint32_t m1 = max(m2 & 0xffffu, m2 >> 16);
+                    const uint32_t group = (kLanes == 32 ? 0xffffffffu : (1u << (kLanes & 31)) - 1u)
+                                           << (side * kLanes);
+                    if (__ballot_sync(0xffffffffu, m1 >= inf) & group) bad |= 1u << i;
+                    else most = max(most, m1);
+                }
+                most = __reduce_max_sync(0xffffffffu, most);
                 if (lane == 0) {
+                    const float amax = p.bf16 ? __uint_as_float(most << 16)
+                                              : DT<__half>::w2f(most).x;
                     atomicMax(&sh_amax[segment & 1], __float_as_uint(amax));
                     gemm::mbar_arrive(bar(B_QMAX));
                 }
@@ -674,15 +780,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
                 const float by = power_of_two(13 - query_exponent(sh_amax[segment & 1]));
                 if (threadIdx.x == 0) sh_amax[(segment + 1) & 1] = 0;
                 const uint32_t qb = sbase + S::kQ + (kTwo ? pipe * S::kOperand : 0);
-#pragma unroll 4
-                for (int e = 0; e < D; e += 8) {
+#pragma unroll
+                for (int i = 0; i < kN; ++i) {
                     float x[8];
-                    q8(e, x);
-                    uint4 w = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-                    if (finite)
-                        w = make_uint4(pack_h2(x[0] * by, x[1] * by), pack_h2(x[2] * by, x[3] * by),
+                    if (p.bf16) DT<__nv_bfloat16>::unpack(w[i], x);
+                    else DT<__half>::unpack(w[i], x);
+                    uint4 h = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+                    if (!((bad >> i) & 1u))
+                        h = make_uint4(pack_h2(x[0] * by, x[1] * by), pack_h2(x[2] * by, x[3] * by),
                                        pack_h2(x[4] * by, x[5] * by), pack_h2(x[6] * by, x[7] * by));
-                    gemm::sts128(qb + operand_at<D>(r, e >> 6, (e & 63) >> 3), w);
+                    gemm::sts128(qb + operand_at<D>((warp & 3) * 32 + i * kSide + side, chunk >> 3,
+                                                    chunk & 7),
+                                 h);
                 }
                 gemm::fence_async_shared();
                 __syncwarp();
@@ -726,24 +835,28 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
                         vis[w] &= see;
                     }
                 }
-                // the row's largest score
-                const float top = edge ? row_top<true>(ts, ti, vis) : row_top<false>(ts, ti, vis);
-                const bool lower = vm > 0.f && vm * power_of_two(k) > kWeightScale;  // uniform
-                if (__any_sync(0xffffffffu, lower || top > m + kSlack)) {
-                    if (lower) k = min(k, 11 - (int)((__float_as_uint(vm) >> 23) & 0xff) + 127);
-                    const float m1 = fmaxf(m, top);
-                    const float off1 = (m1 == -INFINITY ? 0.f : m1) - (float)k;
-                    const float by = m == -INFINITY ? 1.f : exp2_fast(off - off1);
-                    m = m1;
-                    off = off1;
-                    l *= by;
-                    if (done) {
+                // a warp without rows leaves its weights as they are: they
+                // reach no other row
+                if (warp_live) {
+                    // the row's largest score
+                    const float top = edge ? row_top<true>(ts, ti, vis) : row_top<false>(ts, ti, vis);
+                    const bool lower = vm > 0.f && vm * power_of_two(k) > kWeightScale;  // uniform
+                    if (__any_sync(0xffffffffu, lower || top > m + kSlack)) {
+                        if (lower) k = min(k, 11 - (int)((__float_as_uint(vm) >> 23) & 0xff) + 127);
+                        const float m1 = fmaxf(m, top);
+                        const float off1 = (m1 == -INFINITY ? 0.f : m1) - (float)k;
+                        const float by = m == -INFINITY ? 1.f : exp2_fast(off - off1);
+                        m = m1;
+                        off = off1;
+                        l *= by;
+                        if (done) {
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) tmem_scale32(to + 32 * c, by);
+                            for (int c = 0; c < D / 32; ++c) tmem_scale32(to + 32 * c, by);
+                        }
                     }
+                    l += edge ? row_weights<true>(ts, ti, vis, off)
+                              : row_weights<false>(ts, ti, vis, off);
                 }
-                l += edge ? row_weights<true>(ts, ti, vis, off)
-                          : row_weights<false>(ts, ti, vis, off);
                 tmem_st_wait();
                 gemm::tmem_fence_before();
                 __syncwarp();
