@@ -1,6 +1,7 @@
 // kv_api.cu -- the C ABI's attention side: per-head norm and rotation, the
 // 8-bit key / value cache, attention of drafted tokens over it.  Argument
 // checks come before anything is enqueued; no memory is allocated.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <utility>
@@ -484,8 +485,9 @@ int64_t rarn_tree_attention_workspace_bytes(int64_t tokens, int64_t B, int64_t q
         tokens >= kMaxItems / q_heads)
         return -1;
     if (tokens == 0 || B == 0) return 0;
-    const tree::Plan pl = tree::plan(tokens, B, q_heads, kv_heads, D);
-    return pl.segments < kMaxItems ? pl.bytes : -1;
+    const tree::Plan a = tree::plan(tokens, B, q_heads, kv_heads, D, false),
+                     b = tree::plan(tokens, B, q_heads, kv_heads, D, true);
+    return a.segments < kMaxItems ? std::max(a.bytes, b.bytes) : -1;
 }
 
 rarn_status rarn_tree_attention(rarn_heads out, rarn_heads q, const rarn_kv_cache *cache,
@@ -512,9 +514,12 @@ rarn_status rarn_tree_attention(rarn_heads out, rarn_heads q, const rarn_kv_cach
     if (!context_lens || !starts || !on(context_lens, 4) || !on(starts, 4))
         return RARN_ERR_INVALID_ARG;
     if (tokens >= kMaxItems / q.heads || !packs_ok(q)) return RARN_ERR_UNSUPPORTED;
-    const tree::Plan pl = tree::plan(tokens, B, q.heads, cache->heads, D);
+    const tree::Plan pl =
+        tree::plan(tokens, B, q.heads, cache->heads, D, cache->page_size % tree::kBoxSlots == 0);
     if (pl.segments >= kMaxItems) return RARN_ERR_UNSUPPORTED;
-    if (!workspace || !on(workspace, 32) || (int64_t)workspace_bytes < pl.bytes)
+    if (!workspace || !on(workspace, 32) ||
+        (int64_t)workspace_bytes <
+            rarn_tree_attention_workspace_bytes(tokens, B, q.heads, cache->heads, D))
         return RARN_ERR_INVALID_ARG;
     const Range outs[2] = {range_of(out, tokens, D), solid(workspace, pl.bytes)};
     const Range ins[8] = {range_of(q, tokens, D), cr.k, cr.v, cr.ks, cr.vs,

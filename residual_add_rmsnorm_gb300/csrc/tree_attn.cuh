@@ -197,11 +197,11 @@ __device__ __forceinline__ Cursor find_part(const Params &p, int rows, int tile,
     return c;
 }
 
-// The CTA whose part holds tile `t` of the line.
-__device__ __forceinline__ int part_of(const Cursor &c, int t) {
-    const int edge = c.more * (c.each + 1);
-    return t < edge ? (unsigned)t / (unsigned)(c.each + 1)
-                    : c.more + (unsigned)(t - edge) / (unsigned)c.each;
+// The CTA whose part holds tile `t` of the line (Cursor's each and more).
+__device__ __forceinline__ int part_of(int each, int more, int t) {
+    const int edge = more * (each + 1);
+    return t < edge ? (unsigned)t / (unsigned)(each + 1)
+                    : more + (unsigned)(t - edge) / (unsigned)each;
 }
 
 // A key's place in the cache: code and scale offsets of (its page, its slot),
@@ -1037,7 +1037,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D <= 128 ? 4 : 2)
         }
         if (t0 == 0 && threadIdx.x == 0)
             p.joins[seg0 + which] =
-                Join{(int)blockIdx.x, whole ? -1 : part_of(cur, at + sg.s.tiles - 1),
+                Join{(int)blockIdx.x, whole ? -1 : part_of(cur.each, cur.more, at + sg.s.tiles - 1),
                      (int)sg.row0, sg.s.n, sg.head, sg.block, 0, 0};
         at += t1 - t0;
         gemm::fence_async_shared();  // the join's accesses before the next copies

@@ -43,9 +43,9 @@ inline cudaError_t launch_join(const Params &p, int rows, bool many, bool pdl, c
 }
 
 // The codes of one tensor as a 4-D tensor [pages][heads][slots][D], boxes of
-// kStep slots by at most 128 bytes, stored in StepLayout's order.
+// `slots` slots by at most 128 bytes, stored in StepLayout's order.
 template <int D>
-inline bool encode_codes(CUtensorMap *map, const void *base, const Cache &c) {
+inline bool encode_codes(CUtensorMap *map, const void *base, const Cache &c, int slots) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     using L = StepLayout<D>;
@@ -55,7 +55,7 @@ inline bool encode_codes(CUtensorMap *map, const void *base, const Cache &c) {
     auto stride = [](int64_t s, int64_t n) { return (cuuint64_t)(n > 1 ? s : 16); };
     const cuuint64_t strides[3] = {stride(c.slot_stride, c.page_size),
                                    stride(c.head_stride, c.heads), stride(c.page_stride, c.pages)};
-    const cuuint32_t box[4] = {(cuuint32_t)L::kHalf, (cuuint32_t)kStep, 1, 1};
+    const cuuint32_t box[4] = {(cuuint32_t)L::kHalf, (cuuint32_t)slots, 1, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -74,8 +74,8 @@ inline cudaError_t launch_rows(const Params &p, const Plan &pl, int num_sms, boo
     static std::atomic<int> known[64];
     auto kernel = k_tree_rows<D, NQ, NP, kE5M2, kStages, kTma>;
     CUtensorMap km{}, vm{};
-    if (kTma && !(encode_codes<D>(&km, p.cache.k, p.cache) &&
-                  encode_codes<D>(&vm, p.cache.v, p.cache)))
+    if (kTma && !(encode_codes<D>(&km, p.cache.k, p.cache, kStep) &&
+                  encode_codes<D>(&vm, p.cache.v, p.cache, kStep)))
         return cudaErrorInvalidValue;
     int ctas = 0;
     cudaError_t e = resident(kernel, kThreads, S::kBytes, num_sms, kMaxCtas, known, &ctas);
@@ -111,30 +111,40 @@ inline cudaError_t launch_type(const Params &p, const Plan &pl, int num_sms, boo
     return launch_copies<D, kE5M2, false>(p, pl, num_sms, pdl, st);
 }
 
-template <int D, bool kE5M2, bool kTwo>
+template <int D, int NP, bool kE5M2, bool kTwo>
 inline cudaError_t launch_tiles(const Params &p, const Plan &pl, int num_sms, bool pdl,
                                 cudaStream_t st) {
     static std::atomic<int> known[64];
-    auto kernel = k_tree_tile<D, kE5M2, kTwo>;
-    constexpr int smem = TileSmem<D>::kBytes;
+    auto kernel = k_tree_tile<D, NP, kE5M2, kTwo>;
+    constexpr int smem = TileSmem<D, NP, kTwo>::kBytes;
+    CUtensorMap km{}, vm{};
+    if (!encode_codes<D>(&km, p.cache.k, p.cache, kBox) ||
+        !encode_codes<D>(&vm, p.cache.v, p.cache, kBox))
+        return cudaErrorInvalidValue;
     int ctas = 0;
     cudaError_t e = resident(kernel, kTileThreads, smem, num_sms, kMaxTileCtas, known, &ctas);
     if (e != cudaSuccess) return e;
-    if ((e = launch_kernel(kernel, dim3(ctas), dim3(kTileThreads), smem, st, pdl, 1, p)) !=
+    if ((e = launch_kernel(kernel, dim3(ctas), dim3(kTileThreads), smem, st, pdl, 1, p, km, vm)) !=
         cudaSuccess)
         return e;
     return launch_join<D>(p, pl.rows, ctas >= 4 * pl.expected, pdl, st);
 }
 
+template <int D, bool kE5M2>
+inline cudaError_t launch_tile_type(const Params &p, const Plan &pl, int num_sms, bool pdl,
+                                    cudaStream_t st) {
+    if (pl.rows == 256)
+        return p.bf16 ? launch_tiles<D, 2, kE5M2, true>(p, pl, num_sms, pdl, st)
+                      : launch_tiles<D, 3, kE5M2, true>(p, pl, num_sms, pdl, st);
+    return p.bf16 ? launch_tiles<D, 2, kE5M2, false>(p, pl, num_sms, pdl, st)
+                  : launch_tiles<D, 3, kE5M2, false>(p, pl, num_sms, pdl, st);
+}
+
 template <bool kE5M2>
 cudaError_t launch_tree(const Params &p, const Plan &pl, int num_sms, bool pdl, cudaStream_t st) {
-    if (pl.tiles) {
-        if (p.D == 64)
-            return pl.rows == 256 ? launch_tiles<64, kE5M2, true>(p, pl, num_sms, pdl, st)
-                                  : launch_tiles<64, kE5M2, false>(p, pl, num_sms, pdl, st);
-        return pl.rows == 256 ? launch_tiles<128, kE5M2, true>(p, pl, num_sms, pdl, st)
-                              : launch_tiles<128, kE5M2, false>(p, pl, num_sms, pdl, st);
-    }
+    if (pl.tiles)
+        return p.D == 64 ? launch_tile_type<64, kE5M2>(p, pl, num_sms, pdl, st)
+                         : launch_tile_type<128, kE5M2>(p, pl, num_sms, pdl, st);
     switch (p.D) {
     case 64: return launch_type<64, kE5M2>(p, pl, num_sms, pdl, st);
     case 96: return launch_type<96, kE5M2>(p, pl, num_sms, pdl, st);

@@ -7,6 +7,8 @@
 namespace rarn {
 namespace tree {
 
+constexpr int kBoxSlots = 8;
+
 struct Plan {
     int rows;          // rows (drafted token x query head of the group) of a segment
     bool tiles;        // the tensor-memory kernel (tree_tile.cuh)
@@ -17,12 +19,13 @@ struct Plan {
 
 inline bool dim_ok(int64_t D) { return D == 64 || D == 96 || D == 128 || D == 192 || D == 256; }
 
-// tokens drafted tokens in all, of B sequences.
-inline Plan plan(int64_t tokens, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
+// tokens drafted tokens in all, of B sequences; boxes: the pages are made of
+// whole groups of eight slots, which the tensor-memory kernel copies.
+inline Plan plan(int64_t tokens, int64_t B, int64_t Hq, int64_t Hk, int64_t D, bool boxes) {
     Plan p{};
     const int64_t G = Hq / Hk;
     const int64_t per = ((tokens + B - 1) / B) * G;  // rows of an average sequence
-    p.tiles = (D == 64 || D == 128) && per > 16;
+    p.tiles = boxes && (D == 64 || D == 128) && per > 16;
     p.rows = p.tiles ? (per > 128 ? 256 : 128) : per > 8 && D <= 128 ? 16 : 8;
     const int64_t ctas = p.tiles ? 160 : 608;
     // every sequence ends in at most one block that is not full

@@ -2,105 +2,133 @@
 // 128 or 256 rows (drafted tokens x query heads of a group) against tiles of
 // 128 keys on the fifth-generation tensor cores.
 //
-//   S = Q K^T, P = 2^(s - m) vs, O = P V      binary16 operands, binary32 sums
+//   S = Q K^T    the keys' codes as they are, against the queries split into
+//                e4m3 pieces (two hold a bfloat16, three a binary16), 8-bit
+//                operands, binary32 sums
+//   O = P V      binary16 operands, binary32 sums; P = 2^(s - m) vs
 //
-// With more than a few dozen rows the second product's conversions no longer
-// hide behind the reads, and mma.sync's binary16 rate (a quarter of
-// tcgen05's) becomes the bound; here the codes become binary16 once per tile
-// in shared memory, whatever the number of rows.
+// With more than a few dozen rows mma.sync's rate (a quarter of tcgen05's) and
+// the second product's conversions, which every block of rows makes anew,
+// become the bound of k_tree_rows; here the values become binary16 once per
+// tile in shared memory, whatever the number of rows, and the keys never.
 //
 // One CTA per SM, persistent over its part of the line of tiles:
-//   * eight converter warps load two tiles ahead into registers, convert the
-//     codes (exactly) and store keys and values in 128-byte-swizzled rows,
-//     and the tile's scales beside them;
-//   * two pipelines of four softmax warps, a thread per row: scores from
-//     tensor memory, running maximum with slack, weights rounded to binary16
-//     over the scores' columns; one thread of each issues its tcgen05.mma: S
-//     into the pipeline's 128 columns, and O += P V with P read from tensor
-//     memory and V from the same row layout as K (as the N-major operand).
-// Sixteen warps in all: with a seventeenth for the products a thread has 96
-// registers instead of 128, and what spills goes through the little L1 that
-// shared memory leaves (three times the time).
+//   * one warp looks up pages and copies codes by TMA, boxes of eight slots,
+//     the keys' straight into their operand's swizzled rows, a few tiles
+//     ahead; it puts the tile's scales beside them;
+//   * four warps convert the values' codes (exactly) into an operand;
+//   * two pipelines of four softmax warps: scores from tensor memory, running
+//     maximum with slack, weights rounded to binary16 over the scores'
+//     columns; one thread of each issues its tcgen05.mma: S into the
+//     pipeline's 128 columns, and O += P V with P read from tensor memory.
 // With up to 128 rows the pipelines take alternate tiles of the same rows, and
 // their states are joined at the end; with up to 256 rows each has its own
 // 128. While one pipeline is at its softmax the other's products run.
+//
+// Code that runs once per tile is kept in rolled loops: three roles share an
+// SM's instruction cache.
 //
 // Every wait is bounded; one that runs out sets watchdog bit 5, the CTA's
 // warps give up together, and its tensor memory is freed.
 #pragma once
 
 #include "tree_attn.cuh"
+#include "tree_plan.h"
 
 namespace rarn {
 namespace tree {
 
 constexpr int kTileKeys = 128;   // keys of a tile
 constexpr int kTileRows = 128;   // rows of a pipeline
+constexpr int kBox = kBoxSlots;  // slots of a TMA box
 constexpr int kSoftWarps = 8;
-constexpr int kConvWarps = 8;       // 16 keys of a tile each
-constexpr int kTileThreads = 32 * (kSoftWarps + kConvWarps);
+constexpr int kConvWarps = 4;
+constexpr int kTileThreads = 32 * (kSoftWarps + kConvWarps + 1);
 constexpr int kMaxTileCtas = 160;
+constexpr int kInfos = 8;        // tiles whose scales are kept
 
 // What the softmax needs of a tile besides its scores.
 struct TileInfo {
-    float kk[kTileKeys];      // key scale x softmax scale x what undoes Q's scaling
-    float vs[kTileKeys];      // value scale, 0 where there is no key
-    float vmax[kConvWarps];   // largest finite |vs| of 16 keys
-    uint16_t ok[kConvWarps];  // keys that exist
+    float kk[kTileKeys];  // key scale x softmax scale (log2 units), 0 where there is no key
+    float vs[kTileKeys];  // value scale, 0 where there is no key
+    uint32_t ok[4];       // keys that exist
+    float vmax;           // largest finite |vs|
+    int unused[3];
 };
 
-template <int D>
+// Shared memory: the queries' pieces (over which pipeline 1's state is laid
+// for the join), rings of the keys' and the values' codes, two converted
+// value tiles, the tiles' scales.
+template <int D, int NP, bool kTwo>
 struct TileSmem {
-    static constexpr int kOperand = kTileKeys * D * 2;  // one tile of K, V or Q in binary16
-    static constexpr int kQ = 0;                        // two of them
-    static constexpr int kK = 2 * kOperand;             // two stages
-    static constexpr int kV = 4 * kOperand;             // two stages
-    static constexpr int kInfo = 6 * kOperand;          // four tiles
-    static constexpr int kBytes = kInfo + 4 * (int)sizeof(TileInfo) + 1024;
+    static constexpr int kCodes = kTileKeys * D;       // bytes of a tile's codes
+    static constexpr int kHalf = 2 * kCodes;           // in binary16
+    static constexpr int kQ = 0;
+    static constexpr int kQBytes = kTwo ? 2 * NP * kCodes : 4 * kCodes;
+    static constexpr int kStagesK = kTwo && NP == 3 ? 2 : 3;
+    static constexpr int kStagesV = kTwo && NP == 3 ? 1 : 2;
+    static constexpr int kK = kQ + kQBytes;
+    static constexpr int kV = kK + kStagesK * kCodes;
+    static constexpr int kVh = kV + kStagesV * kCodes;
+    static constexpr int kInfo = kVh + 2 * kHalf;
+    static constexpr int kBytes = kInfo + kInfos * (int)sizeof(TileInfo) + 1024;
+    static_assert(4 * kCodes >= kTileRows * D * 4 || kTwo, "room for the join");
 };
 
 // Barriers, in one array.
 enum Bar : int {
-    B_KFULL = 0, B_KEMPTY = 2, B_VFULL = 4, B_VEMPTY = 6, B_SFULL = 8, B_PFULL = 10, B_ODONE = 12,
-    B_INFO = 14, B_QMAX = 18, B_QREADY = 19, B_MERGE = 20, B_DRAIN = 21, B_QDONE = 22, B_NEXT = 23,
-    B_COUNT = 24
+    B_KFULL = 0, B_KEMPTY = 3, B_VFULL = 6, B_VEMPTY = 8, B_HFULL = 10, B_HEMPTY = 12,
+    B_SFULL = 14, B_PFULL = 16, B_ODONE = 18, B_QREADY = 20, B_INFO = 22, B_MERGE = 30,
+    B_QDONE = 31, B_NEXT = 32, B_DRAIN = 33, B_COUNT = 34
 };
 
-// A CTA's share of the line, segment by segment.  Every role walks it alike.
+// A CTA's share of the line, segment by segment.  Every role walks it alike;
+// the softmax warps, short of registers, keep theirs in shared memory.
 struct Walk {
-    const Params &p;
-    int rows;
     int at, hi, base, seg0;
     Segment sg;
     int t0, t1, which;
 
-    __device__ __forceinline__ Walk(const Params &p_, int rows_, const Cursor &c)
-        : p(p_), rows(rows_), at(c.lo), hi(c.hi), base(c.base), seg0(c.seg0), t0(0), t1(0),
-          which(0) {
+    __device__ __forceinline__ void begin(const Cursor &c) {
+        at = c.lo;
+        hi = c.hi;
+        base = c.base;
+        seg0 = c.seg0;
+        t0 = t1 = which = 0;
         sg.b = c.b;
     }
     // The next segment; false when there is none.
-    __device__ __forceinline__ bool next() {
-        at += t1 - t0;
+    __device__ __forceinline__ bool next(const Params &p, int rows) {
+        int a = at + t1 - t0, bs = base, sb = sg.b, s0 = seg0;
         t0 = t1 = 0;
-        while (at < hi) {
-            sg.s = seq_of(p, sg.b, rows, kTileKeys);
-            const int units = (int)units_of(p, sg.s);
-            if (at < base + units) {
-                const int rel = at - base;
-                which = (unsigned)rel / (unsigned)sg.s.tiles;
-                t0 = rel - which * sg.s.tiles;
-                t1 = min(t0 + hi - at, sg.s.tiles);
-                sg.head = (unsigned)which / (unsigned)sg.s.blocks;
-                sg.block = which - sg.head * sg.s.blocks;
-                sg.row0 = p.starts[sg.b];
-                return true;
+        bool found = false;
+        while (a < hi) {
+            const Seq q = seq_of(p, sb, rows, kTileKeys);
+            const int units = (int)units_of(p, q);
+            if (a < bs + units) {
+                const int rel = a - bs;
+                const int w = (unsigned)rel / (unsigned)q.tiles;
+                const int first = rel - w * q.tiles;
+                which = w;
+                t0 = first;
+                t1 = min(first + hi - a, q.tiles);
+                sg.s = q;
+                const int head = (unsigned)w / (unsigned)q.blocks;
+                sg.head = head;
+                sg.block = w - head * q.blocks;
+                sg.row0 = p.starts[sb];
+                found = true;
+                break;
             }
-            base += units;
-            seg0 += p.cache.heads * sg.s.blocks;
-            ++sg.b;
+            bs += units;
+            s0 += p.cache.heads * q.blocks;
+            ++sb;
         }
-        return false;
+        at = a;
+        base = bs;
+        seg0 = s0;
+        sg.b = sb;
+        return found;
     }
 };
 
@@ -125,13 +153,6 @@ __device__ __forceinline__ bool tile_wait(const Params &p, uint32_t bar, uint32_
     }
 }
 
-// Exponent of a block's largest query magnitude (binary32 bits): Q is scaled
-// by 2^(13 - e), its largest element then in [2^13, 2^14).
-__device__ __forceinline__ int query_exponent(unsigned int amax) {
-    const int e = amax ? (int)(amax >> 23) - 127 : 13;
-    return e < -100 ? -100 : e;
-}
-
 __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }
 
 // Codes that are NaN or infinite become zero.
@@ -141,10 +162,14 @@ __device__ __forceinline__ uint32_t finite_codes(uint32_t w) {
     return w & ~__vcmpeq4(w & top, top);
 }
 
-// Byte of 16-byte chunk c (8 elements) of a row of `half` 64 elements: K-major
-// rows for Q and K, and the N-major form of V, are one layout.
+// Byte of 16-byte chunk x of a row of codes, in the TMA swizzle of rows of D
+// bytes; and of chunk c (8 elements) of a row of `half` 64 binary16 elements.
 template <int D>
-__device__ __forceinline__ uint32_t operand_at(int row, int half, int c) {
+__device__ __forceinline__ uint32_t code_at(int row, int x) {
+    return row * D + ((x ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ uint32_t half_at(int row, int half, int c) {
     return half * (kTileKeys * 128) + row * 128 + ((c ^ (row & 7)) << 4);
 }
 
@@ -160,9 +185,29 @@ __device__ __forceinline__ uint64_t value_desc(uint32_t saddr) {
     return d;
 }
 
-template <int N, bool kNMajorB>
-__host__ __device__ constexpr uint32_t tile_desc() {
-    return gemm::instr_desc<__half, N>() | (kNMajorB ? 1u << 16 : 0u);
+// Instruction descriptors: 8-bit operands of e4m3 (0) by e4m3 or e5m2 (1), and
+// binary16 with an N-major second operand.
+template <bool kE5M2>
+__host__ __device__ constexpr uint32_t scores_desc() {
+    return (1u << 4) | (0u << 7) | ((kE5M2 ? 1u : 0u) << 10) |
+           ((uint32_t)(kTileKeys >> 3) << 17) | ((uint32_t)(kTileRows >> 4) << 24);
+}
+
+template <int N>
+__host__ __device__ constexpr uint32_t products_desc() {
+    return gemm::instr_desc<__half, N>() | (1u << 16);
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // The first operand in tensor memory.
@@ -254,10 +299,15 @@ __device__ __forceinline__ void add_nonfinite(const Params &p, const Segment &sg
     }
 }
 
-// 16 columns of tensor memory on their way to registers, and their arrival.
-__device__ __forceinline__ void tmem_ld16_begin(uint32_t taddr, float (&r)[16]) {
+// The softmax reads scores in fragments: of 16 rows and 8 columns a lane has
+// columns 2c, 2c + 1 (c = lane % 4) of rows g and g + 8 (g = lane / 4).  A
+// lane so meets a quarter of a tile's keys in each of four rows, not all of
+// them in one, and the keys' factors, which every row needs, cost a quarter of
+// the shared-memory reads that a row to a lane takes.
+// 32 columns of 16 rows on their way to registers (4 i ..: columns 8 i ..).
+__device__ __forceinline__ void tmem_frag_begin(uint32_t taddr, float (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
           "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]),
@@ -265,21 +315,31 @@ __device__ __forceinline__ void tmem_ld16_begin(uint32_t taddr, float (&r)[16]) 
         : "r"(taddr));
 }
 
-__device__ __forceinline__ void tmem_ld16_end(float (&r)[16]) {
+// The arrival of both halves of a warp's rows.
+__device__ __forceinline__ void tmem_frag_end(float (&r)[16], float (&q)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]),
                    "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]),
                    "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
                  :
                  : "memory");
+    asm volatile(""
+                 : "+f"(q[0]), "+f"(q[1]), "+f"(q[2]), "+f"(q[3]), "+f"(q[4]), "+f"(q[5]),
+                   "+f"(q[6]), "+f"(q[7]), "+f"(q[8]), "+f"(q[9]), "+f"(q[10]), "+f"(q[11]),
+                   "+f"(q[12]), "+f"(q[13]), "+f"(q[14]), "+f"(q[15])
+                 :
+                 : "memory");
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+// 16 columns of 16 rows: the same fragments as binary16 pairs.
+__device__ __forceinline__ void tmem_frag_store(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+        "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
         : "memory");
 }
+
+constexpr uint32_t kHalfRows = 16u << 16;  // tensor memory's address of a warp's second 16 rows
 
 // Two binary32 values in one 64-bit register, and packed arithmetic on them.
 __device__ __forceinline__ uint64_t two(float a, float b) {
@@ -318,86 +378,145 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// A row's largest score of a tile: columns of S at `ts` times the keys'
-// factors.  kEdge: only where bits of vis are set.
-template <bool kEdge>
-__device__ __forceinline__ float row_top(uint32_t ts, const TileInfo &ti,
-                                         const uint32_t (&vis)[4]) {
-    float t0 = -INFINITY, t1 = -INFINITY;
-    float buf[2][16];
-    tmem_ld16_begin(ts, buf[0]);
+// A value of each of a lane's four rows (g, g + 8, g + 16, g + 24) from or to
+// the lane that owns the row (lane = row of the warp).
+__device__ __forceinline__ void rows_from_owner(float own, float (&v)[4]) {
+    const int g = (threadIdx.x & 31) >> 2;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        float(&s)[16] = buf[c & 1];
-        tmem_ld16_end(s);
-        if (c < 7) tmem_ld16_begin(ts + 16 * (c + 1), buf[(c + 1) & 1]);
-        const uint32_t v16 = kEdge ? vis[c >> 1] >> (16 * (c & 1)) : 0u;
-#pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-            const ulonglong2 kk = *reinterpret_cast<const ulonglong2 *>(ti.kk + 16 * c + j);
-            float2 a = apart(mul2(two(s[j], s[j + 1]), kk.x));
-            float2 b = apart(mul2(two(s[j + 2], s[j + 3]), kk.y));
-            if (kEdge) {
-                if (!((v16 >> j) & 1u)) a.x = -INFINITY;
-                if (!((v16 >> (j + 1)) & 1u)) a.y = -INFINITY;
-                if (!((v16 >> (j + 2)) & 1u)) b.x = -INFINITY;
-                if (!((v16 >> (j + 3)) & 1u)) b.y = -INFINITY;
-            }
-            t0 = max3(t0, a.x, a.y);
-            t1 = max3(t1, b.x, b.y);
-        }
-    }
-    return fmaxf(t0, t1);
+    for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, own, g + 8 * i);
 }
 
-// A row's weights of a tile, 2^(score - off) times the value scales, in
-// binary16 over the scores' columns; returns the sum of 2^(score - off).
+__device__ __forceinline__ float rows_to_owner(const float (&v)[4]) {
+    const int lane = threadIdx.x & 31;
+    float own = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x = __shfl_sync(0xffffffffu, v[i], 4 * (lane & 7));
+        if ((lane >> 3) == i) own = x;
+    }
+    return own;
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint32_t (&v)[4], int c) {
+    return c == 0 ? v[0] : c == 1 ? v[1] : c == 2 ? v[2] : v[3];
+}
+
+// The largest scores of a warp's 32 rows over a tile (S at `ts`, columns times
+// the keys' factors), each in the lane that owns the row.  kEdge: only where
+// bits of vis (of the lane's own row) are set.  back: what undoes the scaling
+// of the own row's query.
+template <bool kEdge>
+__device__ __forceinline__ float row_top(uint32_t ts, const TileInfo &ti,
+                                         const uint32_t (&vis)[4], float back) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c2 = 2 * (lane & 3);
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    float ahead[2][16];
+    tmem_frag_begin(ts, ahead[0]);
+    tmem_frag_begin(ts + kHalfRows, ahead[1]);
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        float s[2][16];
+        uint64_t kk[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            kk[j] = *reinterpret_cast<const uint64_t *>(ti.kk + 32 * c + 8 * j + c2);
+        const uint32_t word = kEdge ? word_of(vis, c) : 0u;
+        tmem_frag_end(ahead[0], ahead[1]);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            s[0][j] = ahead[0][j];
+            s[1][j] = ahead[1][j];
+        }
+        if (c < 3) {
+            tmem_frag_begin(ts + 32 * (c + 1), ahead[0]);
+            tmem_frag_begin(ts + 32 * (c + 1) + kHalfRows, ahead[1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // row g + 8 i
+            const uint32_t v = kEdge ? __shfl_sync(0xffffffffu, word, g + 8 * i) >> c2 : 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = 4 * j + 2 * (i & 1);
+                float2 a = apart(mul2(two(s[i >> 1][at], s[i >> 1][at + 1]), kk[j]));
+                if (kEdge) {
+                    if (!((v >> (8 * j)) & 1u)) a.x = -INFINITY;
+                    if (!((v >> (8 * j + 1)) & 1u)) a.y = -INFINITY;
+                }
+                top[i] = max3(top[i], a.x, a.y);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+    }
+    return rows_to_owner(top) * back;
+}
+
+// The warp's weights of a tile, 2^(score - off) times the value scales, in
+// binary16 over the scores' columns; returns the sums of 2^(score - off), in
+// the lanes that own the rows.
 template <bool kEdge>
 __device__ __forceinline__ float row_weights(uint32_t ts, const TileInfo &ti,
-                                             const uint32_t (&vis)[4], float off) {
-    uint64_t l0 = two(0.f, 0.f), l1 = l0;
-    const uint64_t shift = two(-off, -off);
-    float buf[2][16];
-    tmem_ld16_begin(ts, buf[0]);
+                                             const uint32_t (&vis)[4], float own_off,
+                                             float own_back) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c2 = 2 * (lane & 3);
+    float off[4], back[4];
+    rows_from_owner(-own_off, off);
+    rows_from_owner(own_back, back);
+    uint64_t l[4];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        float(&s)[16] = buf[c & 1];
-        tmem_ld16_end(s);
-        if (c < 7) tmem_ld16_begin(ts + 16 * (c + 1), buf[(c + 1) & 1]);
-        const uint32_t v16 = kEdge ? vis[c >> 1] >> (16 * (c & 1)) : 0u;
-        uint32_t w[8];
+    for (int i = 0; i < 4; ++i) l[i] = two(0.f, 0.f);
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        float s[2][16];
+        tmem_frag_begin(ts + 32 * c, s[0]);
+        tmem_frag_begin(ts + 32 * c + kHalfRows, s[1]);
+        uint64_t kk[4], vs[4];
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-            const ulonglong2 kk = *reinterpret_cast<const ulonglong2 *>(ti.kk + 16 * c + j);
-            const ulonglong2 vs = *reinterpret_cast<const ulonglong2 *>(ti.vs + 16 * c + j);
-            float2 a = apart(fma2(two(s[j], s[j + 1]), kk.x, shift));
-            float2 b = apart(fma2(two(s[j + 2], s[j + 3]), kk.y, shift));
-            const uint32_t v4 = v16 >> j;
-            if (kEdge) {
-                if (!(v4 & 1u)) a.x = -INFINITY;
-                if (!(v4 & 2u)) a.y = -INFINITY;
-                if (!(v4 & 4u)) b.x = -INFINITY;
-                if (!(v4 & 8u)) b.y = -INFINITY;
-            }
-            const uint64_t pa = two(exp2_fast(a.x), exp2_fast(a.y));
-            const uint64_t pb = two(exp2_fast(b.x), exp2_fast(b.y));
-            l0 = add2(l0, pa);
-            l1 = add2(l1, pb);
-            a = apart(mul2(pa, vs.x));
-            b = apart(mul2(pb, vs.y));
-            if (kEdge) {
-                if (!(v4 & 1u)) a.x = 0.f;
-                if (!(v4 & 2u)) a.y = 0.f;
-                if (!(v4 & 4u)) b.x = 0.f;
-                if (!(v4 & 8u)) b.y = 0.f;
-            }
-            w[j / 2] = pack_h2(a.x, a.y);
-            w[j / 2 + 1] = pack_h2(b.x, b.y);
+        for (int j = 0; j < 4; ++j) {
+            kk[j] = *reinterpret_cast<const uint64_t *>(ti.kk + 32 * c + 8 * j + c2);
+            vs[j] = *reinterpret_cast<const uint64_t *>(ti.vs + 32 * c + 8 * j + c2);
         }
-        tmem_st8(ts + 8 * c, w);  // behind every load that is under way
+        const uint32_t word = kEdge ? word_of(vis, c) : 0u;
+        tmem_frag_end(s[0], s[1]);
+        uint32_t w[2][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // row g + 8 i
+            const uint32_t v = kEdge ? __shfl_sync(0xffffffffu, word, g + 8 * i) >> c2 : 0u;
+            const uint64_t shift = two(off[i], off[i]), by = two(back[i], back[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = 4 * j + 2 * (i & 1);
+                float2 a = apart(
+                    fma2(mul2(two(s[i >> 1][at], s[i >> 1][at + 1]), kk[j]), by, shift));
+                if (kEdge) {
+                    if (!((v >> (8 * j)) & 1u)) a.x = -INFINITY;
+                    if (!((v >> (8 * j + 1)) & 1u)) a.y = -INFINITY;
+                }
+                const uint64_t pr = two(exp2_fast(a.x), exp2_fast(a.y));
+                l[i] = add2(l[i], pr);
+                a = apart(mul2(pr, vs[j]));
+                if (kEdge) {
+                    if (!((v >> (8 * j)) & 1u)) a.x = 0.f;
+                    if (!((v >> (8 * j + 1)) & 1u)) a.y = 0.f;
+                }
+                w[i >> 1][2 * j + (i & 1)] = pack_h2(a.x, a.y);
+            }
+        }
+        tmem_frag_store(ts + 16 * c, w[0]);  // over columns that are read
+        tmem_frag_store(ts + 16 * c + kHalfRows, w[1]);
     }
-    const float2 x = apart(add2(l0, l1));
-    return x.x + x.y;
+    float sum[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = apart(l[i]);
+        sum[i] = x.x + x.y;
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+    }
+    return rows_to_owner(sum);
 }
 
 // The k of an offset m - k.
@@ -405,83 +524,13 @@ __device__ __forceinline__ int k_of(float off, float m) {
     return __float2int_rn((m == -INFINITY ? 0.f : m) - off);
 }
 
-// ---------------------------------------------------------------------------
-// Converters
-// ---------------------------------------------------------------------------
-
-// A tile as a converter lane knows it: key (lane & 15) of the warp's 16.
-struct Look {
-    int64_t code;     // where the key's codes lie, < 0: nowhere
-    float sc;         // lanes 0 .. 15: its key scale, 16 .. 31: its value scale
-    bool past;        // the tile reaches behind the context
-    bool first;       // of its segment
-};
-
-// Loads of each of K and V by a converter thread: 256 threads, 16 codes a load.
-template <int D>
-constexpr int kConvLoads = D / 32;
-
-// Where a converter thread's i-th load belongs: row of the warp's 16, chunk of
-// 16 codes.  Eight neighbouring lanes store two rows' neighbouring chunks,
-// which the swizzle keeps in different banks.
-template <int D>
-__device__ __forceinline__ void conv_place(int lane, int i, int &row, int &x) {
-    if constexpr (D == 128) {
-        row = ((lane >> 2) & 3) + 4 * i;
-        x = (lane & 3) | ((lane >> 4) << 2);
-    } else {
-        row = (lane >> 2) + 8 * i;
-        x = lane & 3;
-    }
-}
-
-__device__ __forceinline__ uint4 ld_past_l1(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
-// A converter thread's share of a tile's codes.
-template <int D>
-struct Codes {
-    uint4 k[kConvLoads<D>], v[kConvLoads<D>];
-
-    __device__ __forceinline__ void load(const Cache &c, int64_t code) {
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int i = 0; i < kConvLoads<D>; ++i) {
-            int row, x;
-            conv_place<D>(lane, i, row, x);
-            const int64_t at = __shfl_sync(0xffffffffu, code, row);
-            k[i] = v[i] = make_uint4(0, 0, 0, 0);
-            if (at >= 0) {
-                k[i] = ld_past_l1(c.k + at + x * 16);
-                v[i] = ld_past_l1(c.v + at + x * 16);
-            }
-        }
-    }
-};
-
-// 16 codes to binary16 into a tile of an operand.
-template <int D, bool kE5M2>
-__device__ __forceinline__ void store_codes(uint32_t base, int row, int x, const uint4 &c) {
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t h[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) kv::codes4_to_h2<kE5M2>(w[j], h[2 * j], h[2 * j + 1]);
-    const int half = x >> 2, ch = (x & 3) * 2;
-    gemm::sts128(base + operand_at<D>(row, half, ch), make_uint4(h[0], h[1], h[2], h[3]));
-    gemm::sts128(base + operand_at<D>(row, half, ch + 1), make_uint4(h[4], h[5], h[6], h[7]));
-}
-
-// ---------------------------------------------------------------------------
-
-// kTwo: 256 rows, 128 to each pipeline; else 128, tiles alternate.
-template <int D, bool kE5M2, bool kTwo>
-__global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
-    using S = TileSmem<D>;
+// kTwo: 256 rows, 128 to each pipeline; else 128, tiles alternate.  NP: pieces
+// of a query.
+template <int D, int NP, bool kE5M2, bool kTwo>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    k_tree_tile(const Params p, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap) {
+    using S = TileSmem<D, NP, kTwo>;
     constexpr int kRows = kTwo ? 2 * kTileRows : kTileRows;
     constexpr uint32_t kTmemO = 256;  // O of pipeline 0; S are columns 0 and 128
     extern __shared__ uint8_t smem_raw[];
@@ -490,8 +539,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
     __shared__ uint32_t sh_tmem;
     __shared__ volatile int sh_abort;
     __shared__ volatile int sh_nonfinite;  // a value was kept out of the products
-    __shared__ unsigned int sh_amax[2];    // of the block's queries, by segment parity
-    __shared__ float2 sh_ml[kTileRows];  // pipeline 1's l and offset
+    __shared__ float sh_back[kRows];       // what undoes the scaling of a row's query
+    __shared__ float2 sh_ml[kTileRows];    // pipeline 1's l and offset
     __shared__ float sh_m[kTileRows];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
@@ -502,26 +551,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
     auto bar = [&](int b) { return bars + 8 * b; };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            gemm::mbar_init(bar(B_KFULL + i), kConvWarps);
-            gemm::mbar_init(bar(B_KEMPTY + i), kTwo ? 2 : 1);
-            gemm::mbar_init(bar(B_VFULL + i), kConvWarps);
-            gemm::mbar_init(bar(B_VEMPTY + i), kTwo ? 2 : 1);
-            gemm::mbar_init(bar(B_SFULL + i), 1);
-            gemm::mbar_init(bar(B_PFULL + i), 4);
-            gemm::mbar_init(bar(B_ODONE + i), 1);
+        for (int i = 0; i < B_COUNT; ++i) {
+            // arrivals of one thread, of the four warps of a role, or of the
+            // products of each pipeline
+            int n = 1;
+            if ((i >= B_VEMPTY && i < B_HFULL + 2) || (i >= B_PFULL && i < B_ODONE) ||
+                (i >= B_QREADY && i < B_INFO) || i == B_MERGE || i == B_NEXT)
+                n = 4;
+            if ((i >= B_KEMPTY && i < B_VFULL) || (i >= B_HEMPTY && i < B_SFULL)) n = kTwo ? 2 : 1;
+            if (i == B_DRAIN) n = 2;
+            gemm::mbar_init(bar(i), n);
         }
-        for (int i = 0; i < 4; ++i) gemm::mbar_init(bar(B_INFO + i), kConvWarps);
-        gemm::mbar_init(bar(B_QMAX), kTwo ? 8 : 4);
-        gemm::mbar_init(bar(B_QREADY), kTwo ? 8 : 4);
-        gemm::mbar_init(bar(B_MERGE), 4);
-        gemm::mbar_init(bar(B_DRAIN), 2);
-        gemm::mbar_init(bar(B_QDONE), 1);
-        gemm::mbar_init(bar(B_NEXT), 4);
         gemm::fence_async_shared();
         sh_abort = 0;
         sh_nonfinite = 0;
-        sh_amax[0] = sh_amax[1] = 0;
     }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -537,155 +580,190 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
     grid_dependency_wait();
     grid_launch_dependents();
     const Cursor cur = find_part<128>(p, kRows, kTileKeys, sh_part);
-    Walk walk(p, kRows, cur);
+    // (its first lane's)
+    __shared__ Walk sh_walk[kSoftWarps];
 
-    if (warp >= kSoftWarps) {
-        // ---------------- converters ----------------
-        const int cw = warp - kSoftWarps;
-        // The stream of tiles over all segments.  While tile n is converted,
-        // the codes of n + 1 and n + 2 are on their way and the pages of
-        // n + 3 are looked up.
+    if (warp == kSoftWarps + kConvWarps) {
+        // ---------------- copies ----------------
+        // The stream of tiles over all segments.  Lane b (and b + 16) knows
+        // the page of box b, lane l the scales of keys 4 l .. 4 l + 3; pages
+        // and scales are loaded a tile ahead.
+        Walk walk;
+        walk.begin(cur);
         int tile = 0;
-        bool more = walk.next();
+        bool more = walk.next(p, kRows);
         if (more) tile = walk.t0;
-        struct Ahead {
-            int j, head;
-            int page;    // -1: none, -2: behind the sequence
-            bool past, first, there;
-        } ah;
-        auto look_up = [&]() {  // begins the look-up of the stream's next tile
-            ah.there = more;
+        struct Next {
+            int page, at, head, live;  // of the lane's box; keys of the tile
+            float ks[4], vs[4];
+            bool there;
+        } nx;
+        auto look = [&]() {
+            nx.there = more;
             if (!more) return;
             const Segment &sg = walk.sg;
-            ah.j = tile * kTileKeys + cw * 16 + (lane & 15);
-            ah.head = sg.head;
-            ah.past = (tile + 1) * kTileKeys > sg.s.ctx;
-            ah.first = tile == walk.t0;
-            ah.page = -2;
-            if (ah.j < sg.s.len) ah.page = max(-1, p.table[sg.b * p.table_stride + p.page_of(ah.j)]);
+            const int j0 = tile * kTileKeys, jb = j0 + kBox * (lane & 15);
+            nx.head = sg.head;
+            nx.live = sg.s.len - j0;
+            nx.page = -1;
+            nx.at = 0;
+            if (jb < sg.s.len) {
+                nx.page = p.table[sg.b * p.table_stride + p.page_of(jb)];
+                nx.at = p.offset_in_page(jb);
+                if (nx.page < 0 || nx.page >= p.cache.pages) {
+                    nx.page = -1;
+                    atomicOr(p.watchdog, kv::kWatchIndex);
+                }
+            }
+            const int page = __shfl_sync(0xffffffffu, nx.page, lane >> 1);
+            const int at = __shfl_sync(0xffffffffu, nx.at, lane >> 1) + 4 * (lane & 1);
+            const int64_t base = (int64_t)page * p.cache.s_page + sg.head * p.cache.s_head;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                nx.ks[i] = nx.vs[i] = 0.f;
+                if (page >= 0 && 4 * lane + i < nx.live) {
+                    nx.ks[i] = p.cache.k_scale[base + (at + i) * p.cache.s_slot];
+                    nx.vs[i] = p.cache.v_scale[base + (at + i) * p.cache.s_slot];
+                }
+            }
             if (++tile >= walk.t1) {
-                more = walk.next();
+                more = walk.next(p, kRows);
                 tile = walk.t0;
             }
         };
-        auto found = [&](Look &x) {  // ends it
-            x.code = -1;
-            x.sc = 0.f;
-            if (!ah.there) return false;
-            x.past = ah.past;
-            x.first = ah.first;
-            if (ah.page >= 0 && ah.page < p.cache.pages) {
-                const KeyAt at = place(p, ah.page, p.offset_in_page(ah.j), ah.head);
-                x.code = at.code;
-                x.sc = (lane < 16 ? p.cache.k_scale : p.cache.v_scale)[at.scale];
-            } else if (ah.page != -2) {
-                atomicOr(p.watchdog, kv::kWatchIndex);
-            }
-            return true;
+        auto copy = [&](const CUtensorMap *map, uint32_t dst, uint32_t full, uint32_t boxes,
+                        const Next &x) {
+            if (lane == 0) gemm::mbar_arrive_expect_tx(full, kBox * D * __popc(boxes));
+            __syncwarp();
+            if (lane < 16 && x.page >= 0)
+                tma_box(dst + lane * (kBox * D), map, full, 0, x.at, x.head, x.page);
         };
-        int segments = 0;  // begun by the tiles stored
-        int n = 0;         // tiles stored
+        look();
+        int ks = 0, vs = 0;          // stages
+        uint32_t kp = 1, vp = 1;     // parities of their releases
+#pragma unroll 1
+        for (int n = 0; nx.there; ++n) {
+            const Next now = nx;
+            const uint32_t boxes = __ballot_sync(0xffffffffu, now.page >= 0) & 0xffffu;
+            bool alive = tile_wait(p, bar(B_KEMPTY + ks), kp, &sh_abort);
+            if (!__all_sync(0xffffffffu, alive)) break;
+            copy(&kmap, sbase + S::kK + ks * S::kCodes, bar(B_KFULL + ks), boxes, now);
+            if (++ks == S::kStagesK) {
+                ks = 0;
+                kp ^= 1;
+            }
+            // The scales.  The tile that had the place eight tiles ago is done
+            // with: the products of tile n - 4 or later, which the release of
+            // this stage of keys waited for, came after its softmax.
+            TileInfo &ti = info[n & (kInfos - 1)];
+            float vmax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ti.kk[4 * lane + i] = now.ks[i] * p.scale_log2;
+                ti.vs[4 * lane + i] = now.vs[i];
+                const float a = fabsf(now.vs[i]);
+                if (a < INFINITY) vmax = fmaxf(vmax, a);
+            }
+            vmax = warp_max(vmax);
+            if (lane < 4) {
+                uint32_t w = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if ((boxes >> (4 * lane + i)) & 1u) w |= 0xffu << (8 * i);
+                const int left = now.live - 32 * lane;
+                ti.ok[lane] = left >= 32 ? w : left <= 0 ? 0u : w & ((1u << left) - 1u);
+            }
+            if (lane == 0) ti.vmax = vmax;
+            __syncwarp();
+            if (lane == 0) gemm::mbar_arrive(bar(B_INFO + (n & (kInfos - 1))));
+            look();
+            alive = tile_wait(p, bar(B_VEMPTY + vs), vp, &sh_abort);
+            if (!__all_sync(0xffffffffu, alive)) break;
+            copy(&vmap, sbase + S::kV + vs * S::kCodes, bar(B_VFULL + vs), boxes, now);
+            if (++vs == S::kStagesV) {
+                vs = 0;
+                vp ^= 1;
+            }
+        }
+        if (sh_abort) {  // let what is under way land before the CTA goes
+            const unsigned long long t0 = gemm::now_ns();
+            while (gemm::now_ns() - t0 < 1000000ull) {
+            }
+        }
+    } else if (warp >= kSoftWarps) {
+        // ---------------- values to binary16 ----------------
+        Walk walk;
+        walk.begin(cur);
+        const int cw = warp - kSoftWarps;
+        constexpr int kPer = D / 16;         // 16-code chunks of a row
+        constexpr int kLoads = kPer;         // of 32 rows by 32 lanes
+        int vs = 0;
+        uint32_t vp = 0;
+        int n = 0;
         bool alive = true;
-        auto store = [&](Codes<D> &c, const Look &now) {
-            const int stage = n & 1;
-            const uint32_t parity = ((n >> 1) & 1) ^ 1;
-            TileInfo &ti = info[n & 3];
-            const uint32_t kbase = sbase + S::kK + stage * S::kOperand;
-            const uint32_t vbase = sbase + S::kV + stage * S::kOperand;
-            alive = tile_wait(p, bar(B_KEMPTY + stage), parity, &sh_abort);
-            if (now.first) {
-                // the scaling of this segment's queries goes into the key scales
-                alive = alive && tile_wait(p, bar(B_QREADY), segments & 1, &sh_abort);
-                ++segments;
-            }
-            alive = __all_sync(0xffffffffu, alive);
-            if (!alive) return;
-#pragma unroll
-            for (int i = 0; i < kConvLoads<D>; ++i) {
-                int row, ch;
-                conv_place<D>(lane, i, row, ch);
-                store_codes<D, kE5M2>(kbase, cw * 16 + row, ch, c.k[i]);
-            }
-            const float undo =
-                power_of_two(query_exponent(sh_amax[(segments - 1) & 1]) - 13) * p.scale_log2;
-            const float vabs = fabsf(now.sc);
-            const float vmax = warp_max(lane >= 16 && vabs < INFINITY ? vabs : 0.f);
-            const uint32_t ok = __ballot_sync(0xffffffffu, now.code >= 0);
-            if (lane < 16) ti.kk[cw * 16 + lane] = now.sc * undo;
-            else ti.vs[cw * 16 + lane - 16] = now.sc;
-            if (lane == 0) {
-                ti.vmax[cw] = vmax;
-                ti.ok[cw] = (uint16_t)ok;
-            }
-            // Behind the context a value may be hidden from some rows, and 0
-            // times NaN or infinity would reach them: such elements become
-            // zero here and are added at the end to the rows that see them.
-            if (now.past) {
+#pragma unroll 1
+        while (alive && walk.next(p, kRows)) {
+#pragma unroll 1
+            for (int t = walk.t0; t < walk.t1; ++t, ++n) {
+                const TileInfo &ti = info[n & (kInfos - 1)];
+                const int stage = n & 1;
+                alive = tile_wait(p, bar(B_INFO + (n & (kInfos - 1))), (n >> 3) & 1, &sh_abort) &&
+                        tile_wait(p, bar(B_VFULL + vs), vp, &sh_abort) &&
+                        tile_wait(p, bar(B_HEMPTY + stage), ((n >> 1) & 1) ^ 1, &sh_abort);
+                alive = __all_sync(0xffffffffu, alive);
+                if (!alive) break;
+                const uint32_t from = sbase + S::kV + vs * S::kCodes,
+                               to = sbase + S::kVh + stage * S::kHalf;
+                const uint32_t ok = ti.ok[cw];
+                // Behind the context a value may be hidden from some rows, and
+                // 0 times NaN or infinity would reach them: such elements
+                // become zero here and are added at the end to the rows that
+                // see them.
+                const bool past = (t + 1) * kTileKeys > walk.sg.s.ctx;
                 bool any = false;
-#pragma unroll
-                for (int i = 0; i < kConvLoads<D>; ++i) {
-                    const uint4 w = c.v[i];
-                    c.v[i] = make_uint4(finite_codes<kE5M2>(w.x), finite_codes<kE5M2>(w.y),
-                                        finite_codes<kE5M2>(w.z), finite_codes<kE5M2>(w.w));
-                    any |= w.x != c.v[i].x || w.y != c.v[i].y || w.z != c.v[i].z ||
-                           w.w != c.v[i].w;
+#pragma unroll 4
+                for (int i = 0; i < kLoads; ++i) {
+                    // eight neighbouring lanes store two rows' neighbouring
+                    // chunks, which the swizzle keeps in different banks
+                    const int r = D == 128 ? ((lane >> 2) & 3) + 4 * i : (lane >> 2) + 8 * i;
+                    const int x = D == 128 ? (lane & 3) | ((lane >> 4) << 2) : lane & 3;
+                    const int row = cw * 32 + r;
+                    uint4 c = gemm::lds128(from + code_at<D>(row, x));
+                    if (!((ok >> r) & 1u)) c = make_uint4(0, 0, 0, 0);
+                    if (past) {
+                        const uint4 f = make_uint4(finite_codes<kE5M2>(c.x), finite_codes<kE5M2>(c.y),
+                                                   finite_codes<kE5M2>(c.z), finite_codes<kE5M2>(c.w));
+                        any |= c.x != f.x || c.y != f.y || c.z != f.z || c.w != f.w;
+                        c = f;
+                    }
+                    uint32_t h[8];
+                    kv::codes4_to_h2<kE5M2>(c.x, h[0], h[1]);
+                    kv::codes4_to_h2<kE5M2>(c.y, h[2], h[3]);
+                    kv::codes4_to_h2<kE5M2>(c.z, h[4], h[5]);
+                    kv::codes4_to_h2<kE5M2>(c.w, h[6], h[7]);
+                    gemm::sts128(to + half_at(row, x >> 2, (x & 3) * 2),
+                                 make_uint4(h[0], h[1], h[2], h[3]));
+                    gemm::sts128(to + half_at(row, x >> 2, (x & 3) * 2 + 1),
+                                 make_uint4(h[4], h[5], h[6], h[7]));
                 }
                 if (any) sh_nonfinite = 1;
+                gemm::fence_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    gemm::mbar_arrive(bar(B_VEMPTY + vs));
+                    gemm::mbar_arrive(bar(B_HFULL + stage));
+                }
+                if (++vs == S::kStagesV) {
+                    vs = 0;
+                    vp ^= 1;
+                }
             }
-            gemm::fence_async_shared();
-            __syncwarp();
-            if (lane == 0) {
-                gemm::mbar_arrive(bar(B_KFULL + stage));
-                gemm::mbar_arrive(bar(B_INFO + (n & 3)));
-            }
-            alive = tile_wait(p, bar(B_VEMPTY + stage), parity, &sh_abort);
-            alive = __all_sync(0xffffffffu, alive);
-            if (!alive) return;
-#pragma unroll
-            for (int i = 0; i < kConvLoads<D>; ++i) {
-                int row, ch;
-                conv_place<D>(lane, i, row, ch);
-                store_codes<D, kE5M2>(vbase, cw * 16 + row, ch, c.v[i]);
-            }
-            gemm::fence_async_shared();
-            __syncwarp();
-            if (lane == 0) gemm::mbar_arrive(bar(B_VFULL + stage));
-            ++n;
-        };
-        // looks of tiles n, n + 1 and n + 2; codes of n and n + 1
-        Codes<D> c0, c1;
-        Look l0, l1, l2;
-        look_up();
-        bool h0 = found(l0);
-        look_up();
-        c0.load(p.cache, l0.code);
-        bool h1 = found(l1);
-        look_up();
-        c1.load(p.cache, l1.code);
-        bool h2 = found(l2);
-        while (h0) {
-            look_up();
-            store(c0, l0);
-            if (!alive) break;
-            c0.load(p.cache, l2.code);
-            l0 = l1;
-            h0 = h1;
-            l1 = l2;
-            h1 = h2;
-            h2 = found(l2);
-            if (!h0) break;
-            look_up();
-            store(c1, l0);
-            if (!alive) break;
-            c1.load(p.cache, l2.code);
-            l0 = l1;
-            h0 = h1;
-            l1 = l2;
-            h1 = h2;
-            h2 = found(l2);
         }
     } else {
         // ---------------- softmax ----------------
+        Walk &walk = sh_walk[warp];
+        if (lane == 0) walk.begin(cur);
+        const int each = cur.each, more = cur.more;
         const int pipe = warp >> 2;
         const int r = threadIdx.x & 127;  // row of the pipeline = lane of tensor memory
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes
@@ -697,18 +775,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
         // that began at tile n is key tile n + t.
         const bool issuer = (threadIdx.x & 127) == 0;
         auto scores = [&](int t, bool last) {
-            const int stage = (n + t) & 1;
-            if (!tile_wait(p, bar(B_KFULL + stage), ((n + t) >> 1) & 1, &sh_abort)) return false;
+            const int stage = (n + t) % S::kStagesK;
+            if (!tile_wait(p, bar(B_KFULL + stage), ((n + t) / S::kStagesK) & 1, &sh_abort))
+                return false;
             gemm::tmem_fence_after();
-            const uint32_t qb = sbase + S::kQ + (kTwo ? pipe * S::kOperand : 0);
-            const uint32_t kb = sbase + S::kK + stage * S::kOperand;
+            const uint32_t qb = sbase + S::kQ + (kTwo ? pipe * NP * S::kCodes : 0);
+            const uint32_t kb = sbase + S::kK + stage * S::kCodes;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (k >> 2) * (kTileKeys * 128) + (k & 3) * 32;
-                gemm::mma_f16(tmem + pipe * 128, gemm::smem_desc(qb + off, 128),
-                              gemm::smem_desc(kb + off, 128), tile_desc<kTileKeys, false>(),
-                              k > 0);
-            }
+            for (int u = 0; u < NP; ++u)
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k)
+                    mma_f8(tmem + pipe * 128, gemm::smem_desc(qb + u * S::kCodes + 32 * k, D),
+                           gemm::smem_desc(kb + 32 * k, D), scores_desc<kE5M2>(), u > 0 || k > 0);
             gemm::mma_commit(bar(B_SFULL + pipe));
             gemm::mma_commit(bar(B_KEMPTY + stage));
             if (!kTwo && last && pipe == 0) gemm::mma_commit(bar(B_QDONE));
@@ -716,14 +794,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
         };
         auto products = [&](int t, bool started, bool last) {
             const int stage = (n + t) & 1;
-            if (!tile_wait(p, bar(B_VFULL + stage), ((n + t) >> 1) & 1, &sh_abort)) return false;
+            if (!tile_wait(p, bar(B_HFULL + stage), ((n + t) >> 1) & 1, &sh_abort)) return false;
             gemm::tmem_fence_after();
-            const uint32_t vb = sbase + S::kV + stage * S::kOperand;
+            const uint32_t vb = sbase + S::kVh + stage * S::kHalf;
 #pragma unroll
             for (int k = 0; k < kTileKeys / 16; ++k)
                 mma_f16_ts(tmem + kTmemO + pipe * 128, tmem + pipe * 128 + 8 * k,
-                           value_desc(vb + k * 2048), tile_desc<D, true>(), started || k > 0);
-            gemm::mma_commit(bar(B_VEMPTY + stage));
+                           value_desc(vb + k * 2048), products_desc<D>(), started || k > 0);
+            gemm::mma_commit(bar(B_HEMPTY + stage));
             if (last) gemm::mma_commit(bar(B_ODONE + pipe));
             return true;
         };
@@ -732,7 +810,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
             alive = __all_sync(0xffffffffu, alive);
             return alive;
         };
-        while (alive && walk.next()) {
+        while (alive) {
+            __syncwarp();
+            int go = 0;
+            if (lane == 0) go = walk.next(p, kRows);
+            if (!__shfl_sync(0xffffffffu, go, 0)) break;
+            __syncwarp();
             const Segment &sg = walk.sg;
             const int T = walk.t1 - walk.t0;
             const int R = sg.block * kRows + (kTwo ? pipe * kTileRows : 0) + r;
@@ -740,62 +823,84 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
             const bool live = tok < sg.s.n;
             const bool warp_live = __any_sync(0xffffffffu, live);
             if (kTwo || pipe == 0) {
-                // Q in binary16, scaled by one power of two for the block: a
-                // row that is not finite is left out of that and becomes NaN.
-                // D / 8 lanes read a row, all of the warp's 32 at once.
-                constexpr int kLanes = D / 8, kSide = 32 / kLanes, kN = 32 / kSide;
+                // Q's e4m3 pieces, each row scaled by a power of two that
+                // brings its largest magnitude to [128, 256): piece u is the
+                // rounded rest.  What is under 2^-18 of the row's largest is
+                // lost.  A row that is not finite becomes NaN.  D / 8 lanes
+                // read a row, four loads at a time.
+                constexpr int kLanes = D / 8, kSide = 32 / kLanes, kN = 32 / kSide, kB = 4;
                 const uint16_t *src = static_cast<const uint16_t *>(p.q.data);
                 const int64_t own =
                     live ? (sg.row0 + tok) * p.q.ts + (int64_t)hq * p.q.hs : -1;
                 const int chunk = lane % kLanes, side = lane / kLanes;
-                uint4 w[kN];
+                const uint32_t inf = NP == 2 ? 0x7f80u : 0x7c00u;
+                const uint32_t qb = sbase + S::kQ + (kTwo ? pipe * NP * S::kCodes : 0);
+                auto load = [&](int i, uint4 (&w)[kB]) {
 #pragma unroll
-                for (int i = 0; i < kN; ++i) {
-                    const int64_t at = __shfl_sync(0xffffffffu, own, i * kSide + side);
-                    w[i] = make_uint4(0, 0, 0, 0);
-                    if (at >= 0) w[i] = ld_past_l1(src + at + chunk * 8);
-                }
-                // magnitudes as the integers they sort as
-                const uint32_t inf = p.bf16 ? 0x7f80u : 0x7c00u;
-                uint32_t most = 0, bad = 0;  // bad: this lane's rows that are not finite, by i
+                    for (int u = 0; u < kB; ++u) {
+                        const int64_t at =
+                            __shfl_sync(0xffffffffu, own, (i + u) * kSide + side);
+                        w[u] = make_uint4(0, 0, 0, 0);
+                        if (at >= 0) w[u] = ld_stream(src + at + chunk * 8);
+                    }
+                };
+                uint4 w[kB], ahead[kB];
+                load(0, ahead);
+#pragma unroll 1
+                for (int i = 0; i < kN; i += kB) {
 #pragma unroll
-                for (int i = 0; i < kN; ++i) {
-                    const uint32_t m2 =
-                        __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
-                                 __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
-                    const uint32_t m1 = max(m2 & 0xffffu, m2 >> 16);
-                    const uint32_t group = (kLanes == 32 ? 0xffffffffu : (1u << (kLanes & 31)) - 1u)
-                                           << (side * kLanes);
-                    if (__ballot_sync(0xffffffffu, m1 >= inf) & group) bad |= 1u << i;
-                    else most = max(most, m1);
-                }
-                most = __reduce_max_sync(0xffffffffu, most);
-                if (lane == 0) {
-                    const float amax = p.bf16 ? __uint_as_float(most << 16)
-                                              : DT<__half>::w2f(most).x;
-                    atomicMax(&sh_amax[segment & 1], __float_as_uint(amax));
-                    gemm::mbar_arrive(bar(B_QMAX));
-                }
-                if (!wait(B_QMAX, segment)) break;
-                const float by = power_of_two(13 - query_exponent(sh_amax[segment & 1]));
-                if (threadIdx.x == 0) sh_amax[(segment + 1) & 1] = 0;
-                const uint32_t qb = sbase + S::kQ + (kTwo ? pipe * S::kOperand : 0);
+                    for (int u = 0; u < kB; ++u) w[u] = ahead[u];
+                    if (i + kB < kN) load(i + kB, ahead);
 #pragma unroll
-                for (int i = 0; i < kN; ++i) {
-                    float x[8];
-                    if (p.bf16) DT<__nv_bfloat16>::unpack(w[i], x);
-                    else DT<__half>::unpack(w[i], x);
-                    uint4 h = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-                    if (!((bad >> i) & 1u))
-                        h = make_uint4(pack_h2(x[0] * by, x[1] * by), pack_h2(x[2] * by, x[3] * by),
-                                       pack_h2(x[4] * by, x[5] * by), pack_h2(x[6] * by, x[7] * by));
-                    gemm::sts128(qb + operand_at<D>((warp & 3) * 32 + i * kSide + side, chunk >> 3,
-                                                    chunk & 7),
-                                 h);
+                    for (int u = 0; u < kB; ++u) {
+                        const int r = (warp & 3) * 32 + (i + u) * kSide + side;
+                        // the row's largest magnitude, as the integer it sorts as
+                        const uint32_t m2 =
+                            __vmaxu2(__vmaxu2(w[u].x & 0x7fff7fffu, w[u].y & 0x7fff7fffu),
+                                     __vmaxu2(w[u].z & 0x7fff7fffu, w[u].w & 0x7fff7fffu));
+                        uint32_t most = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+                        for (int x = kLanes / 2; x > 0; x >>= 1)
+                            most = max(most, __shfl_xor_sync(0xffffffffu, most, x));
+                        const float amax = NP == 2 ? __uint_as_float(most << 16)
+                                                   : DT<__half>::w2f(most).x;
+                        const bool finite = most < inf;
+                        int ex = finite && amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 : 7;
+                        ex = max(ex, -100);
+                        const float by = power_of_two(7 - ex);
+                        if (chunk == 0) sh_back[(kTwo ? pipe * kTileRows : 0) + r] = power_of_two(ex - 7);
+                        float f[8];
+                        if (NP == 2) DT<__nv_bfloat16>::unpack(w[u], f);
+                        else DT<__half>::unpack(w[u], f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] *= by;
+                        const uint32_t to = qb + code_at<D>(r, chunk >> 1) + 8 * (chunk & 1);
+#pragma unroll
+                        for (int v = 0; v < NP; ++v) {
+                            uint32_t c[2];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                c[h] = fp8x2(f[4 * h], f[4 * h + 1], Q_E4M3) |
+                                       fp8x2(f[4 * h + 2], f[4 * h + 3], Q_E4M3) << 16;
+                                uint32_t lo, hi;
+                                kv::codes4_to_h2<false>(c[h], lo, hi);
+                                const float2 a = DT<__half>::w2f(lo), b = DT<__half>::w2f(hi);
+                                f[4 * h] -= a.x;
+                                f[4 * h + 1] -= a.y;
+                                f[4 * h + 2] -= b.x;
+                                f[4 * h + 3] -= b.y;
+                                if (!finite) c[h] = 0x7f7f7f7fu;
+                            }
+                            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(
+                                             to + v * S::kCodes),
+                                         "r"(c[0]), "r"(c[1])
+                                         : "memory");
+                        }
+                    }
                 }
                 gemm::fence_async_shared();
                 __syncwarp();
-                if (lane == 0) gemm::mbar_arrive(bar(B_QREADY));
+                if (lane == 0) gemm::mbar_arrive(bar(B_QREADY + (kTwo ? pipe : 0)));
             }
 
             // weights are 2^(t - off), off = m - k: k lifts them so that the
@@ -807,21 +912,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
             int done = 0;  // items of this segment
             constexpr int kEach = kTwo ? 1 : 2;
             const int t_first = kTwo ? 0 : pipe;
+            if (!wait(B_QREADY + (kTwo ? pipe : 0), segment)) break;
+            const float back = sh_back[(kTwo ? pipe * kTileRows : 0) + r];
             if (t_first < T) {
-                if (issuer)
-                    alive = tile_wait(p, bar(B_QREADY), segment & 1, &sh_abort) &&
-                            scores(t_first, t_first + kEach >= T);
+                if (issuer) alive = scores(t_first, t_first + kEach >= T);
                 alive = __all_sync(0xffffffffu, alive);
                 if (!alive) break;
             }
             for (int t = t_first; t < T; t += kEach) {
                 if (!wait(B_SFULL + pipe, items)) break;
-                if (!wait(B_INFO + ((n + t) & 3), (n + t) >> 2)) break;
+                if (!wait(B_INFO + ((n + t) & (kInfos - 1)), (n + t) >> 3)) break;
                 gemm::tmem_fence_after();
-                const TileInfo &ti = info[(n + t) & 3];
+                const TileInfo &ti = info[(n + t) & (kInfos - 1)];
                 const int j0 = (walk.t0 + t) * kTileKeys;
-                const float4 va = *reinterpret_cast<const float4 *>(ti.vmax);
-                const float vm = fmaxf(fmaxf(va.x, va.y), fmaxf(va.z, va.w));
+                const float vm = ti.vmax;
                 const uint4 okw = *reinterpret_cast<const uint4 *>(ti.ok);
                 uint32_t vis[4] = {okw.x, okw.y, okw.z, okw.w};
                 const bool edge = (okw.x & okw.y & okw.z & okw.w) != 0xffffffffu ||
@@ -839,7 +943,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
                 // reach no other row
                 if (warp_live) {
                     // the row's largest score
-                    const float top = edge ? row_top<true>(ts, ti, vis) : row_top<false>(ts, ti, vis);
+                    const float top = edge ? row_top<true>(ts, ti, vis, back)
+                                           : row_top<false>(ts, ti, vis, back);
                     const bool lower = vm > 0.f && vm * power_of_two(k) > kWeightScale;  // uniform
                     if (__any_sync(0xffffffffu, lower || top > m + kSlack)) {
                         if (lower) k = min(k, 11 - (int)((__float_as_uint(vm) >> 23) & 0xff) + 127);
@@ -854,8 +959,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
                             for (int c = 0; c < D / 32; ++c) tmem_scale32(to + 32 * c, by);
                         }
                     }
-                    l += edge ? row_weights<true>(ts, ti, vis, off)
-                              : row_weights<false>(ts, ti, vis, off);
+                    l += edge ? row_weights<true>(ts, ti, vis, off, back)
+                              : row_weights<false>(ts, ti, vis, off, back);
                 }
                 tmem_st_wait();
                 gemm::tmem_fence_before();
@@ -951,20 +1056,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tree_tile(const Params p) {
                 if (walk.t0 == 0 && pipe == 0 && r == 0)
                     p.joins[walk.seg0 + walk.which] =
                         Join{(int)blockIdx.x,
-                             whole ? -1 : part_of(cur, walk.at + sg.s.tiles - 1),
+                             whole ? -1 : part_of(each, more, walk.at + sg.s.tiles - 1),
                              (int)sg.row0, sg.s.n, sg.head, sg.block, 0, 0};
             }
             gemm::tmem_fence_before();  // O is read before the next segment's products
             if (!kTwo) {
-                // The pipelines begin a segment together: one that skipped
+                // The pipelines begin a segment together: the next queries go
+                // where the joined state was read, and a pipeline that skipped
                 // segments of a single tile could take an old phase of a
                 // barrier for its own.
                 __syncwarp();
-                if (pipe == 0) {
-                    if (lane == 0) gemm::mbar_arrive(bar(B_NEXT));
-                } else if (!wait(B_NEXT, segment)) {
-                    break;
-                }
+                if (pipe == 0 && lane == 0) gemm::mbar_arrive(bar(B_NEXT));
+                if (!wait(B_NEXT, segment)) break;
             }
             n += T;
             ++segment;
