@@ -339,6 +339,18 @@ __device__ __forceinline__ void tmem_frag_store(uint32_t taddr, const uint32_t (
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 constexpr uint32_t kHalfRows = 16u << 16;  // tensor memory's address of a warp's second 16 rows
 
 // Two binary32 values in one 64-bit register, and packed arithmetic on them.
@@ -403,34 +415,24 @@ __device__ __forceinline__ uint32_t word_of(const uint32_t (&v)[4], int c) {
 
 // The largest scores of a warp's 32 rows over a tile (S at `ts`, columns times
 // the keys' factors), each in the lane that owns the row.  kEdge: only where
-// bits of vis (of the lane's own row) are set.  back: what undoes the scaling
-// of the own row's query.
+// bits of vis (of the lane's own row) are set.  For rows without an offset.
 template <bool kEdge>
-__device__ __forceinline__ float row_top(uint32_t ts, const TileInfo &ti,
-                                         const uint32_t (&vis)[4], float back) {
+__device__ __noinline__ float row_top(uint32_t ts, const TileInfo &ti, uint32_t v0,
+                                      uint32_t v1, uint32_t v2, uint32_t v3, float back) {
+    const uint32_t vis[4] = {v0, v1, v2, v3};
     const int lane = threadIdx.x & 31, g = lane >> 2, c2 = 2 * (lane & 3);
     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    float ahead[2][16];
-    tmem_frag_begin(ts, ahead[0]);
-    tmem_frag_begin(ts + kHalfRows, ahead[1]);
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         float s[2][16];
+        tmem_frag_begin(ts + 32 * c, s[0]);
+        tmem_frag_begin(ts + 32 * c + kHalfRows, s[1]);
         uint64_t kk[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             kk[j] = *reinterpret_cast<const uint64_t *>(ti.kk + 32 * c + 8 * j + c2);
         const uint32_t word = kEdge ? word_of(vis, c) : 0u;
-        tmem_frag_end(ahead[0], ahead[1]);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            s[0][j] = ahead[0][j];
-            s[1][j] = ahead[1][j];
-        }
-        if (c < 3) {
-            tmem_frag_begin(ts + 32 * (c + 1), ahead[0]);
-            tmem_frag_begin(ts + 32 * (c + 1) + kHalfRows, ahead[1]);
-        }
+        tmem_frag_end(s[0], s[1]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // row g + 8 i
             const uint32_t v = kEdge ? __shfl_sync(0xffffffffu, word, g + 8 * i) >> c2 : 0u;
@@ -454,38 +456,91 @@ __device__ __forceinline__ float row_top(uint32_t ts, const TileInfo &ti,
     return rows_to_owner(top) * back;
 }
 
-// The warp's weights of a tile, 2^(score - off) times the value scales, in
-// binary16 over the scores' columns; returns the sums of 2^(score - off), in
-// the lanes that own the rows.
-template <bool kEdge>
-__device__ __forceinline__ float row_weights(uint32_t ts, const TileInfo &ti,
-                                             const uint32_t (&vis)[4], float own_off,
-                                             float own_back) {
+// A lane's row of the running softmax.  Weights are 2^(score - off), and with
+// the value scale vs enter the products as binary16.  An offset is chosen when
+// the row first sees a key, such that its largest weight times the tile's
+// largest vs is 2^kCentre, and moves up only when one would pass 2^kHighest: a
+// pass over the scores serves where finding their maximum first took two.
+// What falls under 2^-24, 2^-28 of the largest term, is lost; 2^17 keys at
+// that edge would add up to half of binary16's own rounding.
+struct RowLane {
+    float l;     // sum of weights
+    float off;
+    float back;  // what undoes the scaling of the row's query
+    bool set;    // the offset is chosen (rows that are not there count as such)
+};
+
+constexpr float kCentre = 4.f;
+constexpr float kHighest = 15.f;
+
+// A tile's ceil(log2) of its largest value scale, within what binary32 sums of
+// weights bear.
+__device__ __forceinline__ float lift_of(float vmax) {
+    const int e = (int)(__float_as_uint(vmax) >> 23) - 126;
+    return (float)max(-70, min(e, 100));
+}
+
+// Scales by 2^-down (a row to a lane) what the row has summed up: O (its D
+// columns at `to`, where there is any), and the first `chunks` times 16 columns
+// of binary16 weights at `ts`.
+template <int D>
+__device__ __noinline__ void scale_down(uint32_t to, bool any, uint32_t ts, int chunks,
+                                        float down) {
+    const float by = exp2_fast(-down);
+    if (any) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) tmem_scale32(to + 32 * c, by);
+    }
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+        uint32_t w[16];
+        tmem_ld16(ts + 16 * c, w);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 x = DT<__half>::w2f(w[i]);
+            w[i] = pack_h2(x.x * by, x.y * by);
+        }
+        tmem_st16(ts + 16 * c, w);
+    }
+    tmem_st_wait();
+}
+
+// A warp's weights of a tile (S at `ts`, columns times the keys' factors), in
+// binary16 over the scores' columns.  Where a score is more than `most` over
+// its row's offset, all that the row has so far is scaled down first, so that
+// it comes to `centre`.  kEdge: only keys whose bits of vis (the own row's)
+// are set.
+template <int D, bool kEdge>
+__device__ __forceinline__ void row_weights(uint32_t ts, uint32_t to, bool any,
+                                            const TileInfo &ti, const uint32_t (&vis)[4],
+                                            float most, float centre, RowLane &row) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c2 = 2 * (lane & 3);
     float off[4], back[4];
-    rows_from_owner(-own_off, off);
-    rows_from_owner(own_back, back);
+    rows_from_owner(-row.off, off);
+    rows_from_owner(row.back, back);
     uint64_t l[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) l[i] = two(0.f, 0.f);
+    for (int i = 0; i < 4; ++i) {
+        l[i] = two(0.f, 0.f);
+    }
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < 4;) {
         float s[2][16];
         tmem_frag_begin(ts + 32 * c, s[0]);
         tmem_frag_begin(ts + 32 * c + kHalfRows, s[1]);
-        uint64_t kk[4], vs[4];
+        uint64_t kk[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 4; ++j)
             kk[j] = *reinterpret_cast<const uint64_t *>(ti.kk + 32 * c + 8 * j + c2);
-            vs[j] = *reinterpret_cast<const uint64_t *>(ti.vs + 32 * c + 8 * j + c2);
-        }
         const uint32_t word = kEdge ? word_of(vis, c) : 0u;
         tmem_frag_end(s[0], s[1]);
-        uint32_t w[2][8];
+        float top[4];
+        bool over = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // row g + 8 i
             const uint32_t v = kEdge ? __shfl_sync(0xffffffffu, word, g + 8 * i) >> c2 : 0u;
             const uint64_t shift = two(off[i], off[i]), by = two(back[i], back[i]);
+            float high = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int at = 4 * j + 2 * (i & 1);
@@ -495,9 +550,47 @@ __device__ __forceinline__ float row_weights(uint32_t ts, const TileInfo &ti,
                     if (!((v >> (8 * j)) & 1u)) a.x = -INFINITY;
                     if (!((v >> (8 * j + 1)) & 1u)) a.y = -INFINITY;
                 }
-                const uint64_t pr = two(exp2_fast(a.x), exp2_fast(a.y));
+                s[i >> 1][at] = a.x;
+                s[i >> 1][at + 1] = a.y;
+                high = max3(high, a.x, a.y);
+            }
+            top[i] = high;
+            over |= high > most;
+        }
+        if (__any_sync(0xffffffffu, over)) {
+            // rare: the offset moves up under what is there; then again
+            float d[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float high = top[i];
+                high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 1));
+                high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 2));
+                d[i] = high > most ? high - centre : 0.f;
+                const float q = exp2_fast(-d[i]);
+                l[i] = mul2(l[i], two(q, q));
+                off[i] -= d[i];
+            }
+            const float down = rows_to_owner(d);
+            row.off += down;
+            row.l *= exp2_fast(-down);
+            scale_down<D>(to, any, ts, c, down);
+            continue;
+        }
+        uint64_t vs[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            vs[j] = *reinterpret_cast<const uint64_t *>(ti.vs + 32 * c + 8 * j + c2);
+        uint32_t w[2][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t v = kEdge ? __shfl_sync(0xffffffffu, word, g + 8 * i) >> c2 : 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = 4 * j + 2 * (i & 1);
+                const uint64_t pr =
+                    two(exp2_fast(s[i >> 1][at]), exp2_fast(s[i >> 1][at + 1]));
                 l[i] = add2(l[i], pr);
-                a = apart(mul2(pr, vs[j]));
+                float2 a = apart(mul2(pr, vs[j]));
                 if (kEdge) {
                     if (!((v >> (8 * j)) & 1u)) a.x = 0.f;
                     if (!((v >> (8 * j + 1)) & 1u)) a.y = 0.f;
@@ -507,6 +600,7 @@ __device__ __forceinline__ float row_weights(uint32_t ts, const TileInfo &ti,
         }
         tmem_frag_store(ts + 16 * c, w[0]);  // over columns that are read
         tmem_frag_store(ts + 16 * c + kHalfRows, w[1]);
+        ++c;
     }
     float sum[4];
 #pragma unroll
@@ -516,12 +610,7 @@ __device__ __forceinline__ float row_weights(uint32_t ts, const TileInfo &ti,
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
     }
-    return rows_to_owner(sum);
-}
-
-// The k of an offset m - k.
-__device__ __forceinline__ int k_of(float off, float m) {
-    return __float2int_rn((m == -INFINITY ? 0.f : m) - off);
+    row.l += rows_to_owner(sum);
 }
 
 // kTwo: 256 rows, 128 to each pipeline; else 128, tiles alternate.  NP: pieces
@@ -541,7 +630,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __shared__ volatile int sh_nonfinite;  // a value was kept out of the products
     __shared__ float sh_back[kRows];       // what undoes the scaling of a row's query
     __shared__ float2 sh_ml[kTileRows];    // pipeline 1's l and offset
-    __shared__ float sh_m[kTileRows];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -903,17 +991,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (lane == 0) gemm::mbar_arrive(bar(B_QREADY + (kTwo ? pipe : 0)));
             }
 
-            // weights are 2^(t - off), off = m - k: k lifts them so that the
-            // largest weight times value scale is under 2^12 (kWeightScale),
-            // and drops out of O / l
-            float m = -INFINITY, l = 0.f;
-            int k = 100;
-            float off = -100.f;
+            RowLane row;
+            row.l = row.off = 0.f;
+            row.set = !live;
             int done = 0;  // items of this segment
             constexpr int kEach = kTwo ? 1 : 2;
             const int t_first = kTwo ? 0 : pipe;
             if (!wait(B_QREADY + (kTwo ? pipe : 0), segment)) break;
-            const float back = sh_back[(kTwo ? pipe * kTileRows : 0) + r];
+            row.back = sh_back[(kTwo ? pipe * kTileRows : 0) + r];
             if (t_first < T) {
                 if (issuer) alive = scores(t_first, t_first + kEach >= T);
                 alive = __all_sync(0xffffffffu, alive);
@@ -925,7 +1010,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 gemm::tmem_fence_after();
                 const TileInfo &ti = info[(n + t) & (kInfos - 1)];
                 const int j0 = (walk.t0 + t) * kTileKeys;
-                const float vm = ti.vmax;
                 const uint4 okw = *reinterpret_cast<const uint4 *>(ti.ok);
                 uint32_t vis[4] = {okw.x, okw.y, okw.z, okw.w};
                 const bool edge = (okw.x & okw.y & okw.z & okw.w) != 0xffffffffu ||
@@ -942,25 +1026,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 // a warp without rows leaves its weights as they are: they
                 // reach no other row
                 if (warp_live) {
-                    // the row's largest score
-                    const float top = edge ? row_top<true>(ts, ti, vis, back)
-                                           : row_top<false>(ts, ti, vis, back);
-                    const bool lower = vm > 0.f && vm * power_of_two(k) > kWeightScale;  // uniform
-                    if (__any_sync(0xffffffffu, lower || top > m + kSlack)) {
-                        if (lower) k = min(k, 11 - (int)((__float_as_uint(vm) >> 23) & 0xff) + 127);
-                        const float m1 = fmaxf(m, top);
-                        const float off1 = (m1 == -INFINITY ? 0.f : m1) - (float)k;
-                        const float by = m == -INFINITY ? 1.f : exp2_fast(off - off1);
-                        m = m1;
-                        off = off1;
-                        l *= by;
-                        if (done) {
-#pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) tmem_scale32(to + 32 * c, by);
+                    const float lift = lift_of(ti.vmax);
+                    if (!__all_sync(0xffffffffu, row.set)) {
+                        const float top =
+                            edge ? row_top<true>(ts, ti, vis[0], vis[1], vis[2], vis[3], row.back)
+                                 : row_top<false>(ts, ti, 0, 0, 0, 0, row.back);
+                        if (!row.set && top > -INFINITY) {
+                            row.off = top - (kCentre - lift);
+                            row.set = true;
                         }
                     }
-                    l += edge ? row_weights<true>(ts, ti, vis, off, back)
-                              : row_weights<false>(ts, ti, vis, off, back);
+                    if (edge)
+                        row_weights<D, true>(ts, to, done > 0, ti, vis, kHighest - lift,
+                                             kCentre - lift, row);
+                    else
+                        row_weights<D, false>(ts, to, done > 0, ti, vis, kHighest - lift,
+                                              kCentre - lift, row);
                 }
                 tmem_st_wait();
                 gemm::tmem_fence_before();
@@ -989,8 +1070,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 // this pipeline's state, over the queries once the other
                 // pipeline's last scores are done as well
                 if (!wait(B_QDONE, segment)) break;
-                sh_ml[r] = make_float2(l, off);
-                sh_m[r] = m;
+                sh_ml[r] = make_float2(row.l, row.off);
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     float o[32];
@@ -1005,25 +1085,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (joined) {
                     if (!wait(B_MERGE, merges)) break;
                     ++merges;
-                    const float2 o1 = sh_ml[r];
-                    const float m1 = sh_m[r];
                     // both in the units of the larger offset
-                    const float oo = fmaxf(m == -INFINITY ? -INFINITY : off,
-                                           m1 == -INFINITY ? -INFINITY : o1.y);
-                    f0 = m == -INFINITY ? 0.f : off == oo ? 1.f : exp2_fast(off - oo);
-                    f1 = m1 == -INFINITY ? 0.f : o1.y == oo ? 1.f : exp2_fast(o1.y - oo);
-                    l = (f0 == 0.f ? 0.f : l * f0) + (f1 == 0.f ? 0.f : o1.x * f1);
-                    if (m == -INFINITY || (m1 != -INFINITY && off != oo)) {
-                        m = m1;  // the offset's own maximum: their difference is k
-                        off = m1 == -INFINITY ? off : o1.y;
-                    }
+                    const float2 o1 = sh_ml[r];
+                    const float oo = fmaxf(row.l == 0.f ? -INFINITY : row.off,
+                                           o1.x == 0.f ? -INFINITY : o1.y);
+                    f0 = row.l == 0.f ? 0.f : row.off == oo ? 1.f : exp2_fast(row.off - oo);
+                    f1 = o1.x == 0.f ? 0.f : o1.y == oo ? 1.f : exp2_fast(o1.y - oo);
+                    row.l = row.l * f0 + o1.x * f1;
+                    row.off = oo;
                 }
                 const int64_t slot = 2 * (int64_t)blockIdx.x + (walk.t0 == 0 ? 1 : 0);
                 const int64_t prow = slot * kRows + (kTwo ? pipe * kTileRows : 0) + r;
-                // parts leave in units of 2^-m, without k
-                const float unit = power_of_two(-k_of(off, m));
-                const float by = whole ? (l == 0.f ? 0.f : 1.f / l) : unit;
-                if (!whole) p.ml[prow] = make_float2(m, l * unit);
+                const float by = !whole ? 1.f : row.l == 0.f ? 0.f : 1.f / row.l;
+                if (!whole)
+                    p.ml[prow] = make_float2(row.l == 0.f ? -INFINITY : row.off, row.l);
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     float o[32];
