@@ -88,30 +88,34 @@ struct Walk {
     int at, hi, base, seg0;
     Segment sg;
     int t0, t1, which;
+    int last_unit;  // of the segment, on the line
 
     __device__ __forceinline__ void begin(const Cursor &c) {
         at = c.lo;
         hi = c.hi;
         base = c.base;
         seg0 = c.seg0;
-        t0 = t1 = which = 0;
+        t0 = t1 = which = last_unit = 0;
         sg.b = c.b;
     }
     // The next segment; false when there is none.
     __device__ __forceinline__ bool next(const Params &p, int rows) {
-        int a = at + t1 - t0, bs = base, sb = sg.b, s0 = seg0;
-        t0 = t1 = 0;
+        int a = at, bs = base, sb = sg.b, s0 = seg0;
         bool found = false;
         while (a < hi) {
             const Seq q = seq_of(p, sb, rows, kTileKeys);
             const int units = (int)units_of(p, q);
             if (a < bs + units) {
-                const int rel = a - bs;
-                const int w = (unsigned)rel / (unsigned)q.tiles;
-                const int first = rel - w * q.tiles;
+                const int each = q.tiles + kBegin;
+                const int w = (unsigned)(a - bs) / (unsigned)each;
+                const int x0 = a - bs - w * each, x1 = min(x0 + hi - a, each);
+                a += x1 - x0;
+                const int first = max(x0 - kBegin, 0), end = x1 - kBegin;
+                if (end <= first) continue;
                 which = w;
                 t0 = first;
-                t1 = min(first + hi - a, q.tiles);
+                t1 = end;
+                last_unit = a - x1 + each - 1;
                 sg.s = q;
                 const int head = (unsigned)w / (unsigned)q.blocks;
                 sg.head = head;
@@ -1131,7 +1135,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (walk.t0 == 0 && pipe == 0 && r == 0)
                     p.joins[walk.seg0 + walk.which] =
                         Join{(int)blockIdx.x,
-                             whole ? -1 : part_of(each, more, walk.at + sg.s.tiles - 1),
+                             whole ? -1 : part_of(each, more, walk.last_unit),
                              (int)sg.row0, sg.s.n, sg.head, sg.block, 0, 0};
             }
             gemm::tmem_fence_before();  // O is read before the next segment's products
