@@ -17,13 +17,19 @@
 //     the keys' straight into their operand's swizzled rows, a few tiles
 //     ahead; it puts the tile's scales beside them;
 //   * four warps convert the values' codes (exactly) into an operand;
-//   * two pipelines of four softmax warps: scores from tensor memory, running
-//     maximum with slack, weights rounded to binary16 over the scores'
-//     columns; one thread of each issues its tcgen05.mma: S into the
-//     pipeline's 128 columns, and O += P V with P read from tensor memory.
+//   * two pipelines of four softmax warps take a tile in two passes of 64
+//     keys: scores from tensor memory, weights rounded to binary16 over the
+//     scores' columns;
+//   * a warp for each pipeline issues its tcgen05.mma: S into one of the
+//     pipeline's two times 64 columns, and O += P V with P read from tensor
+//     memory.  S is a pass ahead of the softmax, which so never waits for the
+//     products of its own pass, and issuing them, which takes as long as a
+//     pass, keeps nobody (with both done in line by one of the softmax warps
+//     16 sequences of drafted trees took 159 us, with the passes alone 179,
+//     with the warp as well 126).
 // With up to 128 rows the pipelines take alternate tiles of the same rows, and
 // their states are joined at the end; with up to 256 rows each has its own
-// 128. While one pipeline is at its softmax the other's products run.
+// 128.
 //
 // Code that runs once per tile is kept in rolled loops: three roles share an
 // SM's instruction cache.
@@ -31,6 +37,8 @@
 // Every wait is bounded; one that runs out sets watchdog bit 5, the CTA's
 // warps give up together, and its tensor memory is freed.
 #pragma once
+
+#include <cstddef>
 
 #include "tree_attn.cuh"
 #include "tree_plan.h"
@@ -40,10 +48,12 @@ namespace tree {
 
 constexpr int kTileKeys = 128;   // keys of a tile
 constexpr int kTileRows = 128;   // rows of a pipeline
+constexpr int kPass = 64;        // keys of a pass of the softmax, half a tile
 constexpr int kBox = kBoxSlots;  // slots of a TMA box
 constexpr int kSoftWarps = 8;
 constexpr int kConvWarps = 4;
-constexpr int kTileThreads = 32 * (kSoftWarps + kConvWarps + 1);
+constexpr int kIssueWarps = 2;   // of a pipeline's products
+constexpr int kTileThreads = 32 * (kSoftWarps + kConvWarps + 1 + kIssueWarps);
 constexpr int kMaxTileCtas = 160;
 constexpr int kInfos = 8;        // tiles whose scales are kept
 
@@ -78,8 +88,8 @@ struct TileSmem {
 // Barriers, in one array.
 enum Bar : int {
     B_KFULL = 0, B_KEMPTY = 3, B_VFULL = 6, B_VEMPTY = 8, B_HFULL = 10, B_HEMPTY = 12,
-    B_SFULL = 14, B_PFULL = 16, B_ODONE = 18, B_QREADY = 20, B_INFO = 22, B_MERGE = 30,
-    B_QDONE = 31, B_NEXT = 32, B_DRAIN = 33, B_COUNT = 34
+    B_SFULL = 14, B_PFULL = 18, B_ODONE = 22, B_QREADY = 26, B_INFO = 28, B_MERGE = 36,
+    B_QDONE = 37, B_NEXT = 38, B_DRAIN = 39, B_COUNT = 40
 };
 
 // A CTA's share of the line, segment by segment.  Every role walks it alike;
@@ -194,7 +204,7 @@ __device__ __forceinline__ uint64_t value_desc(uint32_t saddr) {
 template <bool kE5M2>
 __host__ __device__ constexpr uint32_t scores_desc() {
     return (1u << 4) | (0u << 7) | ((kE5M2 ? 1u : 0u) << 10) |
-           ((uint32_t)(kTileKeys >> 3) << 17) | ((uint32_t)(kTileRows >> 4) << 24);
+           ((uint32_t)(kPass >> 3) << 17) | ((uint32_t)(kTileRows >> 4) << 24);
 }
 
 template <int N>
@@ -262,7 +272,7 @@ __device__ __forceinline__ void tmem_scale32(uint32_t taddr, float by) {
 
 // Which of the 32 keys from drafted token d0 (negative: context) on a row
 // sees.
-__device__ __forceinline__ uint32_t seen_word(const Params &p, int64_t row, int tok, int n,
+__device__ __forceinline__ uint32_t seen_word(const Params &p, int64_t row, int tok,
                                               int d0) {
     if (d0 + 31 < 0) return 0xffffffffu;
     if (!p.mask) {
@@ -275,7 +285,6 @@ __device__ __forceinline__ uint32_t seen_word(const Params &p, int64_t row, int 
     };
     const int w = d0 >= 0 ? d0 >> 5 : -1, sh = d0 & 31;  // -1: the word of the context's end
     const uint32_t lo = d0 >= 0 ? word(w) : 0xffffffffu;
-    (void)n;
     return sh ? __funnelshift_r(lo, word(w + 1), sh) : lo;
 }
 
@@ -355,6 +364,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
+__device__ __forceinline__ uint64_t lds64(uint32_t a) {
+    uint64_t v;
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// Where a tile's figures are in shared memory.
+constexpr uint32_t kInfoVs = offsetof(TileInfo, vs), kInfoOk = offsetof(TileInfo, ok),
+                   kInfoVmax = offsetof(TileInfo, vmax);
+
 constexpr uint32_t kHalfRows = 16u << 16;  // tensor memory's address of a warp's second 16 rows
 
 // Two binary32 values in one 64-bit register, and packed arithmetic on them.
@@ -413,29 +432,25 @@ __device__ __forceinline__ float rows_to_owner(const float (&v)[4]) {
     return own;
 }
 
-__device__ __forceinline__ uint32_t word_of(const uint32_t (&v)[4], int c) {
-    return c == 0 ? v[0] : c == 1 ? v[1] : c == 2 ? v[2] : v[3];
-}
-
-// The largest scores of a warp's 32 rows over a tile (S at `ts`, columns times
-// the keys' factors), each in the lane that owns the row.  kEdge: only where
-// bits of vis (of the lane's own row) are set.  For rows without an offset.
+// The largest scores of a warp's 32 rows over a pass (S at `ts`, columns times
+// the keys' factors at `ti`), each in the lane that owns the row.  kEdge: only
+// where bits of v0, v1 (of the lane's own row) are set.  For rows without an
+// offset.
 template <bool kEdge>
-__device__ __noinline__ float row_top(uint32_t ts, const TileInfo &ti, uint32_t v0,
-                                      uint32_t v1, uint32_t v2, uint32_t v3, float back) {
-    const uint32_t vis[4] = {v0, v1, v2, v3};
+__device__ __noinline__ float row_top(uint32_t ts, uint32_t ti, uint32_t v0, uint32_t v1,
+                                      float back) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c2 = 2 * (lane & 3);
     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < kPass / 32; ++c) {
         float s[2][16];
         tmem_frag_begin(ts + 32 * c, s[0]);
         tmem_frag_begin(ts + 32 * c + kHalfRows, s[1]);
         uint64_t kk[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            kk[j] = *reinterpret_cast<const uint64_t *>(ti.kk + 32 * c + 8 * j + c2);
-        const uint32_t word = kEdge ? word_of(vis, c) : 0u;
+            kk[j] = lds64(ti + 4 * (32 * c + 8 * j + c2));
+        const uint32_t word = kEdge ? (c ? v1 : v0) : 0u;
         tmem_frag_end(s[0], s[1]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // row g + 8 i
@@ -468,10 +483,12 @@ __device__ __noinline__ float row_top(uint32_t ts, const TileInfo &ti, uint32_t 
 // What falls under 2^-24, 2^-28 of the largest term, is lost; 2^17 keys at
 // that edge would add up to half of binary16's own rounding.
 struct RowLane {
-    float l;     // sum of weights
-    float off;
-    float back;  // what undoes the scaling of the row's query
+    float off;   // of the own row
     bool set;    // the offset is chosen (rows that are not there count as such)
+    // of the four rows that the lane has fragments of: minus the offset, what
+    // undoes the scaling of the row's query, and the sums over the lane's keys
+    float sub[4], back[4];
+    uint64_t l[4];
 };
 
 constexpr float kCentre = 4.f;
@@ -509,41 +526,33 @@ __device__ __noinline__ void scale_down(uint32_t to, bool any, uint32_t ts, int 
     tmem_st_wait();
 }
 
-// A warp's weights of a tile (S at `ts`, columns times the keys' factors), in
-// binary16 over the scores' columns.  Where a score is more than `most` over
-// its row's offset, all that the row has so far is scaled down first, so that
-// it comes to `centre`.  kEdge: only keys whose bits of vis (the own row's)
-// are set.
-template <int D, bool kEdge>
-__device__ __forceinline__ void row_weights(uint32_t ts, uint32_t to, bool any,
-                                            const TileInfo &ti, const uint32_t (&vis)[4],
-                                            float most, float centre, RowLane &row) {
+// A warp's weights of a pass (S at `ts`, columns times the keys' factors at
+// `ti`), in binary16 over the scores' columns.  Where a score is more than
+// `most` over its row's offset, all that the row has so far is scaled down
+// first, once the products under way are in (`settled`), so that it comes to
+// `centre`.  kEdge: only keys whose bits of v0, v1 (the own row's) are set.
+template <int D, bool kEdge, class Settled>
+__device__ __forceinline__ bool row_weights(uint32_t ts, uint32_t to, bool any, uint32_t ti,
+                                            uint32_t v0, uint32_t v1, float most, float centre,
+                                            RowLane &row, const Settled &settled) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c2 = 2 * (lane & 3);
-    float off[4], back[4];
-    rows_from_owner(-row.off, off);
-    rows_from_owner(row.back, back);
-    uint64_t l[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        l[i] = two(0.f, 0.f);
-    }
 #pragma unroll 1
-    for (int c = 0; c < 4;) {
+    for (int c = 0; c < kPass / 32;) {
         float s[2][16];
         tmem_frag_begin(ts + 32 * c, s[0]);
         tmem_frag_begin(ts + 32 * c + kHalfRows, s[1]);
         uint64_t kk[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            kk[j] = *reinterpret_cast<const uint64_t *>(ti.kk + 32 * c + 8 * j + c2);
-        const uint32_t word = kEdge ? word_of(vis, c) : 0u;
+            kk[j] = lds64(ti + 4 * (32 * c + 8 * j + c2));
+        const uint32_t word = kEdge ? (c ? v1 : v0) : 0u;
         tmem_frag_end(s[0], s[1]);
         float top[4];
         bool over = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // row g + 8 i
             const uint32_t v = kEdge ? __shfl_sync(0xffffffffu, word, g + 8 * i) >> c2 : 0u;
-            const uint64_t shift = two(off[i], off[i]), by = two(back[i], back[i]);
+            const uint64_t shift = two(row.sub[i], row.sub[i]), by = two(row.back[i], row.back[i]);
             float high = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -571,19 +580,19 @@ __device__ __forceinline__ void row_weights(uint32_t ts, uint32_t to, bool any,
                 high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 2));
                 d[i] = high > most ? high - centre : 0.f;
                 const float q = exp2_fast(-d[i]);
-                l[i] = mul2(l[i], two(q, q));
-                off[i] -= d[i];
+                row.l[i] = mul2(row.l[i], two(q, q));
+                row.sub[i] -= d[i];
             }
             const float down = rows_to_owner(d);
             row.off += down;
-            row.l *= exp2_fast(-down);
+            if (any && !settled()) return false;
             scale_down<D>(to, any, ts, c, down);
             continue;
         }
         uint64_t vs[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            vs[j] = *reinterpret_cast<const uint64_t *>(ti.vs + 32 * c + 8 * j + c2);
+            vs[j] = lds64(ti + kInfoVs + 4 * (32 * c + 8 * j + c2));
         uint32_t w[2][8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -593,7 +602,7 @@ __device__ __forceinline__ void row_weights(uint32_t ts, uint32_t to, bool any,
                 const int at = 4 * j + 2 * (i & 1);
                 const uint64_t pr =
                     two(exp2_fast(s[i >> 1][at]), exp2_fast(s[i >> 1][at + 1]));
-                l[i] = add2(l[i], pr);
+                row.l[i] = add2(row.l[i], pr);
                 float2 a = apart(mul2(pr, vs[j]));
                 if (kEdge) {
                     if (!((v >> (8 * j)) & 1u)) a.x = 0.f;
@@ -606,15 +615,20 @@ __device__ __forceinline__ void row_weights(uint32_t ts, uint32_t to, bool any,
         tmem_frag_store(ts + 16 * c + kHalfRows, w[1]);
         ++c;
     }
+    return true;
+}
+
+// The sum of weights of the lane's own row.
+__device__ __forceinline__ float row_sum(const RowLane &row) {
     float sum[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 x = apart(l[i]);
+        const float2 x = apart(row.l[i]);
         sum[i] = x.x + x.y;
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
     }
-    row.l += rows_to_owner(sum);
+    return rows_to_owner(sum);
 }
 
 // kTwo: 256 rows, 128 to each pipeline; else 128, tiles alternate.  NP: pieces
@@ -644,12 +658,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < B_COUNT; ++i) {
-            // arrivals of one thread, of the four warps of a role, or of the
-            // products of each pipeline
+            // arrivals of one thread, of the four warps of a role, of the
+            // products of each pipeline, or of all who begin a segment
             int n = 1;
             if ((i >= B_VEMPTY && i < B_HFULL + 2) || (i >= B_PFULL && i < B_ODONE) ||
-                (i >= B_QREADY && i < B_INFO) || i == B_MERGE || i == B_NEXT)
+                (i >= B_QREADY && i < B_INFO) || i == B_MERGE)
                 n = 4;
+            if (i == B_NEXT) n = kSoftWarps + 1;
             if ((i >= B_KEMPTY && i < B_VFULL) || (i >= B_HEMPTY && i < B_SFULL)) n = kTwo ? 2 : 1;
             if (i == B_DRAIN) n = 2;
             gemm::mbar_init(bar(i), n);
@@ -782,6 +797,92 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             while (gemm::now_ns() - t0 < 1000000ull) {
             }
         }
+    } else if (warp > kSoftWarps + kConvWarps) {
+        // ---------------- a pipeline's products ----------------
+        // In the order that keeps the tensor cores ahead of the softmax: the
+        // scores of a pass are issued behind the products of the pass two
+        // before, whose columns they take.
+        const int pipe = warp - (kSoftWarps + kConvWarps + 1);
+        Walk walk;
+        walk.begin(cur);
+        int n = 0;                    // tiles of finished segments
+        int items = 0, segment = 0;   // items: tiles of this pipeline
+        constexpr int kEach = kTwo ? 1 : 2;
+        // Item t of a segment that began at tile n is key tile n + t.
+        auto scores = [&](int t, int half, bool last) {
+            const int stage = (n + t) % S::kStagesK;
+            if (half == 0 &&
+                !tile_wait(p, bar(B_KFULL + stage), ((n + t) / S::kStagesK) & 1, &sh_abort))
+                return false;
+            gemm::tmem_fence_after();
+            const uint32_t qb = sbase + S::kQ + (kTwo ? pipe * NP * S::kCodes : 0);
+            const uint32_t kb = sbase + S::kK + stage * S::kCodes + half * (kPass * D);
+#pragma unroll
+            for (int u = 0; u < NP; ++u)
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k)
+                    mma_f8(tmem + pipe * 128 + half * kPass, gemm::smem_desc(qb + u * S::kCodes + 32 * k, D),
+                           gemm::smem_desc(kb + 32 * k, D), scores_desc<kE5M2>(), u > 0 || k > 0);
+            gemm::mma_commit(bar(B_SFULL + 2 * pipe + half));
+            if (half == 1) {
+                gemm::mma_commit(bar(B_KEMPTY + stage));
+                if (!kTwo && last && pipe == 0) gemm::mma_commit(bar(B_QDONE));
+            }
+            return true;
+        };
+        auto products = [&](int t, int half, bool started) {
+            const int stage = (n + t) & 1;
+            if (half == 0 &&
+                !tile_wait(p, bar(B_HFULL + stage), ((n + t) >> 1) & 1, &sh_abort))
+                return false;
+            gemm::tmem_fence_after();
+            const uint32_t vb = sbase + S::kVh + stage * S::kHalf + half * (kPass / 16 * 2048);
+#pragma unroll
+            for (int k = 0; k < kPass / 16; ++k)
+                mma_f16_ts(tmem + kTmemO + pipe * 128, tmem + pipe * 128 + half * kPass + 8 * k,
+                           value_desc(vb + k * 2048), products_desc<D>(), started || k > 0);
+            if (half == 1) gemm::mma_commit(bar(B_HEMPTY + stage));
+            gemm::mma_commit(bar(B_ODONE + 2 * pipe + half));
+            return true;
+        };
+        auto segments = [&]() {
+#pragma unroll 1
+            while (walk.next(p, kRows)) {
+                const int T = walk.t1 - walk.t0;
+                if (!tile_wait(p, bar(B_QREADY + (kTwo ? pipe : 0)), segment & 1, &sh_abort))
+                    return;
+                const int first = kTwo ? 0 : pipe;
+                if (first < T)
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half)
+                        if (!scores(first, half, first + kEach >= T)) return;
+#pragma unroll 1
+                for (int t = first; t < T; t += kEach, ++items) {
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        if (!tile_wait(p, bar(B_PFULL + 2 * pipe + half), items & 1, &sh_abort) ||
+                            !products(t, half, t > first || half > 0))
+                            return;
+                        if (t + kEach < T && !scores(t + kEach, half, t + 2 * kEach >= T)) return;
+                    }
+                }
+                if (!kTwo && pipe == 1) {
+                    gemm::mbar_arrive(bar(B_NEXT));
+                    if (!tile_wait(p, bar(B_NEXT), segment & 1, &sh_abort)) return;
+                }
+                n += T;
+                ++segment;
+            }
+        };
+        if (lane == 0) {
+            segments();
+            // nothing may be in flight when the tensor memory goes
+            gemm::mma_commit(bar(B_DRAIN));
+            const unsigned long long t0 = gemm::now_ns();
+            while (!gemm::mbar_try_wait(bar(B_DRAIN), 0))
+                if (gemm::now_ns() - t0 > kWaitLimitNs) break;
+        }
+        __syncwarp();
     } else if (warp >= kSoftWarps) {
         // ---------------- values to binary16 ----------------
         Walk walk;
@@ -797,7 +898,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         while (alive && walk.next(p, kRows)) {
 #pragma unroll 1
             for (int t = walk.t0; t < walk.t1; ++t, ++n) {
-                const TileInfo &ti = info[n & (kInfos - 1)];
+                const uint32_t ti =
+                    sbase + S::kInfo + (n & (kInfos - 1)) * (uint32_t)sizeof(TileInfo);
                 const int stage = n & 1;
                 alive = tile_wait(p, bar(B_INFO + (n & (kInfos - 1))), (n >> 3) & 1, &sh_abort) &&
                         tile_wait(p, bar(B_VFULL + vs), vp, &sh_abort) &&
@@ -806,7 +908,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (!alive) break;
                 const uint32_t from = sbase + S::kV + vs * S::kCodes,
                                to = sbase + S::kVh + stage * S::kHalf;
-                const uint32_t ok = ti.ok[cw];
+                const uint32_t ok = __float_as_uint(lds_f(ti + kInfoOk + 4 * cw));
                 // Behind the context a value may be hidden from some rows, and
                 // 0 times NaN or infinity would reach them: such elements
                 // become zero here and are added at the end to the rows that
@@ -861,42 +963,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes
         const uint32_t ts = tmem + pipe * 128 + lanes, to = tmem + kTmemO + pipe * 128 + lanes;
         int n = 0;                            // tiles of finished segments
-        int items = 0, segment = 0, merges = 0, rounds = 0;
+        int items = 0, segment = 0, merges = 0;  // items: passes of this pipeline
         bool alive = true;
-        // The pipeline's products, issued by one thread: item t of a segment
-        // that began at tile n is key tile n + t.
-        const bool issuer = (threadIdx.x & 127) == 0;
-        auto scores = [&](int t, bool last) {
-            const int stage = (n + t) % S::kStagesK;
-            if (!tile_wait(p, bar(B_KFULL + stage), ((n + t) / S::kStagesK) & 1, &sh_abort))
-                return false;
-            gemm::tmem_fence_after();
-            const uint32_t qb = sbase + S::kQ + (kTwo ? pipe * NP * S::kCodes : 0);
-            const uint32_t kb = sbase + S::kK + stage * S::kCodes;
-#pragma unroll
-            for (int u = 0; u < NP; ++u)
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k)
-                    mma_f8(tmem + pipe * 128, gemm::smem_desc(qb + u * S::kCodes + 32 * k, D),
-                           gemm::smem_desc(kb + 32 * k, D), scores_desc<kE5M2>(), u > 0 || k > 0);
-            gemm::mma_commit(bar(B_SFULL + pipe));
-            gemm::mma_commit(bar(B_KEMPTY + stage));
-            if (!kTwo && last && pipe == 0) gemm::mma_commit(bar(B_QDONE));
-            return true;
-        };
-        auto products = [&](int t, bool started, bool last) {
-            const int stage = (n + t) & 1;
-            if (!tile_wait(p, bar(B_HFULL + stage), ((n + t) >> 1) & 1, &sh_abort)) return false;
-            gemm::tmem_fence_after();
-            const uint32_t vb = sbase + S::kVh + stage * S::kHalf;
-#pragma unroll
-            for (int k = 0; k < kTileKeys / 16; ++k)
-                mma_f16_ts(tmem + kTmemO + pipe * 128, tmem + pipe * 128 + 8 * k,
-                           value_desc(vb + k * 2048), products_desc<D>(), started || k > 0);
-            gemm::mma_commit(bar(B_HEMPTY + stage));
-            if (last) gemm::mma_commit(bar(B_ODONE + pipe));
-            return true;
-        };
         auto wait = [&](int b, int parity) {
             alive = tile_wait(p, bar(b), parity & 1, &sh_abort);
             alive = __all_sync(0xffffffffu, alive);
@@ -996,77 +1064,80 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
 
             RowLane row;
-            row.l = row.off = 0.f;
+            row.off = 0.f;
             row.set = !live;
-            int done = 0;  // items of this segment
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                row.sub[i] = 0.f;
+                row.l[i] = two(0.f, 0.f);
+            }
+            bool done = false;  // products of this segment are issued
             constexpr int kEach = kTwo ? 1 : 2;
             const int t_first = kTwo ? 0 : pipe;
             if (!wait(B_QREADY + (kTwo ? pipe : 0), segment)) break;
-            row.back = sh_back[(kTwo ? pipe * kTileRows : 0) + r];
-            if (t_first < T) {
-                if (issuer) alive = scores(t_first, t_first + kEach >= T);
-                alive = __all_sync(0xffffffffu, alive);
-                if (!alive) break;
-            }
+            const float back = sh_back[(kTwo ? pipe * kTileRows : 0) + r];
+            rows_from_owner(back, row.back);
             for (int t = t_first; t < T; t += kEach) {
-                if (!wait(B_SFULL + pipe, items)) break;
-                if (!wait(B_INFO + ((n + t) & (kInfos - 1)), (n + t) >> 3)) break;
-                gemm::tmem_fence_after();
-                const TileInfo &ti = info[(n + t) & (kInfos - 1)];
-                const int j0 = (walk.t0 + t) * kTileKeys;
-                const uint4 okw = *reinterpret_cast<const uint4 *>(ti.ok);
-                uint32_t vis[4] = {okw.x, okw.y, okw.z, okw.w};
-                const bool edge = (okw.x & okw.y & okw.z & okw.w) != 0xffffffffu ||
-                                  j0 + kTileKeys > sg.s.ctx;  // uniform
-                if (edge) {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const int d0 = j0 + 32 * w - sg.s.ctx;  // drafted token of bit 0
-                        uint32_t see = 0;
-                        if (live) see = seen_word(p, sg.row0 + tok, tok, sg.s.n, d0);
-                        vis[w] &= see;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    if (!wait(B_SFULL + 2 * pipe + half, items >> 1)) break;
+                    if (!wait(B_INFO + ((n + t) & (kInfos - 1)), (n + t) >> 3)) break;
+                    gemm::tmem_fence_after();
+                    const uint32_t info = sbase + S::kInfo +
+                                          ((n + t) & (kInfos - 1)) * (uint32_t)sizeof(TileInfo);
+                    const uint32_t ti = info + 4 * kPass * half, tsh = ts + kPass * half;
+                    const int j0 = (walk.t0 + t) * kTileKeys + kPass * half;
+                    const uint64_t okw = lds64(info + kInfoOk + 8 * half);
+                    uint32_t v0 = (uint32_t)okw, v1 = (uint32_t)(okw >> 32);
+                    const bool edge = okw != ~0ull || j0 + kPass > sg.s.ctx;  // uniform
+                    if (edge) {
+                        const int d0 = j0 - sg.s.ctx;  // drafted token of v0's bit 0
+                        v0 &= live ? seen_word(p, sg.row0 + tok, tok, d0) : 0u;
+                        v1 &= live ? seen_word(p, sg.row0 + tok, tok, d0 + 32) : 0u;
                     }
-                }
-                // a warp without rows leaves its weights as they are: they
-                // reach no other row
-                if (warp_live) {
-                    const float lift = lift_of(ti.vmax);
-                    if (!__all_sync(0xffffffffu, row.set)) {
-                        const float top =
-                            edge ? row_top<true>(ts, ti, vis[0], vis[1], vis[2], vis[3], row.back)
-                                 : row_top<false>(ts, ti, 0, 0, 0, 0, row.back);
-                        if (!row.set && top > -INFINITY) {
-                            row.off = top - (kCentre - lift);
-                            row.set = true;
+                    // a warp without rows leaves its weights as they are: they
+                    // reach no other row
+                    if (warp_live) {
+                        const float lift = lift_of(lds_f(info + kInfoVmax));
+                        if (!__all_sync(0xffffffffu, row.set)) {
+                            const float top = edge ? row_top<true>(tsh, ti, v0, v1, back)
+                                                   : row_top<false>(tsh, ti, 0, 0, back);
+                            if (!row.set && top > -INFINITY) {
+                                row.off = top - (kCentre - lift);
+                                row.set = true;
+                            }
+                            rows_from_owner(-row.off, row.sub);
                         }
+                        auto settled = [&]() {
+                            const bool in = wait(B_ODONE + 2 * pipe + (half ^ 1), (items - 1) >> 1);
+                            gemm::tmem_fence_after();
+                            return in;
+                        };
+                        if (edge)
+                            alive = row_weights<D, true>(tsh, to, done, ti, v0, v1,
+                                                         kHighest - lift, kCentre - lift, row,
+                                                         settled);
+                        else
+                            alive = row_weights<D, false>(tsh, to, done, ti, v0, v1,
+                                                          kHighest - lift, kCentre - lift, row,
+                                                          settled);
                     }
-                    if (edge)
-                        row_weights<D, true>(ts, to, done > 0, ti, vis, kHighest - lift,
-                                             kCentre - lift, row);
-                    else
-                        row_weights<D, false>(ts, to, done > 0, ti, vis, kHighest - lift,
-                                              kCentre - lift, row);
+                    tmem_st_wait();
+                    gemm::tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) gemm::mbar_arrive(bar(B_PFULL + 2 * pipe + half));
+                    if (!alive) break;
+                    ++items;
+                    done = true;
                 }
-                tmem_st_wait();
-                gemm::tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) gemm::mbar_arrive(bar(B_PFULL + pipe));
-                if (issuer) {
-                    alive = tile_wait(p, bar(B_PFULL + pipe), items & 1, &sh_abort) &&
-                            products(t, done > 0, t + kEach >= T);
-                    if (alive && t + kEach < T) alive = scores(t + kEach, t + 2 * kEach >= T);
-                }
-                alive = __all_sync(0xffffffffu, alive);
                 if (!alive) break;
-                ++items;
-                ++done;
             }
             if (!alive) break;
             if (done) {
-                if (!wait(B_ODONE + pipe, rounds)) break;
-                ++rounds;
+                if (!wait(B_ODONE + 2 * pipe + 1, (items - 1) >> 1)) break;
                 gemm::tmem_fence_after();
             }
+            float row_l = row_sum(row);
             const bool whole = walk.t0 == 0 && walk.t1 == sg.s.tiles;
             float *buf = reinterpret_cast<float *>(smem + S::kQ);  // [column][row]
             const bool joined = !kTwo && T > 1;
@@ -1074,7 +1145,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 // this pipeline's state, over the queries once the other
                 // pipeline's last scores are done as well
                 if (!wait(B_QDONE, segment)) break;
-                sh_ml[r] = make_float2(row.l, row.off);
+                sh_ml[r] = make_float2(row_l, row.off);
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     float o[32];
@@ -1091,18 +1162,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     ++merges;
                     // both in the units of the larger offset
                     const float2 o1 = sh_ml[r];
-                    const float oo = fmaxf(row.l == 0.f ? -INFINITY : row.off,
+                    const float oo = fmaxf(row_l == 0.f ? -INFINITY : row.off,
                                            o1.x == 0.f ? -INFINITY : o1.y);
-                    f0 = row.l == 0.f ? 0.f : row.off == oo ? 1.f : exp2_fast(row.off - oo);
+                    f0 = row_l == 0.f ? 0.f : row.off == oo ? 1.f : exp2_fast(row.off - oo);
                     f1 = o1.x == 0.f ? 0.f : o1.y == oo ? 1.f : exp2_fast(o1.y - oo);
-                    row.l = row.l * f0 + o1.x * f1;
+                    row_l = row_l * f0 + o1.x * f1;
                     row.off = oo;
                 }
                 const int64_t slot = 2 * (int64_t)blockIdx.x + (walk.t0 == 0 ? 1 : 0);
                 const int64_t prow = slot * kRows + (kTwo ? pipe * kTileRows : 0) + r;
-                const float by = !whole ? 1.f : row.l == 0.f ? 0.f : 1.f / row.l;
+                const float by = !whole ? 1.f : row_l == 0.f ? 0.f : 1.f / row_l;
                 if (!whole)
-                    p.ml[prow] = make_float2(row.l == 0.f ? -INFINITY : row.off, row.l);
+                    p.ml[prow] = make_float2(row_l == 0.f ? -INFINITY : row.off, row_l);
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     float o[32];
@@ -1141,24 +1212,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             gemm::tmem_fence_before();  // O is read before the next segment's products
             if (!kTwo) {
                 // The pipelines begin a segment together: the next queries go
-                // where the joined state was read, and a pipeline that skipped
-                // segments of a single tile could take an old phase of a
-                // barrier for its own.
+                // where the joined state was read, and who skipped segments of
+                // a single tile could take an old phase of a barrier for its
+                // own.
                 __syncwarp();
-                if (pipe == 0 && lane == 0) gemm::mbar_arrive(bar(B_NEXT));
+                if (lane == 0) gemm::mbar_arrive(bar(B_NEXT));
                 if (!wait(B_NEXT, segment)) break;
             }
             n += T;
             ++segment;
         }
-        // nothing may be in flight when the tensor memory goes
-        if (issuer) {
-            gemm::mma_commit(bar(B_DRAIN));
-            const unsigned long long t0 = gemm::now_ns();
-            while (!gemm::mbar_try_wait(bar(B_DRAIN), 0))
-                if (gemm::now_ns() - t0 > kWaitLimitNs) break;
-        }
-        __syncwarp();
     }
     gemm::tmem_fence_before();
     __syncthreads();
