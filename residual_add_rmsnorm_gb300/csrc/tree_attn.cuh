@@ -64,6 +64,7 @@ struct Params {
     bool whole_steps;        // a step of 16 keys lies inside one page, its scales adjacent on a
                              // 16-byte boundary
     int page_shift;          // log2 of the page size, or -1
+    int box;                 // slots of k_tree_tile's TMA boxes
 
     __device__ __forceinline__ int page_of(int j) const {
         return page_shift >= 0 ? j >> page_shift : j / cache.page_size;

@@ -112,14 +112,17 @@ inline cudaError_t launch_type(const Params &p, const Plan &pl, int num_sms, boo
 }
 
 template <int D, int NP, bool kE5M2, bool kTwo>
-inline cudaError_t launch_tiles(const Params &p, const Plan &pl, int num_sms, bool pdl,
+inline cudaError_t launch_tiles(const Params &given, const Plan &pl, int num_sms, bool pdl,
                                 cudaStream_t st) {
     static std::atomic<int> known[64];
     auto kernel = k_tree_tile<D, NP, kE5M2, kTwo>;
     constexpr int smem = TileSmem<D, NP, kTwo>::kBytes;
     CUtensorMap km{}, vm{};
-    if (!encode_codes<D>(&km, p.cache.k, p.cache, kBox) ||
-        !encode_codes<D>(&vm, p.cache.v, p.cache, kBox))
+    // The largest boxes that lie inside a page and a tile.
+    Params p = given;
+    for (p.box = kBox; p.box < kTileKeys && p.cache.page_size % (2 * p.box) == 0;) p.box *= 2;
+    if (!encode_codes<D>(&km, p.cache.k, p.cache, p.box) ||
+        !encode_codes<D>(&vm, p.cache.v, p.cache, p.box))
         return cudaErrorInvalidValue;
     int ctas = 0;
     cudaError_t e = resident(kernel, kTileThreads, smem, num_sms, kMaxTileCtas, known, &ctas);

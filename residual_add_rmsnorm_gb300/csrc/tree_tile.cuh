@@ -13,9 +13,11 @@
 // tile in shared memory, whatever the number of rows, and the keys never.
 //
 // One CTA per SM, persistent over its part of the line of tiles:
-//   * one warp looks up pages and copies codes by TMA, boxes of eight slots,
-//     the keys' straight into their operand's swizzled rows, a few tiles
-//     ahead; it puts the tile's scales beside them;
+//   * one warp looks up pages and copies codes by TMA, the keys' straight into
+//     their operand's swizzled rows, a few tiles ahead; it puts the tile's
+//     scales beside them.  Boxes are as large as the pages allow: the warp's
+//     time per box bounds it with boxes of eight slots (one context of 131072
+//     keys in pages of 64: 137 us, with boxes of 64 slots 123);
 //   * four warps convert the values' codes (exactly) into an operand;
 //   * two pipelines of four softmax warps take a tile in two passes of 64
 //     keys: scores from tensor memory, weights rounded to binary16 over the
@@ -49,7 +51,7 @@ namespace tree {
 constexpr int kTileKeys = 128;   // keys of a tile
 constexpr int kTileRows = 128;   // rows of a pipeline
 constexpr int kPass = 64;        // keys of a pass of the softmax, half a tile
-constexpr int kBox = kBoxSlots;  // slots of a TMA box
+constexpr int kBox = kBoxSlots;  // slots of the smallest TMA box
 constexpr int kSoftWarps = 8;
 constexpr int kConvWarps = 4;
 constexpr int kIssueWarps = 2;   // of a pipeline's products
@@ -693,60 +695,70 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (warp == kSoftWarps + kConvWarps) {
         // ---------------- copies ----------------
         // The stream of tiles over all segments.  Lane b (and b + 16) knows
-        // the page of box b, lane l the scales of keys 4 l .. 4 l + 3; pages
-        // and scales are loaded a tile ahead.
+        // the page of slots 8 b .. 8 b + 7, lane l the scales of keys 4 l .. 4 l + 3.  Pages
+        // are loaded two tiles ahead and scales one, or each tile would wait
+        // for one load after the other.
         Walk walk;
         walk.begin(cur);
         int tile = 0;
         bool more = walk.next(p, kRows);
         if (more) tile = walk.t0;
         struct Next {
-            int page, at, head, live;  // of the lane's box; keys of the tile
-            float ks[4], vs[4];
+            int page, at, head, live;  // of the lane's slots; keys of the tile
             bool there;
-        } nx;
-        auto look = [&]() {
-            nx.there = more;
-            if (!more) return;
-            const Segment &sg = walk.sg;
-            const int j0 = tile * kTileKeys, jb = j0 + kBox * (lane & 15);
-            nx.head = sg.head;
-            nx.live = sg.s.len - j0;
-            nx.page = -1;
-            nx.at = 0;
-            if (jb < sg.s.len) {
-                nx.page = p.table[sg.b * p.table_stride + p.page_of(jb)];
-                nx.at = p.offset_in_page(jb);
-                if (nx.page < 0 || nx.page >= p.cache.pages) {
-                    nx.page = -1;
-                    atomicOr(p.watchdog, kv::kWatchIndex);
+        } nx, after;
+        float ksc[4], vsc[4];  // of tile nx
+        auto look = [&]() {   // nx becomes the tile behind, after the one behind that
+            nx = after;
+            after.there = more;
+            if (more) {
+                const Segment &sg = walk.sg;
+                const int j0 = tile * kTileKeys, jb = j0 + kBox * (lane & 15);
+                after.head = sg.head;
+                after.live = sg.s.len - j0;
+                after.page = -1;
+                after.at = 0;
+                if (jb < sg.s.len) {
+                    after.page = p.table[sg.b * p.table_stride + p.page_of(jb)];
+                    after.at = p.offset_in_page(jb);
                 }
+                if (++tile >= walk.t1) {
+                    more = walk.next(p, kRows);
+                    tile = walk.t0;
+                }
+            }
+            if (!nx.there) return;
+            if (kBox * (lane & 15) < nx.live && (nx.page < 0 || nx.page >= p.cache.pages)) {
+                nx.page = -1;
+                atomicOr(p.watchdog, kv::kWatchIndex);
             }
             const int page = __shfl_sync(0xffffffffu, nx.page, lane >> 1);
             const int at = __shfl_sync(0xffffffffu, nx.at, lane >> 1) + 4 * (lane & 1);
-            const int64_t base = (int64_t)page * p.cache.s_page + sg.head * p.cache.s_head;
+            const int64_t base = (int64_t)page * p.cache.s_page + nx.head * p.cache.s_head;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                nx.ks[i] = nx.vs[i] = 0.f;
+                ksc[i] = vsc[i] = 0.f;
                 if (page >= 0 && 4 * lane + i < nx.live) {
-                    nx.ks[i] = p.cache.k_scale[base + (at + i) * p.cache.s_slot];
-                    nx.vs[i] = p.cache.v_scale[base + (at + i) * p.cache.s_slot];
+                    ksc[i] = p.cache.k_scale[base + (at + i) * p.cache.s_slot];
+                    vsc[i] = p.cache.v_scale[base + (at + i) * p.cache.s_slot];
                 }
             }
-            if (++tile >= walk.t1) {
-                more = walk.next(p, kRows);
-                tile = walk.t0;
-            }
         };
+        // lanes whose eight slots are the first of a box
+        const uint32_t first =
+            __ballot_sync(0xffffffffu, lane < 16 && ((kBox * lane) & (p.box - 1)) == 0);
         auto copy = [&](const CUtensorMap *map, uint32_t dst, uint32_t full, uint32_t boxes,
                         const Next &x) {
-            if (lane == 0) gemm::mbar_arrive_expect_tx(full, kBox * D * __popc(boxes));
+            if (lane == 0)
+                gemm::mbar_arrive_expect_tx(full, p.box * D * __popc(boxes & first));
             __syncwarp();
-            if (lane < 16 && x.page >= 0)
+            if (((first >> lane) & 1u) && x.page >= 0)
                 tma_box(dst + lane * (kBox * D), map, full, 0, x.at, x.head, x.page);
         };
+        after.there = false;
         look();
-        int ks = 0, vs = 0;          // stages
+        look();
+        int ks = 0, vs = 0;    // stages
         uint32_t kp = 1, vp = 1;     // parities of their releases
 #pragma unroll 1
         for (int n = 0; nx.there; ++n) {
@@ -766,9 +778,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             float vmax = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                ti.kk[4 * lane + i] = now.ks[i] * p.scale_log2;
-                ti.vs[4 * lane + i] = now.vs[i];
-                const float a = fabsf(now.vs[i]);
+                ti.kk[4 * lane + i] = ksc[i] * p.scale_log2;
+                ti.vs[4 * lane + i] = vsc[i];
+                const float a = fabsf(vsc[i]);
                 if (a < INFINITY) vmax = fmaxf(vmax, a);
             }
             vmax = warp_max(vmax);
