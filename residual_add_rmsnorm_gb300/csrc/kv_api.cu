@@ -89,6 +89,12 @@ bool same(const rarn_heads &a, const rarn_heads &b) {
     return a.data == b.data && a.token_stride == b.token_stride && a.head_stride == b.head_stride;
 }
 
+// Whether `count` steps of `stride` stay within RARN_MAX_STRIDE, so that no
+// offset below overflows (a single step is never taken).
+bool reaches(int64_t stride, int64_t count) {
+    return stride <= RARN_MAX_STRIDE && (count <= 1 || stride <= RARN_MAX_STRIDE / (count - 1));
+}
+
 // Sizes and strides of a [T, heads, D] matrix; an output's elements must not
 // share memory among themselves.
 rarn_status check_heads(const rarn_heads &h, int64_t T, int64_t D, bool output) {
@@ -97,7 +103,7 @@ rarn_status check_heads(const rarn_heads &h, int64_t T, int64_t D, bool output) 
     if (h.heads > RARN_MAX_HEADS) return RARN_ERR_UNSUPPORTED;
     if (T == 0) return RARN_OK;
     if (!h.data) return RARN_ERR_INVALID_ARG;
-    if (h.token_stride > RARN_MAX_STRIDE || h.head_stride > RARN_MAX_STRIDE)
+    if (!reaches(h.token_stride, T) || h.head_stride > RARN_MAX_STRIDE)
         return RARN_ERR_UNSUPPORTED;
     if (!on(h.data, (unsigned)size_of(h.dtype))) return RARN_ERR_INVALID_ARG;
     if (output) {
@@ -110,10 +116,11 @@ rarn_status check_heads(const rarn_heads &h, int64_t T, int64_t D, bool output) 
     return RARN_OK;
 }
 
-// Whether every head begins on an `a`-byte boundary.
-bool packs_ok(const rarn_heads &h, int a = 16) {
+// Whether every head of T tokens begins on an `a`-byte boundary.
+bool packs_ok(const rarn_heads &h, int64_t T, int a = 16) {
     const int64_t s = size_of(h.dtype);
-    return on(h.data, a) && h.token_stride * s % a == 0 && h.head_stride * s % a == 0;
+    return on(h.data, a) && (T == 1 || h.token_stride * s % a == 0) &&
+           (h.heads == 1 || h.head_stride * s % a == 0);
 }
 
 // Whether the (stride, count) dimensions with `inner` units innermost address
@@ -149,8 +156,8 @@ rarn_status check_cache(const rarn_kv_cache *c, CacheRanges *out) {
     if (c->head_dim % 16 || c->head_dim > 256 || c->heads > RARN_MAX_HEADS ||
         c->page_size > RARN_MAX_PAGE_SIZE || c->num_pages > (int64_t(1) << 31) - 1)
         return RARN_ERR_UNSUPPORTED;
-    if (c->page_stride > RARN_MAX_STRIDE || c->head_stride > RARN_MAX_STRIDE ||
-        c->slot_stride > RARN_MAX_STRIDE || c->scale_page_stride > RARN_MAX_STRIDE ||
+    if (!reaches(c->page_stride, c->num_pages) || c->head_stride > RARN_MAX_STRIDE ||
+        c->slot_stride > RARN_MAX_STRIDE || !reaches(c->scale_page_stride, c->num_pages) ||
         c->scale_head_stride > RARN_MAX_STRIDE || c->scale_slot_stride > RARN_MAX_STRIDE)
         return RARN_ERR_UNSUPPORTED;
     if (!on(c->k, 16) || !on(c->v, 16) || c->page_stride % 16 || c->head_stride % 16 ||
@@ -219,6 +226,7 @@ rarn_status check_rotation(const rarn_rotation *r, int64_t T, int64_t D) {
         return RARN_ERR_INVALID_ARG;
     if (r->rot_dim < 2 || r->rot_dim % 2 || r->rot_dim > D || r->table_rows < 1)
         return RARN_ERR_INVALID_ARG;
+    if (r->table_rows > RARN_MAX_STRIDE) return RARN_ERR_UNSUPPORTED;
     if (T > 0 && (!r->cos_sin || !r->positions)) return RARN_ERR_INVALID_ARG;
     if (!on(r->cos_sin, 4) || !on(r->positions, 8)) return RARN_ERR_INVALID_ARG;
     return RARN_OK;
@@ -337,11 +345,11 @@ rarn_status run_rows(const RowCall &c, void *stream) {
     // the vector kernel: 16-byte packs throughout, both packs of a lane on one
     // side of the rotation's end
     const int64_t e = 16 / s;
-    bool vec = c.D % (2 * e) == 0 && c.D / (2 * e) <= 32 && packs_ok(c.k) &&
+    bool vec = c.D % (2 * e) == 0 && c.D / (2 * e) <= 32 && packs_ok(c.k, c.T) &&
                (!c.q_gamma || on(c.q_gamma, 16)) && (!c.k_gamma || on(c.k_gamma, 16));
-    if (c.has_q) vec = vec && packs_ok(c.q) && packs_ok(c.q_out);
-    if (c.has_k_out) vec = vec && packs_ok(c.k_out);
-    if (c.has_v) vec = vec && packs_ok(c.v);
+    if (c.has_q) vec = vec && packs_ok(c.q, c.T) && packs_ok(c.q_out, c.T);
+    if (c.has_k_out) vec = vec && packs_ok(c.k_out, c.T);
+    if (c.has_v) vec = vec && packs_ok(c.v, c.T);
     if (c.rot) vec = vec && c.rot->rot_dim % (2 * e) == 0 && on(c.rot->cos_sin, 16);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const bool pdl = host::pdl_enabled();
@@ -465,8 +473,8 @@ rarn_status rarn_kv_cache_read(rarn_heads k_out, rarn_heads v_out, const rarn_kv
     p.rows = rows;
     p.D = (int)D;
     p.watchdog = dev.watchdog;
-    const bool vec = packs_ok(k_out, 16) && packs_ok(v_out, 16);
-    const int store = !vec ? 0 : packs_ok(k_out, 32) && packs_ok(v_out, 32) ? 32 : 16;
+    const bool vec = packs_ok(k_out, rows) && packs_ok(v_out, rows);
+    const int store = !vec ? 0 : packs_ok(k_out, rows, 32) && packs_ok(v_out, rows, 32) ? 32 : 16;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const bool pdl = host::pdl_enabled();
     cudaError_t e;
@@ -513,7 +521,9 @@ rarn_status rarn_tree_attention(rarn_heads out, rarn_heads q, const rarn_kv_cach
     if (tokens == 0 || B == 0) return RARN_OK;
     if (!context_lens || !starts || !on(context_lens, 4) || !on(starts, 4))
         return RARN_ERR_INVALID_ARG;
-    if (tokens >= kMaxItems / q.heads || !packs_ok(q)) return RARN_ERR_UNSUPPORTED;
+    if (tokens >= kMaxItems / q.heads || !packs_ok(q, tokens)) return RARN_ERR_UNSUPPORTED;
+    // keys are counted in 32 bits, with room for a tile behind the last
+    if (table_width > ((int64_t(1) << 31) - 4096) / cache->page_size) return RARN_ERR_UNSUPPORTED;
     const tree::Plan pl =
         tree::plan(tokens, B, q.heads, cache->heads, D, cache->page_size % tree::kBoxSlots == 0);
     if (pl.segments >= kMaxItems) return RARN_ERR_UNSUPPORTED;

@@ -286,3 +286,33 @@ def test_workspace_query(lib):
         assert tree(lib, c, B=4, bytes=n - 1) == INVALID
         if _no_device():
             assert tree(lib, c, B=4, bytes=n) == CUDA
+
+
+@pytest.mark.parametrize("call", SOUND)
+def test_sizes_whose_offsets_would_overflow(lib, call):
+    """Steps times strides beyond 2^40 are refused before they are multiplied."""
+    c = Call(T=1 << 20)
+    heads = {rope: ("q", 2, 8), write: ("k", 3, 2), fused: ("q", 2, 8), read: ("k_out", 0, 2),
+             tree: ("q", 2, 8)}[call]
+    far = {heads[0]: c.heads(heads[1], heads[2], token_stride=1 << 38)}
+    assert call(lib, c, **far) == UNSUPPORTED
+    if call is not rope:
+        assert call(lib, C, cache=C.cache(num_pages=1 << 20, page_stride=1 << 36)) == UNSUPPORTED
+        assert call(lib, C, cache=C.cache(scale_page_stride=1 << 39)) == UNSUPPORTED
+    if call in (rope, fused):
+        assert call(lib, C, rot=C.rotation(table_rows=1 << 60)) == UNSUPPORTED
+    if call is tree:
+        assert call(lib, C, width=1 << 27) == UNSUPPORTED   # 2^31 keys of a sequence
+        if _no_device():
+            assert call(lib, C, width=(1 << 27) - 256) == CUDA
+
+
+def test_strides_of_dimensions_of_one_do_not_matter(lib):
+    if not _no_device():
+        pytest.skip("fake addresses: only without a device")
+    c = Call(T=1)
+    assert tree(lib, c, q=c.heads(2, 8, token_stride=3)) == CUDA
+    c = Call(Hq=2, Hk=1)
+    assert tree(lib, c, q=c.heads(2, 2, head_stride=65)) == UNSUPPORTED
+    c = Call(Hq=1, Hk=1)
+    assert tree(lib, c, q=c.heads(2, 1, head_stride=65)) == CUDA
