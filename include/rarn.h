@@ -555,7 +555,8 @@ rarn_status rarn_ipc_close(void *ptr);
  * multiple of 16 up to 256, `k`, `v` 16-byte aligned and the code strides
  * multiples of 16 (else RARN_ERR_UNSUPPORTED); rows that share memory:
  * RARN_ERR_INVALID_ARG.  Keys and values may lie interleaved by pages in one
- * allocation.
+ * allocation (by slots or heads they count as overlapping: RARN_ERR_ALIAS where
+ * they are written).  A stride times its steps is at most RARN_MAX_STRIDE.
  *
  * Indices in device memory (positions, slots, page tables, lengths) cannot be
  * checked before the launch.  What lies outside its table is left out, never
@@ -685,15 +686,24 @@ rarn_status rarn_kv_cache_read(rarn_heads k_out, rarn_heads v_out, const rarn_kv
  * `tokens`): a sequence whose pair does is taken as empty, and nothing is
  * computed (bit 4) where they name more rows than there are.
  *
- * q, out: one 16-bit type; softmax statistics and sums in binary32, the
- * softmax weights rounded to binary16 (11 bits) for the second product.
+ * q, out: one 16-bit type.  Codes enter both products exactly, and a query
+ * row with every bit down to 2^-18 of its largest magnitude; softmax
+ * statistics and sums are in binary32, the softmax weights, times their
+ * value's scale, rounded to binary16 (11 bits) for the second product, where
+ * what is under 2^-28 of a row's largest is lost.  A row whose queries are not
+ * all finite, or that sees a key with a NaN code, is NaN.
  * head_dim 64, 96, 128, 192 or 256; q 16-byte aligned with strides multiples
- * of 8 elements (else RARN_ERR_UNSUPPORTED).  `workspace`:
+ * of 8 elements (else RARN_ERR_UNSUPPORTED); table_width * page_size
+ * below 2^31 - 4096.  Sequences of more than 16 rows on average (drafted tokens
+ * x query heads of a key head) are fastest with pages of a multiple of 8 slots,
+ * better of 64 or 128, and head_dim 64 or 128.  `workspace`:
  * rarn_tree_attention_workspace_bytes bytes of device memory, 32-byte aligned,
  * scratch for this call alone: calls that may overlap on the GPU need one
  * each.  The lengths are read on the device, so one captured call serves every
  * later length within its page table's width.  Results are the same bits on
- * every call with the same inputs.
+ * every call with the same inputs.  Every wait in the kernels is bounded (2 s):
+ * one that runs out sets bit 5 of the watchdog word, and the call's outputs are
+ * not valid.
  */
 rarn_status rarn_tree_attention(rarn_heads out, rarn_heads q, const rarn_kv_cache *cache,
                                 const int32_t *page_table, int64_t table_stride,
@@ -839,8 +849,8 @@ rarn_status rarn_plan_fp8(rarn_op op, int64_t T, int64_t H, int32_t R, rarn_dtyp
  * wait; bit 2: a wait in a GEMM-form kernel; bit 3: a wait of the
  * tensor-parallel form's barrier between ranks.  Bit 4 is no timeout: an index
  * in device memory lay outside its table (see the attention side), and what it
- * named was left out.  Synchronises the device.  If
- * `clear` is nonzero the word is reset to 0 after reading.
+ * named was left out.  Bit 5: a wait of rarn_tree_attention.  Synchronises the
+ * device.  If `clear` is nonzero the word is reset to 0 after reading.
  */
 rarn_status rarn_watchdog(uint32_t *flags, int clear);
 
