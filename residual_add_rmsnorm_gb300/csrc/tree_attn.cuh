@@ -785,6 +785,8 @@ __device__ __forceinline__ void consume_step(const Params &p, const Segment &sg,
     }
 }
 
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }
+
 // The block's query rows as the second operand of S = K Q^T.  Each row is
 // scaled by a power of two that brings its largest magnitude to [128, 256),
 // then split into NP e4m3 pieces, piece u the rounded rest times 2^4u: two
@@ -821,9 +823,9 @@ __device__ __forceinline__ void load_queries(const Params &p, const Segment &sg,
         }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        int ex = amax > 0.f && amax < INFINITY ? ilogbf(amax) : 7;
-        ex = ex < -100 ? -100 : ex;
-        const float by = ldexpf(1.f, 7 - ex), back = ldexpf(1.f, ex - 7) * p.scale_log2;
+        int ex = amax > 0.f && amax < INFINITY ? (int)(__float_as_uint(amax) >> 23) - 127 : 7;
+        ex = max(ex, -100);
+        const float by = power_of_two(7 - ex), back = power_of_two(ex - 7) * p.scale_log2;
 #pragma unroll
         for (int s = 0; s < D / 32; ++s)
 #pragma unroll
@@ -1080,7 +1082,7 @@ __global__ void __launch_bounds__(256) k_tree_join(const Params p, int rows) {
 #pragma unroll
     for (int n = 0; n < N; ++n) acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (live) {
-        constexpr int U = 4;
+        constexpr int U = kSplit == 1 ? 2 : 4;
         for (int w0 = jn.first + sub; w0 <= jn.last; w0 += U * kSplit) {
             float2 v[U];
             float4 o[U][N];
@@ -1100,7 +1102,7 @@ __global__ void __launch_bounds__(256) k_tree_join(const Params p, int rows) {
             float top = m;
 #pragma unroll
             for (int u = 0; u < U; ++u) top = fmaxf(top, v[u].x);
-            const float old = m == top || m == -INFINITY ? (m == top ? 1.f : 0.f) : exp2f(m - top);
+            const float old = m == top || m == -INFINITY ? (m == top ? 1.f : 0.f) : exp2_fast(m - top);
             m = top;
             l *= old;
 #pragma unroll
@@ -1112,7 +1114,7 @@ __global__ void __launch_bounds__(256) k_tree_join(const Params p, int rows) {
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float f = v[u].x == -INFINITY ? 0.f : v[u].x == m ? 1.f : exp2f(v[u].x - m);
+                const float f = v[u].x == -INFINITY ? 0.f : v[u].x == m ? 1.f : exp2_fast(v[u].x - m);
                 l += f * v[u].y;
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
@@ -1139,7 +1141,7 @@ __global__ void __launch_bounds__(256) k_tree_join(const Params p, int rows) {
 #pragma unroll
         for (int w = 0; w < kSplit; ++w) {
             const float2 v = sh_ml[warp + w];
-            const float f = v.x == -INFINITY ? 0.f : v.x == top ? 1.f : exp2f(v.x - top);
+            const float f = v.x == -INFINITY ? 0.f : v.x == top ? 1.f : exp2_fast(v.x - top);
             l += f * v.y;
 #pragma unroll
             for (int n = 0; n < N; ++n) {

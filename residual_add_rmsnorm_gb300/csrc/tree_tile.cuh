@@ -169,8 +169,6 @@ __device__ __forceinline__ bool tile_wait(const Params &p, uint32_t bar, uint32_
     }
 }
 
-__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }
-
 // Codes that are NaN or infinite become zero.
 template <bool kE5M2>
 __device__ __forceinline__ uint32_t finite_codes(uint32_t w) {
