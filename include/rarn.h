@@ -695,7 +695,7 @@ rarn_status rarn_kv_cache_read(rarn_heads k_out, rarn_heads v_out, const rarn_kv
  * head_dim 64, 96, 128, 192 or 256; q 16-byte aligned with strides multiples
  * of 8 elements (else RARN_ERR_UNSUPPORTED); table_width * page_size at most
  * 2^31 - 4096.  Sequences of many rows (drafted tokens x query heads of a key
- * head, 25 or more on average) are fastest with head_dim 64 or 128 and pages of
+ * head, 17 or more on average) are fastest with head_dim 64 or 128 and pages of
  * a multiple of 8 slots, better of 64 or 128.  `workspace`:
  * rarn_tree_attention_workspace_bytes bytes of device memory, 32-byte aligned,
  * scratch for this call alone: calls that may overlap on the GPU need one

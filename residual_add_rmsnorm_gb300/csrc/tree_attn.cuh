@@ -104,15 +104,18 @@ __device__ __forceinline__ Seq seq_of(const Params &p, int b, int rows, int tile
     return s;
 }
 
-// A segment takes kBegin units of the line for its beginning and end (queries
+// A segment takes some units of the line for its beginning and end (queries
 // read, state joined and written), then one for each of its tiles.  Without
-// them a CTA with many short segments worked on when the others were done (16
-// ragged sequences of drafted trees 229 us with 0, 178 with 2, 159 with 4, 170 with 8; 64 ragged
-// decode sequences 129, 110, 107, 111).
-constexpr int kBegin = 4;
+// them a CTA with many short segments worked on when the others were done.
+// k_tree_rows, tiles of 64 keys: 64 ragged decode sequences took 129 us with 0
+// units, 110 with 2, 106 with 3, 107 with 4, 109 with 6, 111 with 8, 16 short
+// ones of few tokens 45 with 4, 52 with 3.  k_tree_tile, tiles of 128: 16 ragged
+// sequences of 48 and of 96 rows 63 and 70 us with 4, 59 and 60 with 6, 60 and
+// 60 with 8; of 256 rows 135 with 3, 123 with 4 and 6, 128 with 8.
+__device__ __forceinline__ constexpr int begin_units(int tile) { return tile == kTile ? 4 : 6; }
 
-__device__ __forceinline__ int64_t units_of(const Params &p, const Seq &s) {
-    return (int64_t)p.cache.heads * s.blocks * (s.tiles + kBegin);
+__device__ __forceinline__ int64_t units_of(const Params &p, const Seq &s, int tile) {
+    return (int64_t)p.cache.heads * s.blocks * (s.tiles + begin_units(tile));
 }
 
 // Where a CTA's part of the line begins: CTA w has `each` tiles, one more
@@ -137,7 +140,7 @@ __device__ __forceinline__ Cursor find_part(const Params &p, int rows, int tile,
     if (threadIdx.x < kN)
         for (int b = b0; b < b1; ++b) {
             const Seq s = seq_of(p, b, rows, tile);
-            mine += units_of(p, s);
+            mine += units_of(p, s, tile);
             segs += (int64_t)p.cache.heads * s.blocks;
         }
     // inclusive scans inside the warp, then over the warps
@@ -189,7 +192,7 @@ __device__ __forceinline__ Cursor find_part(const Params &p, int rows, int tile,
         int b = b0;
         for (;; ++b) {
             const Seq s = seq_of(p, b, rows, tile);
-            const int64_t n = units_of(p, s);
+            const int64_t n = units_of(p, s, tile);
             if (c.lo < at + n) break;
             at += n;
             seg += (int64_t)p.cache.heads * s.blocks;
@@ -920,7 +923,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D <= 128 ? 4 : 2)
     sg.b = cur.b;
     while (at < cur.hi) {
         sg.s = seq_of(p, sg.b, kRows, kTile);
-        const int units = (int)units_of(p, sg.s);
+        constexpr int kBegin = begin_units(kTile);
+        const int units = (int)units_of(p, sg.s, kTile);
         if (at >= base + units) {
             base += units;
             seg0 += p.cache.heads * sg.s.blocks;

@@ -24,24 +24,25 @@ inline bool dim_ok(int64_t D) { return D == 64 || D == 96 || D == 128 || D == 19
 //
 // k_tree_rows reads a segment's keys once for each 16 rows, k_tree_tile once for
 // all, but spends about 10 us where a CTA's segment begins and ends.  With few
-// segments, each CTA has a part of one, and the tiles win from 25 rows on;
-// where CTAs have ends of several, from about 37 (us, rows against tiles; 8 key
-// heads of 128, bfloat16 queries, average rows and keys):
-//   1 sequence of 32768    24 rows  51 / 50      32 rows   51 / 51
-//   1 sequence of 65536    32 rows  85 / 75      48 rows  120 / 74
-//   16 sequences of 2100   24 rows  57 / 68      36 rows   70 / 67     44 rows  81 / 69
-//   64 sequences of 590    24 rows  74 / 116     36 rows   99 / 115    44 rows 117 / 121
-//   (binary16 queries, e5m2, 16 of 2100: 24 rows 60 / 74, 36 rows 75 / 73; heads
-//   of 64: 24 rows 40 / 52, 36 rows 52 / 52, 48 rows 62 / 53)
+// segments, each CTA has a part of one, and the tiles win as soon as rows fill
+// more than a block of 16; where CTAs have ends of several, from about 33 rows
+// on (us, rows against tiles; 8 key heads of 128, bfloat16 queries, average
+// rows and keys):
+//   1 sequence of 32768    16 rows  34 / 44      24 rows   50 / 45
+//   1 sequence of 65536    32 rows  86 / 67      48 rows  121 / 68
+//   16 sequences of 2100   24 rows  55 / 58      28 rows   59 / 58     36 rows  68 / 58
+//   64 sequences of 590    32 rows  86 / 105     36 rows   95 / 106    44 rows 113 / 106
+//   (binary16 queries, e5m2, 16 of 2100: 28 rows 66 / 65, 36 rows 74 / 65; heads
+//   of 64: 24 rows 39 / 50, 36 rows 51 / 50, 48 rows 62 / 51)
 // Tiles of 256 rows against two blocks of 128: 16 sequences of 2100, 140 rows,
-// 77 / 115.  Blocks of 16 rows against two of 8, with half the CTAs on an SM: 16
+// 74 / 115.  Blocks of 16 rows against two of 8, with half the CTAs on an SM: 16
 // sequences of 2100, 12 rows, 37 / 35; 1 of 65536, 32 rows, 85 / 103; 64 of
 // 590, 24 rows, 74 / 70.
 inline Plan plan(int64_t tokens, int64_t B, int64_t Hq, int64_t Hk, int64_t D, bool boxes) {
     Plan p{};
     const int64_t G = Hq / Hk;
     const int64_t per = ((tokens + B - 1) / B) * G;  // rows of an average sequence
-    p.tiles = boxes && (D == 64 || D == 128) && per > (2 * B * Hk >= 160 ? 36 : 24);
+    p.tiles = boxes && (D == 64 || D == 128) && per > (2 * B * Hk >= 160 ? 32 : 16);
     p.rows = p.tiles ? (per > 128 ? 256 : 128) : per > 8 && D <= 128 ? 16 : 8;
     const int64_t ctas = p.tiles ? 160 : 608;
     // every sequence ends in at most one block that is not full

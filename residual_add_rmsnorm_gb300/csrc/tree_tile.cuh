@@ -50,6 +50,7 @@ namespace rarn {
 namespace tree {
 
 constexpr int kTileKeys = 128;   // keys of a tile
+static_assert(kTileKeys != kTile, "begin_units tells the kernels apart");
 constexpr int kTileRows = 128;   // rows of a pipeline
 constexpr int kPass = 64;        // keys of a pass of the softmax, half a tile
 constexpr int kBox = kBoxSlots;  // slots of the smallest TMA box
@@ -117,7 +118,8 @@ struct Walk {
         bool found = false;
         while (a < hi) {
             const Seq q = seq_of(p, sb, rows, kTileKeys);
-            const int units = (int)units_of(p, q);
+            constexpr int kBegin = begin_units(kTileKeys);
+            const int units = (int)units_of(p, q, kTileKeys);
             if (a < bs + units) {
                 const int each = q.tiles + kBegin;
                 const int w = (unsigned)(a - bs) / (unsigned)each;
