@@ -687,11 +687,12 @@ rarn_status rarn_kv_cache_read(rarn_heads k_out, rarn_heads v_out, const rarn_kv
  * computed (bit 4) where they name more rows than there are.
  *
  * q, out: one 16-bit type.  Codes enter both products exactly, and a query
- * row with every bit down to 2^-18 of its largest magnitude; softmax
+ * row with every bit down to 2^-17 of its largest magnitude; softmax
  * statistics and sums are in binary32, the softmax weights, times their
  * value's scale, rounded to binary16 (11 bits) for the second product, where
- * what is under 2^-28 of a row's largest is lost.  A row whose queries are not
- * all finite, or that sees a key with a NaN code, is NaN.
+ * what is under 2^-27 of the row's largest weight times the largest value scale
+ * is lost.  A row whose queries are not all finite, or that sees a key with a
+ * NaN code, is NaN.
  * head_dim 64, 96, 128, 192 or 256; q 16-byte aligned with strides multiples
  * of 8 elements (else RARN_ERR_UNSUPPORTED); table_width * page_size at most
  * 2^31 - 4096.  Sequences of many rows (drafted tokens x query heads of a key

@@ -41,7 +41,7 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 struct Join {
     int first, last;  // CTAs whose parts add up to it (last < 0: nothing to add)
     int row0, n;      // its sequence's first drafted token, and how many
-    int head, block, unused0, unused1;
+    int head, block, pad[2];
 };
 
 struct Params {
@@ -547,9 +547,9 @@ __device__ __forceinline__ void issue_step(const Params &p, const Segment &sg, c
 // The same by TMA, from one lane, where a step lies inside one page and its
 // scales are adjacent: the box of its keys' rows and that of its values', and
 // the two runs of scales.  `page` is the page's number, loaded ahead.  Slots
-// behind the sequence's end come along and are masked.  Measured against the
-// copies above (64 sequences of up to 8192 tokens, 8 key heads of 128, one
-// token each): see k_tree_rows.
+// behind the sequence's end come along and are masked.  64 sequences of up to
+// 8192 tokens, 8 key heads of 128, one token each: 125.5 us, with the copies
+// above 131.7 (both before segments' ends counted in the split).
 template <int D>
 __device__ __forceinline__ void issue_step_tma(const Params &p, const Segment &sg,
                                                const CUtensorMap *kmap, const CUtensorMap *vmap,
@@ -888,6 +888,13 @@ struct Smem {
 // copies in flight and their own running maxima and sums, so nothing in the
 // loop waits for another warp; they are joined through shared memory at the
 // end of the CTA's share of the segment.
+//
+// Bound by memory where sequences are long: 64 of up to 8192 tokens, 8 key
+// heads of 128, one token of 32 heads each, take 107 us with the join (5.1 TB/s,
+// 75 % of a copy's rate); the rest goes to the ends of 512 segments and to the
+// last CTAs.  One sequence's token takes 12 us, two launches and the chain of
+// lengths, page, keys and parts.  mma.sync serves up to 16 rows, whose products
+// take less than their keys' reading.
 template <int D, int NQ, int NP, bool kE5M2, int kStages, bool kTma>
 __global__ void __launch_bounds__(kThreads, NQ == 1 && D <= 128 ? 4 : 2)
     k_tree_rows(const Params p, const __grid_constant__ CUtensorMap kmap,
@@ -1062,7 +1069,10 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D <= 128 ? 4 : 2)
 
 // Adds the parts of the segments that no CTA covered wholly, in tile order.
 // kSplit warps share a row's parts: 1 where there are many segments of a few
-// parts, 8 where there are few of many (one long sequence: 76 parts each).
+// parts, 8 where there are few of many (one long sequence: 19 to 76 parts each).
+// Bound by instructions rather than by its reads, which come from L2: 128
+// segments of 256 rows in two or three parts, 8 us; two parts at a time there
+// (four: 10 us).
 template <int D, int kSplit>
 __global__ void __launch_bounds__(256) k_tree_join(const Params p, int rows) {
     constexpr int N = (D + 127) / 128;

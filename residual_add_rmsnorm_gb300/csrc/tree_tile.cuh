@@ -67,7 +67,7 @@ struct TileInfo {
     float vs[kTileKeys];  // value scale, 0 where there is no key
     uint32_t ok[4];       // keys that exist
     float vmax;           // largest finite |vs|
-    int unused[3];
+    int pad[3];       // to a multiple of 16 bytes
 };
 
 // Shared memory: the queries' pieces (over which pipeline 1's state is laid
@@ -483,8 +483,9 @@ __device__ __noinline__ float row_top(uint32_t ts, uint32_t ti, uint32_t v0, uin
 // the row first sees a key, such that its largest weight times the tile's
 // largest vs is 2^kCentre, and moves up only when one would pass 2^kHighest: a
 // pass over the scores serves where finding their maximum first took two.
-// What falls under 2^-24, 2^-28 of the largest term, is lost; 2^17 keys at
-// that edge would add up to half of binary16's own rounding.
+// What falls under 2^-24 of the product's units, 2^-27 of the row's largest weight times
+// the largest value scale, is lost; 2^16 keys at that edge would add up to
+// half of binary16's own rounding.
 struct RowLane {
     float off;   // of the own row
     bool set;    // the offset is chosen (rows that are not there count as such)
@@ -533,7 +534,8 @@ __device__ __noinline__ void scale_down(uint32_t to, bool any, uint32_t ts, int 
 // `ti`), in binary16 over the scores' columns.  Where a score is more than
 // `most` over its row's offset, all that the row has so far is scaled down
 // first, once the products under way are in (`settled`), so that it comes to
-// `centre`.  kEdge: only keys whose bits of v0, v1 (the own row's) are set.
+// `centre` or up to one under it: by a power of two, which rounds no weight
+// anew.  kEdge: only keys whose bits of v0, v1 (the own row's) are set.
 template <int D, bool kEdge, class Settled>
 __device__ __forceinline__ bool row_weights(uint32_t ts, uint32_t to, bool any, uint32_t ti,
                                             uint32_t v0, uint32_t v1, float most, float centre,
@@ -581,7 +583,7 @@ __device__ __forceinline__ bool row_weights(uint32_t ts, uint32_t to, bool any, 
                 float high = top[i];
                 high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 1));
                 high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 2));
-                d[i] = high > most ? high - centre : 0.f;
+                d[i] = high > most ? ceilf(high - centre) : 0.f;
                 const float q = exp2_fast(-d[i]);
                 row.l[i] = mul2(row.l[i], two(q, q));
                 row.sub[i] -= d[i];
@@ -998,7 +1000,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (kTwo || pipe == 0) {
                 // Q's e4m3 pieces, each row scaled by a power of two that
                 // brings its largest magnitude to [128, 256): piece u is the
-                // rounded rest.  What is under 2^-18 of the row's largest is
+                // rounded rest.  What is under 2^-17 of the row's largest is
                 // lost.  A row that is not finite becomes NaN.  D / 8 lanes
                 // read a row, four loads at a time.
                 constexpr int kLanes = D / 8, kSide = 32 / kLanes, kN = 32 / kSide, kB = 4;

@@ -10,10 +10,16 @@ Bounds (u = 2^-24, binary32's half step; h(t) = eps(t) / 2, a storage type's):
     within half a step of the format at u, plus 2^-18 of |u|'s terms.
   * read back: one product and one rounding: h(t) + 2^-23.
   * attention: with A the largest sum |q_d K_d| * scale of a row, the scores are
-    off by at most D 2^-22 A (a tensor core's binary32 sums may truncate), the
-    weights by e^that - 1 and by binary16's rounding 2^-11 (their divisor too,
-    but for that rounding), the L-term sums by L 2^-22: all times
-    sum p_j |V_j|, then one rounding of the result.
+    off by at most D 2^-22 A (a tensor core's binary32 sums may truncate), and by
+    2^-17 max|q| sum |K_d| * scale for the queries' 8-bit pieces (the row is scaled
+    to a largest magnitude in [2^7, 2^8) and the last piece's step is 2^-9: an
+    element loses at most 2^-10); the weights by e^that - 1 and by binary16's
+    rounding 2^-11 (their divisor too, but for that rounding), the L-term sums
+    by L 2^-22: all times sum p_j |V_j|.  Weights times value scales that are
+    subnormal in binary16 are off by up to 2^-25 instead: the row's largest
+    weight w times 2^e, the power of two at or over a tile's largest value scale
+    m (2^e < 2 m), is held at 2^3 or more, so that 2^-25 is at most 2^-27 w m, a
+    key, times its code.  Then one rounding of the result.
 """
 from __future__ import annotations
 
@@ -96,9 +102,10 @@ def check_codes(codes, scale, want, mag, fmt, mode, what=""):
     assert not bad.any(), f"{what}: {int(bad.sum())} codes off, {float((err / tol).max()):.3g} tol"
 
 
-def attention(q, k, v, visible, scale):
-    """One sequence: q [n, Hq, D], k, v [L, Hk, D] binary64, visible [n, L].
-    (out, its bound without the last rounding)."""
+def attention(q, k, v, visible, scale, codes=None):
+    """One sequence: q [n, Hq, D], k, v [L, Hk, D] binary64, visible [n, L];
+    codes [L, Hk, D]: magnitudes of the values' codes times the largest value
+    scale of their head.  (out, its bound without the last rounding)."""
     n, Hq, D = q.shape
     L, Hk = k.shape[0], k.shape[1]
     G = Hq // Hk
@@ -113,9 +120,13 @@ def attention(q, k, v, visible, scale):
             s = (kh[w] @ q[i, h]) * scale
             p = torch.softmax(s, 0)
             A = float(((kh[w].abs() @ q[i, h].abs()) * scale).max())
-            rel = 2.0 ** -11 + 2 * math.expm1(D * 2.0 ** -22 * A) + L * 2.0 ** -22 + 2.0 ** -20
+            cut = float(kh[w].abs().sum(-1).max() * q[i, h].abs().max()) * scale * 2.0 ** -17
+            rel = (2.0 ** -11 + 2 * math.expm1(D * 2.0 ** -22 * A + cut) + L * 2.0 ** -22 +
+                   2.0 ** -20)
             out[i, h] = p @ vh[w]
             tol[i, h] = rel * (p @ vh[w].abs())
+            if codes is not None:
+                tol[i, h] += 2.0 ** -27 * p.max() * codes[w, h // G].sum(0)
     return out, tol
 
 

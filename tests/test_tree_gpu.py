@@ -102,8 +102,12 @@ class Case:
             k = self.values(c.k, c.k_scale, b, L)
             v = self.values(c.v, c.v_scale, b, L)
             s = int(self.starts[b])
+            at = self.slots(b, L)
+            codes = R.decode(rows_at(c.v, at, self.page), self.fmt).abs()
+            codes *= (rows_at(c.v_scale, at, self.page).to(R.F64).abs().amax(0)[None, :, None]
+                      if self.mode == "row" else float(c.v_scale))
             want, tol = R.attention(self.q[s:s + n], k, v, self.visible(b),
-                                    self.D ** -0.5 if scale is None else scale)
+                                    self.D ** -0.5 if scale is None else scale, codes)
             R.check_attention(got[s:s + n], want, tol, f"sequence {b}")
 
 
@@ -420,3 +424,97 @@ def test_decode_steps_with_the_library():
     rarn.kv_cache_read(cache, pages, torch.tensor([0, done], dtype=torch.int32, device=dev), *out)
     assert ((out[1].cpu().to(R.F64) - vv).abs() <= 2.0 ** -8 * vv.abs()).all()
     assert rarn.watchdog() == 0
+
+
+# Rows enough for the tensor-memory kernel: its box sizes, both pipelines' ways
+# of sharing rows, types, head sizes, and segments of one tile among others.
+MANY_ROWS = {
+    "short and long": dict(ctx=[(37 * i) % 390 for i in range(250)],
+                           new=[17 + i % 4 for i in range(250)], Hq=4, Hk=2, D=64),
+    "short and long, 256 rows": dict(ctx=[(61 * i) % 700 for i in range(60)],
+                                     new=[66 + i % 9 for i in range(60)], Hq=4, Hk=2, D=128),
+    "page 8": dict(ctx=[300, 7], new=[30, 21], Hq=8, Hk=2, D=128, page=8, layout="tokens"),
+    "page 40": dict(ctx=[333], new=[33], Hq=8, Hk=2, D=64, page=40, layout="pool"),
+    "page 96": dict(ctx=[200, 95, 96], new=[9, 30, 17], Hq=8, Hk=2, D=128, page=96),
+    "page 128": dict(ctx=[130, 127, 128], new=[30, 10, 20], Hq=8, Hk=1, D=128, page=128),
+    "page 256": dict(ctx=[130, 500], new=[30, 12], Hq=8, Hk=2, D=64, page=256, layout="pool"),
+    "f16, 256 rows": dict(ctx=[2000, 31], new=[40, 21], Hq=16, Hk=2, D=128, dt="f16"),
+    "f16, 256 rows, D 64, e5m2": dict(ctx=[700, 0, 90], new=[30, 41, 20], Hq=16, Hk=2, D=64,
+                                      dt="f16", fmt="e5m2", page=32),
+    "e5m2, 256 rows, one scale": dict(ctx=[1300], new=[64], Hq=10, Hk=2, D=128, fmt="e5m2",
+                                      mode="tensor", page=64),
+    "long": dict(ctx=[9000], new=[20], Hq=4, Hk=2, D=64),
+    "long, 256 rows": dict(ctx=[9000], new=[50], Hq=8, Hk=2, D=128, page=64),
+}
+
+
+@pytest.mark.parametrize("name", MANY_ROWS)
+def test_many_rows(name):
+    c = Case(**MANY_ROWS[name])
+    out = c.run()
+    assert rarn.watchdog() == 0
+    c.check(out)
+    assert torch.equal(c.run(out=torch.zeros_like(out)), out)
+
+
+@pytest.mark.parametrize("n,G,D,dt", [(2, 4, 128, "bf16"), (20, 2, 128, "bf16"),
+                                      (20, 2, 64, "f16"), (40, 4, 128, "f16"),
+                                      (40, 4, 64, "bf16")])
+def test_scores_that_keep_growing(n, G, D, dt):
+    """Keys whose scales rise along the context, so that each row's largest
+    score moves up again and again, within a tile and from tile to tile."""
+    c = Case([900], [n], 2 * G, 2, D, dt=dt, seed=8)
+    L = 900 + n
+    at = c.slots(0, L).cuda()
+    grow = torch.linspace(0.2, 5.0, L, device="cuda")
+    c.cache.k_scale[at // 16, :, at % 16] *= grow[:, None]
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("n", [20, 80])
+def test_missing_pages_are_hidden_from_many_rows(n):
+    c = Case([300, 40], [n, 4], 4, 2, 128, mask="chain")
+    full = c.table.clone()
+    c.table[0, 2] = -1
+    c.table[0, 9] = 1 << 30
+    got = c.run().cpu()
+    assert rarn.watchdog() == INDEX_BIT
+    c.table = full
+    vis = c.visible(0)
+    vis[:, 32:48] = vis[:, 144:160] = False
+    k, v = (c.values(t, s, 0, 300 + n) for t, s in ((c.cache.k, c.cache.k_scale),
+                                                    (c.cache.v, c.cache.v_scale)))
+    R.check_attention(got[:n], *R.attention(c.q[:n], k, v, vis, 128 ** -0.5))
+
+
+@pytest.mark.parametrize("n", [20, 70])
+def test_graphs_of_many_rows_on_two_streams(n):
+    """Two captured calls with a workspace each, replayed at once, their
+    lengths changed after the capture."""
+    cases = [Case([900 - 7 * i, 40], [n, 3 + i], 8, 2, 128, seed=10 * i) for i in (1, 2)]
+    made = []
+    for c in cases:
+        N = c.q.shape[0]
+        a = dict(q=c.q.cuda(), page_table=c.table.cuda(), cache=c.cache,
+                 context_lens=torch.tensor([3, 5], dtype=torch.int32, device="cuda"),
+                 starts=torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda"),
+                 mask=c.mask.cuda(), out=torch.zeros(c.q.shape, dtype=c.dt, device="cuda"),
+                 workspace=torch.empty(rarn.tree_attention_workspace_bytes(N, 2, 8, 2, 128),
+                                       dtype=torch.uint8, device="cuda"))
+        rarn.tree_attention(**a)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            rarn.tree_attention(**a)
+        a["context_lens"].copy_(torch.tensor(c.ctx, dtype=torch.int32))
+        a["starts"].copy_(c.starts)
+        made.append((c, a, g, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for _, _, g, s in made:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert rarn.watchdog() == 0
+    for c, a, _, _ in made:
+        c.check(a["out"])
