@@ -717,6 +717,13 @@ rarn_status rarn_tree_attention(rarn_heads out, rarn_heads q, const rarn_kv_cach
 int64_t rarn_tree_attention_workspace_bytes(int64_t tokens, int64_t B, int64_t q_heads,
                                             int64_t kv_heads, int64_t D);
 
+/* Describe the kernel that a rarn_tree_attention call of these sizes gets (pure
+ * host logic): "tree.tiles rows=256", "tree.rows rows=8" or the like, rows
+ * being those of a block.  Writes a NUL-terminated description into out[cap];
+ * RARN_ERR_UNSUPPORTED (out says so) for sizes that the call rejects. */
+rarn_status rarn_plan_tree_attention(int64_t tokens, int64_t B, int64_t q_heads, int64_t kv_heads,
+                                     int64_t D, int64_t page_size, char *out, size_t cap);
+
 /* Rows that one launch sequence of rarn_gemm_add_rms_norm_noalloc covers for
  * a row length H: floor(floor((2^20 - 16) / (H / 128 + 1)) / 128) * 128
  * (16128 at H = 8192, 8064 at H = 16384); -1 if H is not supported. */

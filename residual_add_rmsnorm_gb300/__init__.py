@@ -45,7 +45,7 @@ __all__ = ["rms_norm", "fused_add_rms_norm", "reduce_add_rms_norm", "rms_norm_ho
            "ipc_export", "ipc_import", "ipc_close", "TP_MAX_RANKS", "TP_SIGNAL_BYTES",
            "IPC_HANDLE_BYTES", "qk_norm_rope", "KVCache", "kv_cache_write",
            "qk_norm_rope_kv_write", "kv_cache_read", "tree_attention",
-           "tree_attention_workspace_bytes", "ROTATION_STYLES"]
+           "tree_attention_workspace_bytes", "plan_tree_attention", "ROTATION_STYLES"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "librarn.so")
@@ -207,6 +207,8 @@ def library() -> ctypes.CDLL:
     lib.rarn_plan_gemm.argtypes = [i64, i64, i64, c_int, ctypes.c_int32, ctypes.c_char_p,
                                    ctypes.c_size_t]
     lib.rarn_plan_gemm.restype = c_int
+    lib.rarn_plan_tree_attention.argtypes = [i64] * 6 + [ctypes.c_char_p, ctypes.c_size_t]
+    lib.rarn_plan_tree_attention.restype = c_int
     lib.rarn_plan_fp8in.argtypes = [i64, i64, ctypes.c_int32, c_int, c_int, ctypes.c_int32,
                                     ctypes.c_int32, ctypes.c_char_p, ctypes.c_size_t]
     lib.rarn_plan_fp8in.restype = c_int
@@ -985,6 +987,18 @@ def tree_attention_workspace_bytes(tokens: int, sequences: int, q_heads: int, kv
     """Workspace bytes tree_attention needs for these sizes (-1: unsupported)."""
     return int(library().rarn_tree_attention_workspace_bytes(tokens, sequences, q_heads, kv_heads,
                                                              head_dim))
+
+
+def plan_tree_attention(tokens: int, sequences: int, q_heads: int, kv_heads: int, head_dim: int,
+                        page_size: int) -> str:
+    """Which kernel a tree_attention call of these sizes gets (host logic
+    only)."""
+    buf = ctypes.create_string_buffer(64)
+    st = library().rarn_plan_tree_attention(tokens, sequences, q_heads, kv_heads, head_dim,
+                                            page_size, buf, 64)
+    if st not in (0, 2):
+        _check(st, "rarn_plan_tree_attention")
+    return buf.value.decode()
 
 
 def tree_attention(q, cache: KVCache, page_table, context_lens, starts, mask=None,

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstdio>
 #include <utility>
 
 #include "../../include/rarn.h"
@@ -496,6 +497,25 @@ int64_t rarn_tree_attention_workspace_bytes(int64_t tokens, int64_t B, int64_t q
     const tree::Plan a = tree::plan(tokens, B, q_heads, kv_heads, D, false),
                      b = tree::plan(tokens, B, q_heads, kv_heads, D, true);
     return a.segments < kMaxItems ? std::max(a.bytes, b.bytes) : -1;
+}
+
+rarn_status rarn_plan_tree_attention(int64_t tokens, int64_t B, int64_t q_heads, int64_t kv_heads,
+                                     int64_t D, int64_t page_size, char *out, size_t cap) {
+    if (!out || cap == 0 || tokens < 0 || B < 0 || q_heads < 1 || kv_heads < 1 || page_size < 1)
+        return RARN_ERR_INVALID_ARG;
+    if (page_size > RARN_MAX_PAGE_SIZE ||
+        rarn_tree_attention_workspace_bytes(tokens, B, q_heads, kv_heads, D) < 0) {
+        snprintf(out, cap, "none: unsupported sizes");
+        return RARN_ERR_UNSUPPORTED;
+    }
+    if (tokens == 0 || B == 0) {
+        snprintf(out, cap, "none: no rows");
+        return RARN_OK;
+    }
+    const tree::Plan pl = tree::plan(tokens, B, q_heads, kv_heads, D,
+                                     page_size % tree::kBoxSlots == 0);
+    snprintf(out, cap, "tree.%s rows=%d", pl.tiles ? "tiles" : "rows", pl.rows);
+    return RARN_OK;
 }
 
 rarn_status rarn_tree_attention(rarn_heads out, rarn_heads q, const rarn_kv_cache *cache,

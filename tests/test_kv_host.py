@@ -316,3 +316,25 @@ def test_strides_of_dimensions_of_one_do_not_matter(lib):
     assert tree(lib, c, q=c.heads(2, 2, head_stride=65)) == UNSUPPORTED
     c = Call(Hq=1, Hk=1)
     assert tree(lib, c, q=c.heads(2, 1, head_stride=65)) == CUDA
+
+
+@pytest.mark.parametrize("args,want", [
+    ((1, 1, 32, 8, 128, 16), "tree.rows rows=8"), ((64, 64, 32, 8, 128, 16), "tree.rows rows=8"),
+    ((4, 1, 32, 8, 128, 16), "tree.rows rows=16"), ((5, 1, 32, 8, 128, 16), "tree.tiles rows=128"),
+    ((5, 1, 32, 8, 128, 12), "tree.rows rows=16"), ((50, 1, 32, 8, 256, 16), "tree.rows rows=8"),
+    ((64 * 8, 64, 32, 8, 128, 16), "tree.rows rows=16"),
+    ((64 * 9, 64, 32, 8, 128, 16), "tree.tiles rows=128"),
+    ((16 * 32, 16, 64, 8, 64, 8), "tree.tiles rows=256"),
+    ((0, 4, 8, 2, 64, 16), "none: no rows"),
+    ((4, 4, 8, 2, 80, 16), "none: unsupported sizes"),
+])
+def test_plan_tree_attention(lib, args, want):
+    assert rarn.plan_tree_attention(*args) == want
+
+
+def test_plan_tree_attention_refusals(lib):
+    buf = ctypes.create_string_buffer(64)
+    assert lib.rarn_plan_tree_attention(-1, 1, 8, 2, 64, 16, buf, 64) == INVALID
+    assert lib.rarn_plan_tree_attention(1, 1, 8, 2, 64, 0, buf, 64) == INVALID
+    assert lib.rarn_plan_tree_attention(1, 1, 8, 2, 64, 16, None, 64) == INVALID
+    assert lib.rarn_plan_tree_attention(1, 1, 8, 2, 64, 16, buf, 0) == INVALID

@@ -451,6 +451,8 @@ MANY_ROWS = {
 @pytest.mark.parametrize("name", MANY_ROWS)
 def test_many_rows(name):
     c = Case(**MANY_ROWS[name])
+    assert rarn.plan_tree_attention(c.q.shape[0], len(c.ctx), c.Hq, c.Hk, c.D,
+                                    c.page).startswith("tree.tiles")
     out = c.run()
     assert rarn.watchdog() == 0
     c.check(out)
