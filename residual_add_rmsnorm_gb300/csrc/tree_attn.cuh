@@ -428,7 +428,9 @@ __device__ __forceinline__ void load_row(uint32_t (&w)[N], uint32_t base, int ro
 constexpr float kSlack = 3.f;
 // Weights enter the second product in binary16 as p vs / ref * 2^12, at most
 // 2^15: what falls under 2^-24 of that, 2^-36 of the largest term, is lost,
-// which 2^20 keys cannot add up to a rounding of the result.
+// which 2^20 keys cannot add up to a rounding of the result.  The divisor sums
+// the weights before that rounding (64 decode sequences 107 -> 103 us against
+// taking each weight's rounding into it).
 constexpr float kWeightScale = 4096.f;
 
 // A warp's running softmax and accumulators.
@@ -632,9 +634,13 @@ __device__ __forceinline__ void consume_step(const Params &p, const Segment &sg,
     uint32_t ok[1];
     lds(ok, stage.tail + L::kOk);
     // s[n][0..1]: key g, rows 2c, 2c + 1; s[n][2..3]: key g + 8
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[n][i] *= (i < 2 ? ks0 : ks1) * cs[n][i & 1];
     const bool edge = ok[0] != 0xffffu || j0 + kStep > sg.s.ctx;  // uniform
     uint32_t hidden = 0;  // bit 4 n + i: s[n][i] is not visible
-    if (edge) {
+    if (__builtin_expect(edge, 0)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int j = g + 8 * h, d = j0 + j - sg.s.ctx;
@@ -646,28 +652,25 @@ __device__ __forceinline__ void consume_step(const Params &p, const Segment &sg,
                 for (int e = 0; e < 2; ++e) {
                     const int i = tok[n][e];
                     const bool vis = exists && i >= 0 && (d < 0 || sees(p, sg.row0 + i, i, d));
-                    if (!vis) hidden |= 1u << (4 * n + 2 * h + e);
+                    if (!vis) {
+                        hidden |= 1u << (4 * n + 2 * h + e);
+                        s[n][2 * h + e] = -INFINITY;
+                    }
                 }
         }
     }
-    bool grow = false;
+    bool grow = !(fabsf(vs0) <= rs.ref) || !(fabsf(vs1) <= rs.ref);
     float top[NQ][2];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s[n][i] = s[n][i] * ((i < 2 ? ks0 : ks1) * cs[n][i & 1]);
-            if (edge && ((hidden >> (4 * n + i)) & 1u)) s[n][i] = -INFINITY;
-        }
         top[n][0] = fmaxf(s[n][0], s[n][2]);
         top[n][1] = fmaxf(s[n][1], s[n][3]);
         grow |= top[n][0] > rs.m[n][0] + kSlack || top[n][1] > rs.m[n][1] + kSlack;
     }
-    const float v0 = fabsf(vs0), v1 = fabsf(vs1);
-    const float vmax = fmaxf(v0 < INFINITY ? v0 : 0.f, v1 < INFINITY ? v1 : 0.f);
-    grow |= vmax > rs.ref;
     if (__any_sync(0xffffffffu, grow)) {
-        float vm = max_over_keys(vmax);  // the same in every c
+        const float v0 = fabsf(vs0), v1 = fabsf(vs1);  // of finite ones the largest
+        const float vm = max_over_keys(
+            fmaxf(v0 < INFINITY ? v0 : 0.f, v1 < INFINITY ? v1 : 0.f));  // the same in every c
         const float ref = vm > rs.ref ? 2.f * vm < INFINITY ? 2.f * vm : vm : rs.ref;
         const float rr = rs.ref / ref;
         rs.ref = ref;
@@ -689,12 +692,6 @@ __device__ __forceinline__ void consume_step(const Params &p, const Segment &sg,
             }
     }
     const float w0 = vs0 * rs.by, w1 = vs1 * rs.by;
-    // The divisor sums the weights as the product takes them, so that their
-    // rounding is one of the average's weights and not of its size (a lone
-    // key's value comes back exactly).  A scale under 2^-12 of the largest
-    // would make that rounding large: there the weights themselves.
-    const float iw0 = fabsf(w0) >= 1.f ? rcp_fast(w0) : 0.f;
-    const float iw1 = fabsf(w1) >= 1.f ? rcp_fast(w1) : 0.f;
     uint32_t pb[NQ][2];
     float x[NQ][4];
 #pragma unroll
@@ -704,16 +701,18 @@ __device__ __forceinline__ void consume_step(const Params &p, const Segment &sg,
         for (int i = 0; i < 4; ++i) {
             pr[i] = exp2_fast(s[n][i] - rs.off[n][i & 1]);
             x[n][i] = pr[i] * (i < 2 ? w0 : w1);
-            if (edge && ((hidden >> (4 * n + i)) & 1u)) x[n][i] = 0.f;
+        }
+        if (__builtin_expect(edge, 0)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if ((hidden >> (4 * n + i)) & 1u) x[n][i] = 0.f;
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint32_t packed = pack_h2(x[n][2 * h], x[n][2 * h + 1]);
             pb[n][h] = transpose_8x8(packed);
-            const float2 r = DT<__half>::w2f(packed);
-            const float iw = h ? iw1 : iw0;
-            rs.l[n][0] += fmaf(r.x - x[n][2 * h], iw, pr[2 * h]);
-            rs.l[n][1] += fmaf(r.y - x[n][2 * h + 1], iw, pr[2 * h + 1]);
+            rs.l[n][0] += pr[2 * h];
+            rs.l[n][1] += pr[2 * h + 1];
         }
     }
     // values of keys 2c, 2c + 1, 2c + 8, 2c + 9, this lane's eighth of the row
@@ -721,7 +720,7 @@ __device__ __forceinline__ void consume_step(const Params &p, const Segment &sg,
 #pragma unroll
     for (int h = 0; h < 4; ++h)
         load_row<D>(v[h], stage.codes + L::kV, 2 * c + (h & 1) + (h >> 1) * 8, g * (D / 8));
-    if (edge) {
+    if (__builtin_expect(edge, 0)) {
         // Values that are NaN or infinite and not visible to every row: in the
         // product 0 times such a value would be NaN, so those keys leave it
         // (their codes become zero) and are added to the rows that see them.
@@ -890,9 +889,10 @@ struct Smem {
 // end of the CTA's share of the segment.
 //
 // Bound by memory where sequences are long: 64 of up to 8192 tokens, 8 key
-// heads of 128, one token of 32 heads each, take 107 us with the join (5.1 TB/s,
-// 75 % of a copy's rate); the rest goes to the ends of 512 segments and to the
-// last CTAs.  One sequence's token takes 12 us, two launches and the chain of
+// heads of 128, one token of 32 heads each, take 101 us with the join (5.4 TB/s,
+// 80 % of a copy's rate); there 60 % of all issue slots and half the ALU's are
+// taken, by the values' conversion above all, and the ends of 512 segments come
+// on top.  One sequence's token takes 12 us, two launches and the chain of
 // lengths, page, keys and parts.  mma.sync serves up to 16 rows, whose products
 // take less than their keys' reading.
 template <int D, int NQ, int NP, bool kE5M2, int kStages, bool kTma>
