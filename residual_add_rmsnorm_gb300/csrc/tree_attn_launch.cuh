@@ -89,7 +89,7 @@ inline cudaError_t launch_rows(const Params &p, const Plan &pl, int num_sms, boo
 template <int D, int NP, bool kE5M2, bool kTma>
 inline cudaError_t launch_dim(const Params &p, const Plan &pl, int num_sms, bool pdl,
                               cudaStream_t st) {
-    if constexpr (D <= 128)
+    if constexpr (D <= 192)
         if (pl.rows == 16) return launch_rows<D, 2, NP, kE5M2, kTma>(p, pl, num_sms, pdl, st);
     return launch_rows<D, 1, NP, kE5M2, kTma>(p, pl, num_sms, pdl, st);
 }

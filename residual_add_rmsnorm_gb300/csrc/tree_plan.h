@@ -37,13 +37,16 @@ inline bool dim_ok(int64_t D) { return D == 64 || D == 96 || D == 128 || D == 19
 // Tiles of 256 rows against two blocks of 128: 16 sequences of 2100, 140 rows,
 // 74 / 115.  Blocks of 16 rows against two of 8, with half the CTAs on an SM: 16
 // sequences of 2100, 12 rows, 37 / 35; 1 of 65536, 32 rows, 85 / 103; 64 of
-// 590, 24 rows, 74 / 70.
+// 590, 24 rows, 74 / 70.  Heads of 192, whose 16 rows fill the registers: 16
+// sequences of 2100, 24 rows, 73 / 72, 36 rows 90 / 97, 96 rows 198 / 231; 1 of
+// 32768, 24 rows, 64 / 60, 48 rows 88 / 105.  Heads of 256 leave no room.
 inline Plan plan(int64_t tokens, int64_t B, int64_t Hq, int64_t Hk, int64_t D, bool boxes) {
     Plan p{};
     const int64_t G = Hq / Hk;
     const int64_t per = ((tokens + B - 1) / B) * G;  // rows of an average sequence
     p.tiles = boxes && (D == 64 || D == 128) && per > (2 * B * Hk >= 160 ? 32 : 16);
-    p.rows = p.tiles ? (per > 128 ? 256 : 128) : per > 8 && D <= 128 ? 16 : 8;
+    const bool sixteen = D <= 128 ? per > 8 : D <= 192 && per > 32;
+    p.rows = p.tiles ? (per > 128 ? 256 : 128) : sixteen ? 16 : 8;
     const int64_t ctas = p.tiles ? 160 : 608;
     // every sequence ends in at most one block that is not full
     p.segments = Hk * (tokens * G / p.rows + B);

@@ -325,6 +325,7 @@ def test_strides_of_dimensions_of_one_do_not_matter(lib):
     ((64 * 8, 64, 32, 8, 128, 16), "tree.rows rows=16"),
     ((64 * 9, 64, 32, 8, 128, 16), "tree.tiles rows=128"),
     ((16 * 32, 16, 64, 8, 64, 8), "tree.tiles rows=256"),
+    ((8, 1, 32, 8, 192, 16), "tree.rows rows=8"), ((9, 1, 32, 8, 192, 16), "tree.rows rows=16"),
     ((0, 4, 8, 2, 64, 16), "none: no rows"),
     ((4, 4, 8, 2, 80, 16), "none: unsupported sizes"),
 ])

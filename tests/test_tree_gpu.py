@@ -146,6 +146,8 @@ CASES = {
     "sharp, many rows": dict(ctx=[900], new=[40], Hq=16, Hk=2, D=128, gain=6.0, mode="tensor"),
     "f16, many rows": dict(ctx=[300, 44], new=[30, 17], Hq=8, Hk=4, D=128, dt="f16", page=24),
     "group of 3": dict(ctx=[45, 600], new=[11, 23], Hq=9, Hk=3, D=192, dt="f16"),
+    "D 192, 16 rows": dict(ctx=[45, 600], new=[11, 23], Hq=12, Hk=3, D=192, dt="f16", page=7),
+    "D 192, 16 rows, e5m2": dict(ctx=[300], new=[30], Hq=8, Hk=2, D=192, fmt="e5m2"),
 }
 
 
