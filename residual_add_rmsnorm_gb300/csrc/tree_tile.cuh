@@ -516,6 +516,8 @@ __device__ __noinline__ void scale_down(uint32_t to, bool any, uint32_t ts, int 
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) tmem_scale32(to + 32 * c, by);
     }
+    // the pass's earlier weights are stored asynchronously, in another shape
+    if (chunks) tmem_st_wait();
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
         uint32_t w[16];
