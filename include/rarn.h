@@ -691,8 +691,10 @@ rarn_status rarn_kv_cache_read(rarn_heads k_out, rarn_heads v_out, const rarn_kv
  * statistics and sums are in binary32, the softmax weights, times their
  * value's scale, rounded to binary16 (11 bits) for the second product, where
  * what is under 2^-27 of the row's largest weight times the largest value scale
- * is lost.  A row whose queries are not all finite, or that sees a key with a
- * NaN code, is NaN.
+ * is lost.  Scores (scale * q . K_j) from 2^27 on, whose binary32 steps are no
+ * longer small, leave a row the values of its largest ones; a row whose scores
+ * differ by more than binary32 holds may be NaN.  A row whose queries are not all
+ * finite, or that sees a key with a NaN code, is NaN.
  * head_dim 64, 96, 128, 192 or 256; q 16-byte aligned with strides multiples
  * of 8 elements (else RARN_ERR_UNSUPPORTED); table_width * page_size at most
  * 2^31 - 4096.  Sequences of many rows (drafted tokens x query heads of a key

@@ -44,6 +44,7 @@
 #include <cstddef>
 
 #include "tree_attn.cuh"
+#include "tree_offset.h"
 #include "tree_plan.h"
 
 namespace rarn {
@@ -495,9 +496,6 @@ struct RowLane {
     uint64_t l[4];
 };
 
-constexpr float kCentre = 4.f;
-constexpr float kHighest = 15.f;
-
 // A tile's ceil(log2) of its largest value scale, within what binary32 sums of
 // weights bear.
 __device__ __forceinline__ float lift_of(float vmax) {
@@ -537,12 +535,15 @@ __device__ __noinline__ void scale_down(uint32_t to, bool any, uint32_t ts, int 
 // `most` over its row's offset, all that the row has so far is scaled down
 // first, once the products under way are in (`settled`), so that it comes to
 // `centre` or up to one under it: by a power of two, which rounds no weight
-// anew.  kEdge: only keys whose bits of v0, v1 (the own row's) are set.
+// anew that stays normal in binary16.  This is done kMoves times at most for 32
+// keys, nearly always once; a score that is over even then counts as `most`.
+// kEdge: only keys whose bits of v0, v1 (the own row's) are set.
 template <int D, bool kEdge, class Settled>
 __device__ __forceinline__ bool row_weights(uint32_t ts, uint32_t to, bool any, uint32_t ti,
                                             uint32_t v0, uint32_t v1, float most, float centre,
                                             RowLane &row, const Settled &settled) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c2 = 2 * (lane & 3);
+    int moves = 0;  // of the offset, for these keys
 #pragma unroll 1
     for (int c = 0; c < kPass / 32;) {
         float s[2][16];
@@ -579,22 +580,31 @@ __device__ __forceinline__ bool row_weights(uint32_t ts, uint32_t to, bool any, 
         }
         if (__any_sync(0xffffffffu, over)) {
             // rare: the offset moves up under what is there; then again
-            float d[4];
+            if (moves < kMoves) {
+                ++moves;
+                float d[4], off[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float high = top[i];
-                high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 1));
-                high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 2));
-                d[i] = high > most ? ceilf(high - centre) : 0.f;
-                const float q = exp2_fast(-d[i]);
-                row.l[i] = mul2(row.l[i], two(q, q));
-                row.sub[i] -= d[i];
+                for (int i = 0; i < 4; ++i) {
+                    float high = top[i];
+                    high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 1));
+                    high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 2));
+                    d[i] = 0.f;
+                    if (high > most) row.sub[i] = moved_offset(row.sub[i], high, centre, &d[i]);
+                    off[i] = -row.sub[i];
+                    const float q = exp2_fast(-d[i]);
+                    row.l[i] = mul2(row.l[i], two(q, q));
+                }
+                const float down = rows_to_owner(d);
+                row.off = rows_to_owner(off);
+                if (any && !settled()) return false;
+                scale_down<D>(to, any, ts, c, down);
+                continue;
             }
-            const float down = rows_to_owner(d);
-            row.off += down;
-            if (any && !settled()) return false;
-            scale_down<D>(to, any, ts, c, down);
-            continue;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {  // a NaN stays
+                s[0][j] = s[0][j] > most ? most : s[0][j];
+                s[1][j] = s[1][j] > most ? most : s[1][j];
+            }
         }
         uint64_t vs[4];
 #pragma unroll
@@ -620,6 +630,7 @@ __device__ __forceinline__ bool row_weights(uint32_t ts, uint32_t to, bool any, 
         }
         tmem_frag_store(ts + 16 * c, w[0]);  // over columns that are read
         tmem_frag_store(ts + 16 * c + kHalfRows, w[1]);
+        moves = 0;
         ++c;
     }
     return true;
@@ -1120,7 +1131,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             const float top = edge ? row_top<true>(tsh, ti, v0, v1, back)
                                                    : row_top<false>(tsh, ti, 0, 0, back);
                             if (!row.set && top > -INFINITY) {
-                                row.off = top - (kCentre - lift);
+                                row.off = first_offset(top, kCentre - lift);
                                 row.set = true;
                             }
                             rows_from_owner(-row.off, row.sub);
