@@ -940,8 +940,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 // Behind the context a value may be hidden from some rows, and
                 // 0 times NaN or infinity would reach them: such elements
                 // become zero here and are added at the end to the rows that
-                // see them.
-                const bool past = (t + 1) * kTileKeys > walk.sg.s.ctx;
+                // see them.  The context's own reach every row as they are.
+                const int hideable = walk.sg.s.ctx - t * kTileKeys;  // rows from here on
                 bool any = false;
 #pragma unroll 1
                 for (int i = 0; i < kLoads; ++i) {
@@ -952,7 +952,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     const int row = cw * 32 + r;
                     uint4 c = gemm::lds128(from + code_at<D>(row, x));
                     if (!((ok >> r) & 1u)) c = make_uint4(0, 0, 0, 0);
-                    if (past) {
+                    if (row >= hideable) {
                         const uint4 f = make_uint4(finite_codes<kE5M2>(c.x), finite_codes<kE5M2>(c.y),
                                                    finite_codes<kE5M2>(c.z), finite_codes<kE5M2>(c.w));
                         any |= c.x != f.x || c.y != f.y || c.z != f.z || c.w != f.w;
