@@ -1208,8 +1208,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (done) gemm::tmem_ld32(to + 32 * c, o);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        float v = done && f0 != 0.f ? o[j] * f0 : 0.f;
-                        if (joined && f1 != 0.f) v += buf[(32 * c + j) * kTileRows + r] * f1;
+                        // (a factor of zero too: it keeps a NaN)
+                        float v = done ? o[j] * f0 : 0.f;
+                        if (joined) v += buf[(32 * c + j) * kTileRows + r] * f1;
                         o[j] = v * by;
                     }
                     if (sh_nonfinite && live)

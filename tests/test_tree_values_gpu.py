@@ -6,6 +6,7 @@ import torch
 import kv_ref as R
 import residual_add_rmsnorm_gb300 as rarn
 from test_tree_gpu import Case
+from test_tree_scores_gpu import set_scores
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +53,19 @@ def test_context_values_that_are_not_finite(n, G, D, fmt, back):
         got[:, G:, 9] = 0
         want[:, G:, 9] = 0
     R.check_attention(got, want, tol)
+
+
+@pytest.mark.parametrize("n,G,D,fmt", SIZES)
+def test_a_nan_of_no_weight(n, G, D, fmt):
+    """A NaN value in keys whose weights are zero in binary32 beside later
+    ones' makes its rows NaN all the same."""
+    c = Case([700], [n], 2 * G, 2, D, fmt=fmt, seed=32)
+    targets = torch.zeros(700 + n)
+    targets[300:] = 400.0                    # log2 units
+    set_scores(c, 0, targets)
+    at = c.slots(0, 700)[5].item()
+    c.cache.v[at // 16, 0, at % 16, 3] = 0x7f if fmt == "e4m3" else 0x7e
+    got = c.run().cpu()
+    assert torch.isnan(got[:, :G, 3]).all()
+    got[:, :G, 3] = 0
+    assert torch.isfinite(got).all()
