@@ -839,6 +839,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // Item t of a segment that began at tile n is key tile n + t.
         auto scores = [&](int t, int half, bool last) {
             const int stage = (n + t) % S::kStagesK;
+            // The tile that had this stage before is the other pipeline's.  Were
+            // it still on its way, the wait for this one's phase would take the
+            // phase before that for it; the tile's figures come after the
+            // release of the stage, and so after that tile.
+            if (!kTwo && half == 0 &&
+                !tile_wait(p, bar(B_INFO + ((n + t) & (kInfos - 1))), ((n + t) >> 3) & 1,
+                           &sh_abort))
+                return false;
             if (half == 0 &&
                 !tile_wait(p, bar(B_KFULL + stage), ((n + t) / S::kStagesK) & 1, &sh_abort))
                 return false;
