@@ -530,6 +530,21 @@ __device__ __noinline__ void scale_down(uint32_t to, bool any, uint32_t ts, int 
     tmem_st_wait();
 }
 
+// moved_offset out of line, {sub, down}: rare, and the roles share an instruction
+// cache.
+static __device__ __noinline__ float2 move_offset(float sub, float high, float centre) {
+    float2 r;
+    r.x = moved_offset(sub, high, centre, &r.y);
+    return r;
+}
+
+// The smaller; NaN where a is.
+__device__ __forceinline__ float cut(float a, float most) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(most));
+    return r;
+}
+
 // A warp's weights of a pass (S at `ts`, columns times the keys' factors at
 // `ti`), in binary16 over the scores' columns.  Where a score is more than
 // `most` over its row's offset, all that the row has so far is scaled down
@@ -589,7 +604,11 @@ __device__ __forceinline__ bool row_weights(uint32_t ts, uint32_t to, bool any, 
                     high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 1));
                     high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 2));
                     d[i] = 0.f;
-                    if (high > most) row.sub[i] = moved_offset(row.sub[i], high, centre, &d[i]);
+                    if (high > most) {
+                        const float2 moved = move_offset(row.sub[i], high, centre);
+                        row.sub[i] = moved.x;
+                        d[i] = moved.y;
+                    }
                     off[i] = -row.sub[i];
                     const float q = exp2_fast(-d[i]);
                     row.l[i] = mul2(row.l[i], two(q, q));
@@ -601,9 +620,9 @@ __device__ __forceinline__ bool row_weights(uint32_t ts, uint32_t to, bool any, 
                 continue;
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {  // a NaN stays
-                s[0][j] = s[0][j] > most ? most : s[0][j];
-                s[1][j] = s[1][j] > most ? most : s[1][j];
+            for (int j = 0; j < 16; ++j) {
+                s[0][j] = cut(s[0][j], most);
+                s[1][j] = cut(s[1][j], most);
             }
         }
         uint64_t vs[4];
@@ -949,6 +968,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 // 0 times NaN or infinity would reach them: such elements
                 // become zero here and are added at the end to the rows that
                 // see them.  The context's own reach every row as they are.
+                const bool past = (t + 1) * kTileKeys > walk.sg.s.ctx;
                 const int hideable = walk.sg.s.ctx - t * kTileKeys;  // rows from here on
                 bool any = false;
 #pragma unroll 1
@@ -960,7 +980,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     const int row = cw * 32 + r;
                     uint4 c = gemm::lds128(from + code_at<D>(row, x));
                     if (!((ok >> r) & 1u)) c = make_uint4(0, 0, 0, 0);
-                    if (row >= hideable) {
+                    if (past && row >= hideable) {
                         const uint4 f = make_uint4(finite_codes<kE5M2>(c.x), finite_codes<kE5M2>(c.y),
                                                    finite_codes<kE5M2>(c.z), finite_codes<kE5M2>(c.w));
                         any |= c.x != f.x || c.y != f.y || c.z != f.z || c.w != f.w;
