@@ -426,31 +426,43 @@ __device__ __forceinline__ void load_row(uint32_t (&w)[N], uint32_t base, int ro
 // 2^kSlack before its sums are rescaled, so that a rescale (a reduction over
 // the warp and a pass over the accumulators) is rare.
 constexpr float kSlack = 3.f;
-// Weights enter the second product in binary16 as p vs / ref * 2^12, at most
-// 2^15: what falls under 2^-24 of that, 2^-36 of the largest term, is lost,
-// which 2^20 keys cannot add up to a rounding of the result.  The divisor sums
-// the weights before that rounding (64 decode sequences 107 -> 103 us against
-// taking each weight's rounding into it).
-constexpr float kWeightScale = 4096.f;
+// Weights enter the second product in binary16 as p vs by, `by` the power of
+// two that brings the row's largest |vs| to [2^11, 2^12), so at most 2^15: what
+// falls under 2^-24 of that, 2^-35 of the largest term, is lost, which 2^19
+// keys cannot add up to a rounding of the result.  A row's `by` goes by the
+// keys that it sees.  The divisor sums the weights before that rounding (64
+// decode sequences 107 -> 103 us against taking each weight's rounding into
+// it).
+constexpr int kWeightBits = 12;
+constexpr int kMostBy = 127 + 112;  // exponent field of `by` before any key
+
+__device__ __forceinline__ float from_exponent(int field) { return __int_as_float(field << 23); }
+__device__ __forceinline__ int exponent_of(float x) { return __float_as_int(x) >> 23; }
+
+// The exponent field of `by` for a largest |vs| (0: none yet).
+__device__ __forceinline__ int by_for(float most) {
+    return min(kMostBy, 127 + kWeightBits - (exponent_of(most) - 126));
+}
+
+// A maximum before any score: finite, so that a hidden key's weight is 0.
+constexpr float kNoScore = -3e38f;
 
 // A warp's running softmax and accumulators.
 template <int D, int NQ>
 struct RowState {
-    float m[NQ][2];    // running maximum of the lane's rows (log2 units), -inf: none yet
+    float m[NQ][2];    // running maximum of the lane's rows (log2 units), kNoScore: none yet
     float l[NQ][2];    // this lane's keys' sum of weights
-    float ref;         // at least the largest |vs| met, by which weights are divided
-    float by;          // kWeightScale / ref
-    float off[NQ][2];  // m, or 0 while there is none
+    float by[NQ][2];   // what weights are multiplied with
+    float ref;         // the least 2^kWeightBits / by of the lane's rows
     float o[D / 16][NQ][4];
 
     __device__ __forceinline__ void clear() {
-        ref = 1e-30f;
-        by = kWeightScale / ref;
+        ref = from_exponent(254 + kWeightBits - kMostBy);
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-            m[n][0] = m[n][1] = -INFINITY;
+            by[n][0] = by[n][1] = from_exponent(kMostBy);
+            m[n][0] = m[n][1] = kNoScore;
             l[n][0] = l[n][1] = 0.f;
-            off[n][0] = off[n][1] = 0.f;
 #pragma unroll
             for (int t = 0; t < D / 16; ++t)
 #pragma unroll
@@ -668,21 +680,24 @@ __device__ __forceinline__ void consume_step(const Params &p, const Segment &sg,
         grow |= top[n][0] > rs.m[n][0] + kSlack || top[n][1] > rs.m[n][1] + kSlack;
     }
     if (__any_sync(0xffffffffu, grow)) {
-        const float v0 = fabsf(vs0), v1 = fabsf(vs1);  // of finite ones the largest
-        const float vm = max_over_keys(
-            fmaxf(v0 < INFINITY ? v0 : 0.f, v1 < INFINITY ? v1 : 0.f));  // the same in every c
-        const float ref = vm > rs.ref ? 2.f * vm < INFINITY ? 2.f * vm : vm : rs.ref;
-        const float rr = rs.ref / ref;
-        rs.ref = ref;
-        rs.by = kWeightScale / ref;
+        // of finite value scales the largest that a row sees
+        const float v0 = fabsf(vs0) < INFINITY ? fabsf(vs0) : 0.f,
+                    v1 = fabsf(vs1) < INFINITY ? fabsf(vs1) : 0.f;
+        int least = 0;
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                const uint32_t hid = hidden >> (4 * n + e);
+                const float vm =
+                    max_over_keys(fmaxf(hid & 1u ? 0.f : v0, hid & 4u ? 0.f : v1));
+                const int was = exponent_of(rs.by[n][e]), is = min(was, by_for(vm));
+                const float rr = is - was < -126 ? 0.f : from_exponent(127 + is - was);
+                rs.by[n][e] = from_exponent(is);
+                least = max(least, is);
                 const float m = fmaxf(rs.m[n][e], max_over_keys(top[n][e]));
                 const float a = rs.m[n][e] == m ? 1.f : exp2_fast(rs.m[n][e] - m);
                 rs.m[n][e] = m;
-                rs.off[n][e] = m == -INFINITY ? 0.f : m;
                 rs.l[n][e] *= a;
 #pragma unroll
                 for (int t = 0; t < D / 16; ++t) {
@@ -690,8 +705,8 @@ __device__ __forceinline__ void consume_step(const Params &p, const Segment &sg,
                     rs.o[t][n][2 + e] *= a * rr;
                 }
             }
+        rs.ref = from_exponent(254 + kWeightBits - least);
     }
-    const float w0 = vs0 * rs.by, w1 = vs1 * rs.by;
     uint32_t pb[NQ][2];
     float x[NQ][4];
 #pragma unroll
@@ -699,8 +714,8 @@ __device__ __forceinline__ void consume_step(const Params &p, const Segment &sg,
         float pr[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            pr[i] = exp2_fast(s[n][i] - rs.off[n][i & 1]);
-            x[n][i] = pr[i] * (i < 2 ? w0 : w1);
+            pr[i] = exp2_fast(s[n][i] - rs.m[n][i & 1]);
+            x[n][i] = pr[i] * ((i < 2 ? vs0 : vs1) * rs.by[n][i & 1]);
         }
         if (__builtin_expect(edge, 0)) {
 #pragma unroll
@@ -1011,19 +1026,22 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D <= 128 ? 4 : 2)
             for (int e = 0; e < 2; ++e) {
                 const float l = sum_over_keys(rs.l[n][e]);
                 if (g == 0) {
-                    sh_m[warp][8 * n + 2 * c + e] = rs.m[n][e];
+                    sh_m[warp][8 * n + 2 * c + e] =
+                        rs.m[n][e] == kNoScore ? -INFINITY : rs.m[n][e];
                     sh_l[warp][8 * n + 2 * c + e] = l;
                 }
             }
-        const float unit = rs.ref / kWeightScale;
 #pragma unroll
-        for (int n = 0; n < NQ; ++n)
+        for (int n = 0; n < NQ; ++n) {
+            const float unit[2] = {from_exponent(254 - exponent_of(rs.by[n][0])),
+                                   from_exponent(254 - exponent_of(rs.by[n][1]))};
 #pragma unroll
             for (int t = 0; t < D / 16; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     sh_o[(warp * kRows + 8 * n + 2 * c + (i & 1)) * S::kPad + g * (D / 8) + 2 * t +
-                         (i >> 1)] = rs.o[t][n][i] * unit;
+                         (i >> 1)] = rs.o[t][n][i] * unit[i & 1];
+        }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == sg.s.tiles;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (t0 == 0 ? 1 : 0);

@@ -69,3 +69,27 @@ def test_a_nan_of_no_weight(n, G, D, fmt):
     assert torch.isnan(got[:, :G, 3]).all()
     got[:, :G, 3] = 0
     assert torch.isfinite(got).all()
+
+
+# blocks of 8 and of 16 rows
+ROWS = [(3, 2, 64, "e4m3"), (4, 2, 128, "e5m2"), (6, 2, 128, "e4m3"), (6, 2, 96, "e4m3"),
+        (12, 3, 192, "e4m3"), (6, 2, 256, "e5m2")]
+
+
+@pytest.mark.parametrize("n,G,D,fmt", ROWS)
+@pytest.mark.parametrize("ctx", [0, 5, 200])
+@pytest.mark.parametrize("power", [40, 90])
+def test_a_hidden_value_scale(n, G, D, fmt, ctx, power):
+    """A drafted token with a finite value scale far over all others' (what a
+    slot that was left out still holds): the rows that do not see it are as if
+    it were not there, those that see it are right too."""
+    c = Case([ctx], [n], 2 * G, 2, D, fmt=fmt, seed=50)
+    want, tol = clean_rows(c)
+    at = c.slots(0, ctx + n)[ctx + n // 2].item()
+    c.cache.v_scale[at // 16, :, at % 16] = 2.0 ** power
+    got, vis = c.run().cpu(), c.visible(0)
+    assert rarn.watchdog() == 0
+    sees = vis[:, ctx + n // 2]
+    assert sees.any() and not sees.all()
+    R.check_attention(got[~sees], want[~sees], tol[~sees])
+    c.check(got)
