@@ -690,8 +690,9 @@ rarn_status rarn_kv_cache_read(rarn_heads k_out, rarn_heads v_out, const rarn_kv
  * row with every bit down to 2^-17 of its largest magnitude; softmax
  * statistics and sums are in binary32, the softmax weights, times their
  * value's scale, rounded to binary16 (11 bits) for the second product, where
- * what is under 2^-27 of the row's largest weight times the largest value scale
- * is lost.  Scores (scale * q . K_j) from 2^27 on, whose binary32 steps are no
+ * what is under 2^-25 of the row's largest weight times the largest value scale
+ * that the row sees is lost (a value of zeros, to which kv_cache_write gives
+ * the scale 1, counts; scales are good from 2^-70 to 2^90).  Scores (scale * q . K_j) from 2^27 on, whose binary32 steps are no
  * longer small, leave a row the values of its largest ones; a row whose scores
  * differ by more than binary32 holds may be NaN.  A row whose queries are not all
  * finite, or that sees a key with a NaN code, is NaN.

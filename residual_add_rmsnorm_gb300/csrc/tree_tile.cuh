@@ -61,14 +61,17 @@ constexpr int kIssueWarps = 2;   // of a pipeline's products
 constexpr int kTileThreads = 32 * (kSoftWarps + kConvWarps + 1 + kIssueWarps);
 constexpr int kMaxTileCtas = 160;
 constexpr int kInfos = 8;        // tiles whose scales are kept
+constexpr float kLiftSlack = 2.f;
 
 // What the softmax needs of a tile besides its scores.
 struct TileInfo {
     float kk[kTileKeys];  // key scale x softmax scale (log2 units), 0 where there is no key
     float vs[kTileKeys];  // value scale, 0 where there is no key
     uint32_t ok[4];       // keys that exist
-    float vmax;           // largest finite |vs|
-    int pad[3];       // to a multiple of 16 bytes
+    // of each pass's keys: lift_of the largest finite |vs|, and whether others'
+    // are more than kLiftSlack under it
+    float lift[2];
+    float wide[2];  // 1 or 0
 };
 
 // Shared memory: the queries' pieces (over which pipeline 1's state is laid
@@ -376,7 +379,7 @@ __device__ __forceinline__ uint64_t lds64(uint32_t a) {
 
 // Where a tile's figures are in shared memory.
 constexpr uint32_t kInfoVs = offsetof(TileInfo, vs), kInfoOk = offsetof(TileInfo, ok),
-                   kInfoVmax = offsetof(TileInfo, vmax);
+                   kInfoLift = offsetof(TileInfo, lift), kInfoWide = offsetof(TileInfo, wide);
 
 constexpr uint32_t kHalfRows = 16u << 16;  // tensor memory's address of a warp's second 16 rows
 
@@ -484,9 +487,9 @@ __device__ __noinline__ float row_top(uint32_t ts, uint32_t ti, uint32_t v0, uin
 // the row first sees a key, such that its largest weight times the tile's
 // largest vs is 2^kCentre, and moves up only when one would pass 2^kHighest: a
 // pass over the scores serves where finding their maximum first took two.
-// What falls under 2^-24 of the product's units, 2^-27 of the row's largest weight times
-// the largest value scale, is lost; 2^16 keys at that edge would add up to
-// half of binary16's own rounding.
+// What falls under 2^-24 of the product's units, 2^-25 of the row's largest
+// weight times the largest value scale that it sees, is lost; 2^14 keys at that
+// edge would add up to half of binary16's own rounding.
 struct RowLane {
     float off;   // of the own row
     bool set;    // the offset is chosen (rows that are not there count as such)
@@ -496,8 +499,8 @@ struct RowLane {
     uint64_t l[4];
 };
 
-// A tile's ceil(log2) of its largest value scale, within what binary32 sums of
-// weights bear.
+// ceil(log2) of a largest value scale, within what binary32 sums of weights
+// bear.
 __device__ __forceinline__ float lift_of(float vmax) {
     const int e = (int)(__float_as_uint(vmax) >> 23) - 126;
     return (float)max(-70, min(e, 100));
@@ -530,6 +533,21 @@ __device__ __noinline__ void scale_down(uint32_t to, bool any, uint32_t ts, int 
     tmem_st_wait();
 }
 
+// The same over the keys of a pass whose bits of v0, v1 are set (figures at
+// `ti`).  Where a row does not see them all, a hidden token's scale must not
+// choose its offset.
+static __device__ __noinline__ float row_lift(uint32_t ti, uint32_t v0, uint32_t v1) {
+    float most = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < kPass / 2; ++c) {
+        const uint32_t v = c < 16 ? v0 >> (2 * c) : v1 >> (2 * c - 32);
+        const float2 s = apart(lds64(ti + kInfoVs + 8 * c));
+        if ((v & 1u) && fabsf(s.x) < INFINITY) most = fmaxf(most, fabsf(s.x));
+        if ((v & 2u) && fabsf(s.y) < INFINITY) most = fmaxf(most, fabsf(s.y));
+    }
+    return lift_of(most);
+}
+
 // moved_offset out of line, {sub, down}: rare, and the roles share an instruction
 // cache.
 static __device__ __noinline__ float2 move_offset(float sub, float high, float centre) {
@@ -546,18 +564,25 @@ __device__ __forceinline__ float cut(float a, float most) {
 }
 
 // A warp's weights of a pass (S at `ts`, columns times the keys' factors at
-// `ti`), in binary16 over the scores' columns.  Where a score is more than
-// `most` over its row's offset, all that the row has so far is scaled down
-// first, once the products under way are in (`settled`), so that it comes to
-// `centre` or up to one under it: by a power of two, which rounds no weight
-// anew that stays normal in binary16.  This is done kMoves times at most for 32
-// keys, nearly always once; a score that is over even then counts as `most`.
+// `ti`), in binary16 over the scores' columns.  `lift`: of the value scales
+// that the own row sees.  Where a score is more than kHighest - lift over its
+// row's offset, all that the row has so far is scaled down first, once the
+// products under way are in (`settled`), so that it comes to kCentre - lift or
+// up to one under it: by a power of two, which rounds no weight anew that stays
+// normal in binary16.  This is done kMoves times at most for 32 keys, nearly
+// always once; a score that is over even then is cut.
 // kEdge: only keys whose bits of v0, v1 (the own row's) are set.
 template <int D, bool kEdge, class Settled>
 __device__ __forceinline__ bool row_weights(uint32_t ts, uint32_t to, bool any, uint32_t ti,
-                                            uint32_t v0, uint32_t v1, float most, float centre,
+                                            uint32_t v0, uint32_t v1, float lift,
                                             RowLane &row, const Settled &settled) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c2 = 2 * (lane & 3);
+    float most = kHighest - lift;  // the same for all rows within the context, else the least
+    if (kEdge) {
+        float m[4];
+        rows_from_owner(most, m);
+        most = fminf(fminf(m[0], m[1]), fminf(m[2], m[3]));
+    }
     int moves = 0;  // of the offset, for these keys
 #pragma unroll 1
     for (int c = 0; c < kPass / 32;) {
@@ -595,7 +620,11 @@ __device__ __forceinline__ bool row_weights(uint32_t ts, uint32_t to, bool any, 
         }
         if (__any_sync(0xffffffffu, over)) {
             // rare: the offset moves up under what is there; then again
-            if (moves < kMoves) {
+            float limit[4];
+            rows_from_owner(kHighest - lift, limit);
+            over = top[0] > limit[0] || top[1] > limit[1] || top[2] > limit[2] ||
+                   top[3] > limit[3];
+            if (moves < kMoves && __any_sync(0xffffffffu, over)) {
                 ++moves;
                 float d[4], off[4];
 #pragma unroll
@@ -604,8 +633,9 @@ __device__ __forceinline__ bool row_weights(uint32_t ts, uint32_t to, bool any, 
                     high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 1));
                     high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 2));
                     d[i] = 0.f;
-                    if (high > most) {
-                        const float2 moved = move_offset(row.sub[i], high, centre);
+                    if (high > limit[i]) {
+                        const float2 moved =
+                            move_offset(row.sub[i], high, limit[i] - (kHighest - kCentre));
                         row.sub[i] = moved.x;
                         d[i] = moved.y;
                     }
@@ -620,9 +650,10 @@ __device__ __forceinline__ bool row_weights(uint32_t ts, uint32_t to, bool any, 
                 continue;
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                s[0][j] = cut(s[0][j], most);
-                s[1][j] = cut(s[1][j], most);
+            for (int j = 0; j < 16; ++j) {  // of rows g, g + 8, and 16 more
+                const int i = (j >> 1) & 1;
+                s[0][j] = cut(s[0][j], limit[i]);
+                s[1][j] = cut(s[1][j], limit[i + 2]);
             }
         }
         uint64_t vs[4];
@@ -724,8 +755,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     grid_dependency_wait();
     grid_launch_dependents();
     const Cursor cur = find_part<128>(p, kRows, kTileKeys, sh_part);
-    // (its first lane's)
+    // the softmax warps', short of registers: their first lanes', and thread 0's
     __shared__ Walk sh_walk[kSoftWarps];
+    __shared__ int sh_each, sh_more;
+    if (threadIdx.x == 0) {
+        sh_each = cur.each;
+        sh_more = cur.more;
+    }
 
     if (warp == kSoftWarps + kConvWarps) {
         // ---------------- copies ----------------
@@ -810,15 +846,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             // with: the products of tile n - 4 or later, which the release of
             // this stage of keys waited for, came after its softmax.
             TileInfo &ti = info[n & (kInfos - 1)];
-            float vmax = 0.f;
+            float vmax = 0.f, vmin = INFINITY;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 ti.kk[4 * lane + i] = ksc[i] * p.scale_log2;
                 ti.vs[4 * lane + i] = vsc[i];
                 const float a = fabsf(vsc[i]);
                 if (a < INFINITY) vmax = fmaxf(vmax, a);
+                if (a > 0.f) vmin = fminf(vmin, a);
             }
-            vmax = warp_max(vmax);
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) {  // over the half warp of a pass's keys
+                vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, d));
+                vmin = fminf(vmin, __shfl_xor_sync(0xffffffffu, vmin, d));
+            }
             if (lane < 4) {
                 uint32_t w = 0;
 #pragma unroll
@@ -827,7 +868,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 const int left = now.live - 32 * lane;
                 ti.ok[lane] = left >= 32 ? w : left <= 0 ? 0u : w & ((1u << left) - 1u);
             }
-            if (lane == 0) ti.vmax = vmax;
+            if ((lane & 15) == 0) {
+                const float lift = lift_of(vmax);
+                ti.lift[lane >> 4] = lift;
+                ti.wide[lane >> 4] = lift - lift_of(vmin) > kLiftSlack ? 1.f : 0.f;
+            }
             __syncwarp();
             if (lane == 0) gemm::mbar_arrive(bar(B_INFO + (n & (kInfos - 1))));
             look();
@@ -1013,7 +1058,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // ---------------- softmax ----------------
         Walk &walk = sh_walk[warp];
         if (lane == 0) walk.begin(cur);
-        const int each = cur.each, more = cur.more;
         const int pipe = warp >> 2;
         const int r = threadIdx.x & 127;  // row of the pipeline = lane of tensor memory
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes
@@ -1154,7 +1198,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     // a warp without rows leaves its weights as they are: they
                     // reach no other row
                     if (warp_live) {
-                        const float lift = lift_of(lds_f(info + kInfoVmax));
+                        float lift = lds_f(info + kInfoLift + 4 * half);
+                        if (edge && lds_f(info + kInfoWide + 4 * half) != 0.f)
+                            lift = row_lift(ti, v0, v1);
                         if (!__all_sync(0xffffffffu, row.set)) {
                             const float top = edge ? row_top<true>(tsh, ti, v0, v1, back)
                                                    : row_top<false>(tsh, ti, 0, 0, back);
@@ -1170,12 +1216,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             return in;
                         };
                         if (edge)
-                            alive = row_weights<D, true>(tsh, to, done, ti, v0, v1,
-                                                         kHighest - lift, kCentre - lift, row,
+                            alive = row_weights<D, true>(tsh, to, done, ti, v0, v1, lift, row,
                                                          settled);
                         else
-                            alive = row_weights<D, false>(tsh, to, done, ti, v0, v1,
-                                                          kHighest - lift, kCentre - lift, row,
+                            alive = row_weights<D, false>(tsh, to, done, ti, v0, v1, lift, row,
                                                           settled);
                     }
                     tmem_st_wait();
@@ -1263,7 +1307,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (walk.t0 == 0 && pipe == 0 && r == 0)
                     p.joins[walk.seg0 + walk.which] =
                         Join{(int)blockIdx.x,
-                             whole ? -1 : part_of(each, more, walk.last_unit),
+                             whole ? -1 : part_of(sh_each, sh_more, walk.last_unit),
                              (int)sg.row0, sg.s.n, sg.head, sg.block, 0, 0};
             }
             gemm::tmem_fence_before();  // O is read before the next segment's products

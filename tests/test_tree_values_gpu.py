@@ -71,9 +71,10 @@ def test_a_nan_of_no_weight(n, G, D, fmt):
     assert torch.isfinite(got).all()
 
 
-# blocks of 8 and of 16 rows
+# blocks of 8 and of 16 rows; tiles of 128 and 256 rows
 ROWS = [(3, 2, 64, "e4m3"), (4, 2, 128, "e5m2"), (6, 2, 128, "e4m3"), (6, 2, 96, "e4m3"),
-        (12, 3, 192, "e4m3"), (6, 2, 256, "e5m2")]
+        (12, 3, 192, "e4m3"), (6, 2, 256, "e5m2"), (20, 2, 128, "e4m3"), (40, 2, 64, "e5m2"),
+        (80, 2, 128, "e4m3"), (90, 2, 64, "e4m3")]
 
 
 @pytest.mark.parametrize("n,G,D,fmt", ROWS)
