@@ -631,11 +631,12 @@ rarn_status rarn_qk_norm_rope(rarn_heads q_out, rarn_heads k_out, rarn_heads q, 
 /*
  * Token t's keys and values into slot slots[t] of the cache (page
  * slots[t] / page_size).  Row scales: s = max|x| / maxf over the head's
- * elements (1 for zeros), code = x / s rounded to nearest even; tensor
- * scales: code = x / scale[0], saturated.  A negative slot leaves the token
- * out (padding).  The non-negative slots of one call must differ from one
- * another: two tokens written to one slot race, and it may end up with the
- * codes of one and the scale of the other.
+ * elements (1 for zeros) and, as in the 8-bit output forms, code =
+ * (x * (1 / max|x|)) * maxf rounded to nearest even; tensor scales: code =
+ * x / scale[0] (the binary32 quotient) rounded alike and saturated.  A negative
+ * slot leaves the token out (padding).  The non-negative slots of one call must
+ * differ from one another: two tokens written to one slot race, and it may end
+ * up with the codes of one and the scale of the other.
  */
 rarn_status rarn_kv_cache_write(const rarn_kv_cache *cache, rarn_heads k, rarn_heads v,
                                 const int64_t *slots, int64_t T, void *stream);
@@ -691,11 +692,12 @@ rarn_status rarn_kv_cache_read(rarn_heads k_out, rarn_heads v_out, const rarn_kv
  * statistics and sums are in binary32, the softmax weights, times their
  * value's scale, rounded to binary16 (11 bits) for the second product, where
  * what is under 2^-25 of the row's largest weight times the largest value scale
- * that the row sees is lost (a value of zeros, to which kv_cache_write gives
- * the scale 1, counts; scales are good from 2^-70 to 2^90).  Scores (scale * q . K_j) from 2^27 on, whose binary32 steps are no
- * longer small, leave a row the values of its largest ones; a row whose scores
- * differ by more than binary32 holds may be NaN.  A row whose queries are not all
- * finite, or that sees a key with a NaN code, is NaN.
+ * that the row sees is lost (a value of zeros, to which rarn_kv_cache_write
+ * gives the scale 1, counts; value scales are good from 2^-70 to 2^90).  Scores
+ * (scale * q . K_j) from 2^27 on, whose binary32 steps are no longer small, leave
+ * a row the values of its largest ones; a row whose scores differ by more than
+ * binary32 holds may be NaN.  A row whose queries are not all finite, or that
+ * sees a key with a NaN code, is NaN.
  * head_dim 64, 96, 128, 192 or 256; q 16-byte aligned with strides multiples
  * of 8 elements (else RARN_ERR_UNSUPPORTED); table_width * page_size at most
  * 2^31 - 4096.  Sequences of many rows (drafted tokens x query heads of a key

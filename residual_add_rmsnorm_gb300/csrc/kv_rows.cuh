@@ -4,7 +4,8 @@
 //   n = x * rsqrt(mean(x^2) + eps) * gamma       over one head's D elements
 //   (a, b) -> (a cos - b sin, b cos + a sin)     for the first `rot` elements,
 //                                                pairs (i, i + rot / 2) or (2i, 2i + 1)
-//   code = RN(n / s)                             s given, or max|n| / maxf per row
+//   code = RN(n / s)                             s given
+//   code = RN((n * (1 / max|n|)) * maxf)         per row, s = max|n| / maxf
 //
 // All of it is one pass: a head is 128 to 512 bytes, so the row's elements
 // stay in registers between the sum of squares, the rotation and the row's
@@ -266,8 +267,7 @@ __global__ void __launch_bounds__(128, kRowCtas)
         }
     }
     const float inv_d = 1.f / static_cast<float>(p.D);
-    const QMul given = r.codes && p.cache.mode == Q_TENSOR ? QMul{1.f / __ldg(r.scales), 1.f}
-                                                           : QMul{1.f, 1.f};
+    const float given = r.codes && p.cache.mode == Q_TENSOR ? __ldg(r.scales) : 1.f;
     uint8_t *codes = nullptr;
     float *scales = nullptr;
     if (pl.page >= 0) {
@@ -309,20 +309,27 @@ __global__ void __launch_bounds__(128, kRowCtas)
             st_global(d + eb, DT<T>::pack(fb));
         }
         if (codes) {  // uniform
-            QMul m = given;
             if (p.cache.mode == Q_ROW) {
                 float amax = 0.f;
 #pragma unroll
                 for (int j = 0; j < E; ++j) amax = fmaxf(amax, fmaxf(fabsf(fa[j]), fabsf(fb[j])));
                 amax = group_max<LG>(amax);
                 float scale;
-                m = row_mul(amax, p.cache.fmt, &scale);
+                const QMul m = row_mul(amax, p.cache.fmt, &scale);
                 if (l == 0 && live) scales[h * p.cache.s_head] = scale;
-            }
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                fa[j] = (fa[j] * m.m1) * m.m2;
-                fb[j] = (fb[j] * m.m1) * m.m2;
+                for (int j = 0; j < E; ++j) {
+                    fa[j] = (fa[j] * m.m1) * m.m2;
+                    fb[j] = (fb[j] * m.m1) * m.m2;
+                }
+            } else {
+                // divided: a reciprocal's rounding would move ties, and that of
+                // a subnormal scale is infinite
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    fa[j] /= given;
+                    fb[j] /= given;
+                }
             }
             if (live) {
                 uint8_t *d = codes + h * p.cache.head_stride;
@@ -407,6 +414,7 @@ __global__ void __launch_bounds__(128) k_head_rows_any(const RowParams p, int he
         }
     };
     QMul m{1.f, 1.f};
+    float given = 1.f;
     const bool store_codes = pl.page >= 0;
     if (store_codes) {
         if (p.cache.mode == Q_ROW) {
@@ -424,7 +432,7 @@ __global__ void __launch_bounds__(128) k_head_rows_any(const RowParams p, int he
                 r.scales[pl.page * p.cache.s_page + h * p.cache.s_head +
                          pl.at * p.cache.s_slot] = scale;
         } else {
-            m.m1 = 1.f / __ldg(r.scales);
+            given = __ldg(r.scales);
         }
     }
     uint8_t *codes = store_codes ? r.codes + pl.page * p.cache.page_stride +
@@ -440,8 +448,15 @@ __global__ void __launch_bounds__(128) k_head_rows_any(const RowParams p, int he
             if (e1 >= 0) d[e1] = DT<T>::from_f(b);
         }
         if (codes) {
-            codes[e0] = fp8x1((a * m.m1) * m.m2, p.cache.fmt);
-            if (e1 >= 0) codes[e1] = fp8x1((b * m.m1) * m.m2, p.cache.fmt);
+            if (p.cache.mode == Q_ROW) {
+                a = (a * m.m1) * m.m2;
+                b = (b * m.m1) * m.m2;
+            } else {
+                a /= given;
+                b /= given;
+            }
+            codes[e0] = fp8x1(a, p.cache.fmt);
+            if (e1 >= 0) codes[e1] = fp8x1(b, p.cache.fmt);
         }
     }
 }
