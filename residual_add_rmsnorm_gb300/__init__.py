@@ -1026,6 +1026,8 @@ def tree_attention(q, cache: KVCache, page_table, context_lens, starts, mask=Non
     if mask is not None:
         if mask.dim() != 2 or mask.shape[0] != N:
             raise ValueError(f"mask must be [{N}, words]")
+        if mask.shape[1] == 0:  # its address may be that of no mask at all
+            raise ValueError("mask must have one word or more")
         words = mask.shape[1]
         pm = _indices("mask", mask, torch.int32, N * words, dev)
     if workspace is None:
