@@ -709,7 +709,7 @@ rarn_status rarn_kv_cache_read(rarn_heads k_out, rarn_heads v_out, const rarn_kv
  * later length within its page table's width.  Results are the same bits on
  * every call with the same inputs.  Every wait in the kernels is bounded (2 s):
  * one that runs out sets bit 5 of the watchdog word, and the call's outputs are
- * not valid.
+ * not valid: rows that miss keys are NaN or as they were.
  */
 rarn_status rarn_tree_attention(rarn_heads out, rarn_heads q, const rarn_kv_cache *cache,
                                 const int32_t *page_table, int64_t table_stride,
@@ -821,13 +821,15 @@ rarn_status rarn_reset_tuning(void);
 /*
  * Test hook for the watchdog: in the next launch (on any thread) of a stream
  * kernel (16-bit partials, or the TMA-fed kernel of
- * rarn_reduce_add_rms_norm_fp8in) or of the GEMM form, CTA 0 expects 16 bytes
+ * rarn_reduce_add_rms_norm_fp8in), of the GEMM form or of rarn_tree_attention
+ * (its kernels that copy by TMA; in "tree.rows" the fills of CTA 0's first
+ * warp, in "tree.tiles" keys' and values' in turn), CTA 0 expects 16 bytes
  * more for pipeline fill number `fill` (0-based, in issue order) than its
  * copies bring, so that fill never completes; every shared-memory barrier wait of that launch is
  * bounded by `wait_limit_ns` (1 ns .. 2 s).  The waits on that fill run out:
  * the kernel sets the watchdog word (bit 0 / 1: stream consumer / producer;
- * bit 2: GEMM kernel) and returns with its outputs invalid, and the context
- * stays usable.  In the next tensor-parallel launch with signal pads instead,
+ * bit 2: GEMM kernel; bit 5: attention) and returns with its outputs invalid,
+ * and the context stays usable.  In the next tensor-parallel launch with signal pads instead,
  * CTA 0 of rank `fill` (modulo N) never signals at entry, so the other ranks'
  * CTA 0 (and its own) wait out the limit (bit 3); the pads must then be
  * zeroed before the next call.  Returns RARN_ERR_INVALID_ARG for a negative fill or a limit

@@ -72,7 +72,7 @@ thread_local int t_last_cuda_error = 0;
 std::atomic<int> g_path{RARN_PATH_AUTO};
 std::atomic<int> g_pdl{1};
 // test hook (rarn_test_stall): consumed by the next launch of the stream
-// kernel or of the GEMM form
+// kernel, of the GEMM form or of an attention kernel that waits for copies
 std::atomic<long long> g_stall_fill{-1};
 std::atomic<unsigned long long> g_stall_limit_ns{0};
 
@@ -695,6 +695,14 @@ rarn_status current_device(Device *out) {
 }
 
 rarn_status cuda_failed(cudaError_t e) { return cuda_fail(e); }
+
+bool take_stall(long long *fill, unsigned long long *limit_ns) {
+    const long long f = g_stall_fill.exchange(-1);
+    if (f < 0) return false;
+    *fill = f;
+    *limit_ns = g_stall_limit_ns.load();
+    return true;
+}
 
 bool pdl_enabled() { return g_pdl.load() != 0; }
 

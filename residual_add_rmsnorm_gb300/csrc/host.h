@@ -19,6 +19,8 @@ struct Device {
 rarn_status current_device(Device *out);
 // Records a CUDA error for rarn_last_cuda_error and returns RARN_ERR_CUDA.
 rarn_status cuda_failed(cudaError_t e);
+// The test hook's fill and limit (rarn_test_stall), once; false where none is set.
+bool take_stall(long long *fill, unsigned long long *limit_ns);
 // Whether launches carry the programmatic-serialization attribute.
 bool pdl_enabled();
 

@@ -598,6 +598,12 @@ rarn_status rarn_tree_attention(rarn_heads out, rarn_heads q, const rarn_kv_cach
     p.part = reinterpret_cast<float *>(ws + pl.part_off);
     p.max_segs = (int)pl.segments;
     p.watchdog = dev.watchdog;
+    p.wait_limit_ns = tree::kWaitLimitNs;
+    p.stall_fill = -1;
+    long long fill;
+    if ((pl.tiles || (p.whole_steps && tree::rows_by_tma(D))) &&
+        host::take_stall(&fill, &p.wait_limit_ns))
+        p.stall_fill = (int)std::min<long long>(fill, INT32_MAX);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const bool pdl = host::pdl_enabled();
     const cudaError_t e = cache->format == RARN_E5M2

@@ -79,6 +79,9 @@ struct Params {
     float2 *ml;              // [2 W][rows]
     float *part;             // [2 W][rows][D]
     unsigned int *watchdog;
+    unsigned long long wait_limit_ns;
+    int stall_fill;          // test hook: in CTA 0 this fill (of its first warp that copies) never
+                             // completes (-1: off)
 };
 
 // One sequence's share of the line of tiles.
@@ -351,7 +354,7 @@ __device__ __forceinline__ bool wait_stage(const Params &p, uint32_t bar, uint32
             const unsigned long long t = gemm::now_ns();
             if (t0 == 0) {
                 t0 = t;
-            } else if (t - t0 > kWaitLimitNs) {
+            } else if (t - t0 > p.wait_limit_ns) {
                 atomicOr(p.watchdog, kWatchTree);
                 return false;
             }
@@ -561,14 +564,15 @@ __device__ __forceinline__ void issue_step(const Params &p, const Segment &sg, c
 // The same by TMA, from one lane, where a step lies inside one page and its
 // scales are adjacent: the box of its keys' rows and that of its values', and
 // the two runs of scales.  `page` is the page's number, loaded ahead.  Slots
-// behind the sequence's end come along and are masked.  64 sequences of up to
+// behind the sequence's end come along and are masked.  `extra`: bytes that are
+// awaited and never come (the test hook).  64 sequences of up to
 // 8192 tokens, 8 key heads of 128, one token each: 125.5 us, with the copies
 // above 131.7 (both before segments' ends counted in the split).
 template <int D>
 __device__ __forceinline__ void issue_step_tma(const Params &p, const Segment &sg,
                                                const CUtensorMap *kmap, const CUtensorMap *vmap,
                                                const Stage &stage, uint32_t bar, int j0,
-                                               int page) {
+                                               int page, uint32_t extra) {
     using L = StepLayout<D>;
     const bool have = page >= 0 && page < p.cache.pages;
     const int live = min(kStep, sg.s.len - j0);
@@ -582,7 +586,7 @@ __device__ __forceinline__ void issue_step_tma(const Params &p, const Segment &s
     }
     const int at = p.offset_in_page(j0);
     const bool rows = p.cache.mode == Q_ROW;
-    gemm::mbar_arrive_expect_tx(bar, L::kBytes + (rows ? 8 * kStep : 0));
+    gemm::mbar_arrive_expect_tx(bar, L::kBytes + (rows ? 8 * kStep : 0) + extra);
 #pragma unroll
     for (int h = 0; h < D / L::kHalf; ++h) {
         const uint32_t dst = stage.codes + h * (kStep * L::kHalf);
@@ -937,6 +941,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D <= 128 ? 4 : 2)
     }
     uint32_t phases = 0;  // bit i: parity of stage i's next fill
     bool sound = true;    // no wait has run out
+    int to_stall = blockIdx.x == 0 && warp == 0 ? p.stall_fill : -1;  // fills until that one
     grid_dependency_wait();
     grid_launch_dependents();
     const Cursor cur = find_part<kThreads>(p, kRows, kTile, sh_part);
@@ -976,7 +981,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D <= 128 ? 4 : 2)
                     if (nx < j1) page = pages[p.page_of(nx)];
                     if (lane == 0)
                         issue_step_tma<D>(p, sg, &kmap, &vmap, stage_at(i), bars + 8 * i, ahead,
-                                          now);
+                                          now, to_stall == 0 ? 16u : 0u);
+                    --to_stall;
                 }
             } else {
                 if (ahead < j1) issue_step<D>(p, sg, stage_at(i), ahead);
@@ -1018,6 +1024,10 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D <= 128 ? 4 : 2)
             stage = stage == kStages - 1 ? 0 : stage + 1;
         }
         if (!kTma) copies_wait<0>();
+        if (kTma && !sound) {  // what is missing is not passed over
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) rs.l[n][0] = rs.l[n][1] = NAN;
+        }
         // join the warps
         __syncthreads();  // every warp's ring is free
 #pragma unroll

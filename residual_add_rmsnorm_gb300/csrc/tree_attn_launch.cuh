@@ -101,12 +101,11 @@ inline cudaError_t launch_copies(const Params &p, const Plan &pl, int num_sms, b
                   : launch_dim<D, 3, kE5M2, kTma>(p, pl, num_sms, pdl, st);
 }
 
-// TMA boxes need rows of 64 or 128 bytes, steps inside a page and adjacent
-// scales (Params::whole_steps).
+// TMA boxes need steps inside a page and adjacent scales (Params::whole_steps).
 template <int D, bool kE5M2>
 inline cudaError_t launch_type(const Params &p, const Plan &pl, int num_sms, bool pdl,
                                cudaStream_t st) {
-    if constexpr (D == 64 || D % 128 == 0)
+    if constexpr (rows_by_tma(D))
         if (p.whole_steps) return launch_copies<D, kE5M2, true>(p, pl, num_sms, pdl, st);
     return launch_copies<D, kE5M2, false>(p, pl, num_sms, pdl, st);
 }

@@ -9,6 +9,10 @@ namespace tree {
 
 constexpr int kBoxSlots = 8;  // pages of whole groups of these are copied by k_tree_tile
 
+// Whether k_tree_rows copies by TMA where pages and scales allow it
+// (Params::whole_steps): rows of 64 or 128 bytes.
+constexpr bool rows_by_tma(int64_t D) { return D == 64 || D % 128 == 0; }
+
 struct Plan {
     int rows;          // rows (drafted token x query head of the group) of a segment
     bool tiles;        // the tensor-memory kernel (tree_tile.cuh)

@@ -38,7 +38,8 @@
 // 8, 4, 1: 138, 126, 124 us; one context of 131072 keys: 129, 122, 116).
 //
 // Every wait is bounded; one that runs out sets watchdog bit 5, the CTA's
-// warps give up together, and its tensor memory is freed.
+// warps give up together, its segments' records say so (give_up), and its
+// tensor memory is freed.
 #pragma once
 
 #include <cstddef>
@@ -167,7 +168,7 @@ __device__ __forceinline__ bool tile_wait(const Params &p, uint32_t bar, uint32_
             const unsigned long long t = gemm::now_ns();
             if (t0 == 0) {
                 t0 = t;
-            } else if (t - t0 > kWaitLimitNs) {
+            } else if (t - t0 > p.wait_limit_ns) {
                 *abort_flag = 1;
                 atomicOr(p.watchdog, kWatchTree);
                 return false;
@@ -686,6 +687,19 @@ __device__ __forceinline__ bool row_weights(uint32_t ts, uint32_t to, bool any, 
     return true;
 }
 
+// A CTA whose waits ran out: k_tree_join finds no segment that began here, whose
+// record may not have been written, and NaN in what belongs to an earlier one.
+inline __device__ __noinline__ void give_up(const Params &p, const Cursor &cur, int rows) {
+    for (int x = threadIdx.x; x < 2 * rows; x += kTileThreads)
+        p.ml[2 * (int64_t)blockIdx.x * rows + x] = make_float2(NAN, NAN);
+    if (threadIdx.x != 0) return;
+    Walk walk;
+    walk.begin(cur);
+    while (walk.next(p, rows))
+        if (walk.t0 == 0)
+            p.joins[walk.seg0 + walk.which] = Join{(int)blockIdx.x, -1, 0, 0, 0, 0, 0, 0};
+}
+
 // The sum of weights of the lane's own row.
 __device__ __forceinline__ float row_sum(const RowLane &row) {
     float sum[4];
@@ -703,7 +717,7 @@ __device__ __forceinline__ float row_sum(const RowLane &row) {
 // of a query.
 template <int D, int NP, bool kE5M2, bool kTwo>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    k_tree_tile(const Params p, const __grid_constant__ CUtensorMap kmap,
+    k_tree_tile(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap) {
     using S = TileSmem<D, NP, kTwo>;
     constexpr int kRows = kTwo ? 2 * kTileRows : kTileRows;
@@ -755,13 +769,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     grid_dependency_wait();
     grid_launch_dependents();
     const Cursor cur = find_part<128>(p, kRows, kTileKeys, sh_part);
-    // the softmax warps', short of registers: their first lanes', and thread 0's
+    // for the softmax warps, short of registers: their first lanes', and thread 0's
     __shared__ Walk sh_walk[kSoftWarps];
-    __shared__ int sh_each, sh_more;
-    if (threadIdx.x == 0) {
-        sh_each = cur.each;
-        sh_more = cur.more;
-    }
+    __shared__ Cursor sh_cur;
+    if (threadIdx.x == 0) sh_cur = cur;
 
     if (warp == kSoftWarps + kConvWarps) {
         // ---------------- copies ----------------
@@ -815,13 +826,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
             }
         };
+        const int stall_at = blockIdx.x == 0 ? p.stall_fill : -1;
         // lanes whose eight slots are the first of a box
         const uint32_t first =
             __ballot_sync(0xffffffffu, lane < 16 && ((kBox * lane) & (p.box - 1)) == 0);
         auto copy = [&](const CUtensorMap *map, uint32_t dst, uint32_t full, uint32_t boxes,
-                        const Next &x) {
+                        const Next &x, int fill) {
             if (lane == 0)
-                gemm::mbar_arrive_expect_tx(full, p.box * D * __popc(boxes & first));
+                gemm::mbar_arrive_expect_tx(full, p.box * D * __popc(boxes & first) +
+                                                      (fill == stall_at ? 16u : 0u));
             __syncwarp();
             if (((first >> lane) & 1u) && x.page >= 0)
                 tma_box(dst + lane * (kBox * D), map, full, 0, x.at, x.head, x.page);
@@ -829,6 +842,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         after.there = false;
         look();
         look();
+        int nk = 0, nv = 0;    // fills
         int ks = 0, vs = 0;    // stages
         uint32_t kp = 1, vp = 1;     // parities of their releases
 #pragma unroll 1
@@ -837,7 +851,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const uint32_t boxes = __ballot_sync(0xffffffffu, now.page >= 0) & 0xffffu;
             bool alive = tile_wait(p, bar(B_KEMPTY + ks), kp, &sh_abort);
             if (!__all_sync(0xffffffffu, alive)) break;
-            copy(&kmap, sbase + S::kK + ks * S::kCodes, bar(B_KFULL + ks), boxes, now);
+            copy(&kmap, sbase + S::kK + ks * S::kCodes, bar(B_KFULL + ks), boxes, now,
+                 2 * n);
+            ++nk;
             if (++ks == S::kStagesK) {
                 ks = 0;
                 kp ^= 1;
@@ -878,17 +894,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             look();
             alive = tile_wait(p, bar(B_VEMPTY + vs), vp, &sh_abort);
             if (!__all_sync(0xffffffffu, alive)) break;
-            copy(&vmap, sbase + S::kV + vs * S::kCodes, bar(B_VFULL + vs), boxes, now);
+            copy(&vmap, sbase + S::kV + vs * S::kCodes, bar(B_VFULL + vs), boxes, now,
+                 2 * n + 1);
+            ++nv;
             if (++vs == S::kStagesV) {
                 vs = 0;
                 vp ^= 1;
             }
         }
-        if (sh_abort) {  // let what is under way land before the CTA goes
+        if (sh_abort && lane == 0) {
+            // let what is under way land before the CTA goes, if it does
             const unsigned long long t0 = gemm::now_ns();
-            while (gemm::now_ns() - t0 < 1000000ull) {
-            }
+            auto landed = [&](int b, int fills, int stages) {
+                for (int f = max(0, fills - stages); f < fills; ++f)
+                    while (!gemm::mbar_try_wait(bar(b + f % stages), (f / stages) & 1) &&
+                           gemm::now_ns() - t0 < p.wait_limit_ns) {
+                    }
+            };
+            landed(B_KFULL, nk, S::kStagesK);
+            landed(B_VFULL, nv, S::kStagesV);
         }
+        __syncwarp();
     } else if (warp > kSoftWarps + kConvWarps) {
         // ---------------- a pipeline's products ----------------
         // In the order that keeps the tensor cores ahead of the softmax: the
@@ -1307,7 +1333,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (walk.t0 == 0 && pipe == 0 && r == 0)
                     p.joins[walk.seg0 + walk.which] =
                         Join{(int)blockIdx.x,
-                             whole ? -1 : part_of(sh_each, sh_more, walk.last_unit),
+                             whole ? -1 : part_of(sh_cur.each, sh_cur.more, walk.last_unit),
                              (int)sg.row0, sg.s.n, sg.head, sg.block, 0, 0};
             }
             gemm::tmem_fence_before();  // O is read before the next segment's products
@@ -1329,6 +1355,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                      : "memory");
+    if (sh_abort) give_up(p, sh_cur, kRows);  // last: its lanes part
 }
 
 }  // namespace tree
