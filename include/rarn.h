@@ -685,7 +685,10 @@ rarn_status rarn_kv_cache_read(rarn_heads k_out, rarn_heads v_out, const rarn_kv
  * keep their `out` rows as they were; tokens past the page table's width or on
  * a missing page are hidden.  starts must not fall (B + 1 values from 0 to
  * `tokens`): a sequence whose pair does is taken as empty, and nothing is
- * computed (bit 4) where they name more rows than there are.
+ * computed (bit 4) where they name more rows than there are, or where the
+ * call's work passes 2^31 - 1 units: a segment (a sequence, key head and block
+ * of rows, see rarn_plan_tree_attention) has one for each 64 keys and 4 more
+ * ("tree.tiles": for each 128 keys and 6 more).
  *
  * q, out: one 16-bit type.  Codes enter both products exactly, and a query
  * row with every bit down to 2^-17 of its largest magnitude; softmax

@@ -7,7 +7,8 @@
 // drafted tokens, of which token i sees those whose bit is set in its mask
 // row (without a mask: those up to itself).  The G = Hq / Hk query heads that
 // share a key head and a sequence's drafted tokens form the rows of one
-// product, so each cached byte is read once for all of them.
+// product: a cached byte is read once for each block of rows, of 8 or 16 in
+// k_tree_rows, 128 or 256 in k_tree_tile.
 //
 // Work split.  A segment is one sequence, one key head and one block of rows;
 // its keys form tiles of kTile.  All segments' tiles lie on one line, and CTA
