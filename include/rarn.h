@@ -294,6 +294,41 @@ rarn_status rarn_reduce_add_rms_norm_fp8in(void *y, const void *partials, int32_
                                            int64_t H, float eps, rarn_dtype dt, void *stream);
 
 /*
+ * The norms after and before a block, fused with its gate and the residual
+ * stream between them (post-norm and pre-norm, gates learned or made by a
+ * modulation, scaled residuals):
+ *   n = x * rsqrt(mean(x^2) + eps) * x_gamma      (x_gamma NULL: n = x)
+ *   h = RN(residual_scale * residual + scale * (gate * n))
+ *   residual_out <- h;  y = RN(h * rsqrt(mean(h^2) + eps) * gamma)
+ * in binary32, h rounded once to the residual's type and normalised as it is
+ * stored.  ("RMSNorm kernel", 1 Background, twice; the pages fuse neither a
+ * gate nor a norm before the add.)
+ *
+ * x, y, gate and the gammas share one type; residual and residual_out share
+ * one: that or RARN_F32.  gate (NULL: none): `rows` rows of H elements, one
+ * for all tokens (rows == 1), one per token (rows == T), or any number with
+ * index[t] naming token t's row; a token whose index is outside keeps its rows
+ * of y and residual_out as they were (bit 4 of the watchdog word).  scale and
+ * residual_scale must be finite.  y may equal x and residual_out the residual
+ * (same data and row stride); any other overlap of an output returns
+ * RARN_ERR_ALIAS, judged on the row spans.  With every base, stride and H a
+ * multiple of 16 bytes kernels with 16-byte accesses run, otherwise one that
+ * goes element by element.  A stride times its rows is at most
+ * RARN_MAX_STRIDE; everything else is as for the general forms.
+ */
+typedef struct rarn_gate {
+    const void *data;
+    int64_t row_stride;    /* elements */
+    int64_t rows;
+    const int32_t *index;  /* T values in device memory, or NULL */
+} rarn_gate;
+
+rarn_status rarn_gated_add_rms_norm(rarn_rows y, rarn_rows residual_out, rarn_rows x,
+                                    rarn_rows residual, const void *x_gamma, const void *gamma,
+                                    const rarn_gate *gate, float scale, float residual_scale,
+                                    int64_t T, int64_t H, float eps, void *stream);
+
+/*
  * GEMM producer with the fused residual-add RMSNorm as its epilogue: the
  * partial that the fused form adds to the residual is the product of the
  * activations A [T, K] and a linear layer's weight W [H, K]:
@@ -600,6 +635,22 @@ typedef struct rarn_rotation {
     rarn_rotation_style style;
 } rarn_rotation;
 
+/* The same with positions of several axes (time, height, width of an image's or
+ * a video's patches): token t has `axes` positions, axis a's at
+ * positions[a * position_stride + t], and pair i turns by the angles at
+ * element i of the row that its axis names:
+ *   cos_sin[positions[axis_of_pair[i] * position_stride + t], i].
+ * axis_of_pair: rot_dim / 2 values from 0 to axes - 1 in HOST memory, copied by
+ * the call (sections one after another, axes in turn, or any other order). */
+#define RARN_MAX_AXES 4
+
+typedef struct rarn_rotation_axes {
+    rarn_rotation rotation;
+    int32_t axes;  /* 1 .. RARN_MAX_AXES */
+    int64_t position_stride;
+    const uint8_t *axis_of_pair;
+} rarn_rotation_axes;
+
 #define RARN_MAX_HEADS 4096
 #define RARN_MAX_HEAD_DIM 1024
 #define RARN_MAX_PAGE_SIZE (1 << 20)
@@ -629,6 +680,15 @@ rarn_status rarn_qk_norm_rope(rarn_heads q_out, rarn_heads k_out, rarn_heads q, 
                               void *stream);
 
 /*
+ * rarn_qk_norm_rope with positions of several axes.  A token any of whose
+ * positions is outside the table keeps its output rows as they were.
+ */
+rarn_status rarn_qk_norm_rope_axes(rarn_heads q_out, rarn_heads k_out, rarn_heads q, rarn_heads k,
+                                   const void *q_gamma, const void *k_gamma,
+                                   const rarn_rotation_axes *rotation, int64_t T, int64_t D,
+                                   float eps, void *stream);
+
+/*
  * Token t's keys and values into slot slots[t] of the cache (page
  * slots[t] / page_size).  Row scales: s = max|x| / maxf over the head's
  * elements (1 for zeros) and, as in the 8-bit output forms, code =
@@ -652,6 +712,14 @@ rarn_status rarn_qk_norm_rope_kv_write(rarn_heads q_out, const rarn_kv_cache *ca
                                        rarn_heads k, rarn_heads v, const void *q_gamma,
                                        const void *k_gamma, const rarn_rotation *rotation,
                                        const int64_t *slots, int64_t T, float eps, void *stream);
+
+/* rarn_qk_norm_rope_kv_write with positions of several axes. */
+rarn_status rarn_qk_norm_rope_axes_kv_write(rarn_heads q_out, const rarn_kv_cache *cache,
+                                            rarn_heads q, rarn_heads k, rarn_heads v,
+                                            const void *q_gamma, const void *k_gamma,
+                                            const rarn_rotation_axes *rotation,
+                                            const int64_t *slots, int64_t T, float eps,
+                                            void *stream);
 
 /*
  * The cache read back: sequence b's tokens j = 0, 1, ... go to output rows

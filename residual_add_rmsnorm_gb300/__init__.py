@@ -27,6 +27,10 @@ attention of drafted tokens over it):
     rms_norm_fp8(x, gamma, eps, out, scale, fmt="e4m3", scale_mode="tensor")
     fused_add_rms_norm_fp8(x, residual, gamma, eps, out, scale, ...)
     reduce_add_rms_norm_fp8(partials, residual, gamma, eps, out, scale, ...)
+
+The norms after and before a block, with its gate and the residual between them:
+
+    gated_add_rms_norm(x, residual, x_gamma, gamma, eps, gate=gate, scale=0.5)
 """
 from __future__ import annotations
 
@@ -45,7 +49,8 @@ __all__ = ["rms_norm", "fused_add_rms_norm", "reduce_add_rms_norm", "rms_norm_ho
            "ipc_export", "ipc_import", "ipc_close", "TP_MAX_RANKS", "TP_SIGNAL_BYTES",
            "IPC_HANDLE_BYTES", "qk_norm_rope", "KVCache", "kv_cache_write",
            "qk_norm_rope_kv_write", "kv_cache_read", "tree_attention",
-           "tree_attention_workspace_bytes", "plan_tree_attention", "ROTATION_STYLES"]
+           "tree_attention_workspace_bytes", "plan_tree_attention", "ROTATION_STYLES",
+           "SECTION_ORDERS", "gated_add_rms_norm"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "librarn.so")
@@ -56,6 +61,7 @@ PATHS = {"auto": 0, "rows": 1, "stream": 2, "cluster": 3}
 FP8_FORMATS = {"e4m3": 0, "e5m2": 1}
 SCALE_MODES = {"tensor": 0, "row": 1}
 ROTATION_STYLES = {"half": 0, "interleaved": 1}
+SECTION_ORDERS = ("blocks", "cyclic")
 # rarn_tuning knobs (planner overrides; -1 is the planner's own choice)
 TUNING = {"rows_per_thread": 0, "rows_grid": 1, "rows_pipeline": 2, "l2_rows": 3,
           "stream_packs": 4, "stream_groups": 5, "gemm_cols": 6, "gemm_slab": 7,
@@ -105,6 +111,12 @@ class Fp8Rows(ctypes.Structure):
                 ("scale", ctypes.c_void_p)]
 
 
+class Gate(ctypes.Structure):
+    """``rarn_gate``: data pointer, row stride in elements, rows, index."""
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("index", ctypes.c_void_p)]
+
+
 class Heads(ctypes.Structure):
     """``rarn_heads``: data pointer, token and head strides in elements, heads,
     storage type."""
@@ -118,6 +130,13 @@ class Rotation(ctypes.Structure):
     _fields_ = [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p),
                 ("table_rows", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
                 ("style", ctypes.c_int)]
+
+
+class RotationAxes(ctypes.Structure):
+    """``rarn_rotation_axes``: the rotation, axes, elements between two axes'
+    positions, each pair's axis (host memory)."""
+    _fields_ = [("rotation", Rotation), ("axes", ctypes.c_int32),
+                ("position_stride", ctypes.c_int64), ("axis_of_pair", ctypes.c_void_p)]
 
 
 class KvCacheDesc(ctypes.Structure):
@@ -193,6 +212,9 @@ def library() -> ctypes.CDLL:
     lib.rarn_plan_fp8.argtypes = [c_int, i64, i64, i32, c_int, c_int, c_int, ctypes.c_char_p,
                                   ctypes.c_size_t]
     lib.rarn_plan_fp8.restype = c_int
+    lib.rarn_gated_add_rms_norm.argtypes = [Rows, Rows, Rows, Rows, vp, vp, ctypes.POINTER(Gate),
+                                            f32, f32, i64, i64, f32, vp]
+    lib.rarn_gated_add_rms_norm.restype = c_int
     lib.rarn_gemm_add_rms_norm.argtypes = [Rows, Rows, Rows, Rows, vp, i64, i64, i64, f32, vp,
                                            ctypes.c_size_t, vp]
     lib.rarn_gemm_add_rms_norm.restype = c_int
@@ -249,10 +271,16 @@ def library() -> ctypes.CDLL:
     lib.rarn_kv_cache_write.argtypes = [kc, Heads, Heads, vp, i64, vp]
     lib.rarn_qk_norm_rope_kv_write.argtypes = [Heads, kc, Heads, Heads, Heads, vp, vp, rot, vp,
                                                i64, f32, vp]
+    ra = ctypes.POINTER(RotationAxes)
+    lib.rarn_qk_norm_rope_axes.argtypes = [Heads, Heads, Heads, Heads, vp, vp, ra, i64, i64, f32,
+                                           vp]
+    lib.rarn_qk_norm_rope_axes_kv_write.argtypes = [Heads, kc, Heads, Heads, Heads, vp, vp, ra, vp,
+                                                    i64, f32, vp]
     lib.rarn_kv_cache_read.argtypes = [Heads, Heads, kc, vp, i64, i64, vp, i64, i64, vp]
     lib.rarn_tree_attention.argtypes = [Heads, Heads, kc, vp, i64, i64, vp, vp, vp, i64, i64, i64,
                                         f32, vp, ctypes.c_size_t, vp]
     for f in (lib.rarn_qk_norm_rope, lib.rarn_kv_cache_write, lib.rarn_qk_norm_rope_kv_write,
+              lib.rarn_qk_norm_rope_axes, lib.rarn_qk_norm_rope_axes_kv_write,
               lib.rarn_kv_cache_read, lib.rarn_tree_attention):
         f.restype = c_int
     lib.rarn_tree_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
@@ -807,8 +835,77 @@ def _gamma(name, g, D, dtype, device):
     return g.data_ptr()
 
 
+def _matrix(name, t, T, H, dtype, device):
+    """A [T, H] CUDA tensor with unit stride within a row as a rarn_rows."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != T or shape[1] != H:
+        raise ValueError(f"{name} must be [{T}, {H}], got {list(shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if stride[1] != 1 and H > 1:
+        raise ValueError(f"{name} must have unit stride within a row")
+    code = _codes.get(dtype)
+    if code is None:
+        code = _codes[dtype] = _dtype_code(t)
+    return Rows(t.data_ptr(), stride[0], code)
+
+
+def gated_add_rms_norm(x, residual, x_gamma, gamma, eps: float, gate=None, gate_index=None,
+                       scale: float = 1.0, residual_scale: float = 1.0, out=None,
+                       residual_out=None):
+    """The norms after and before a block with its gate and the residual between
+    them:
+
+        n = x * rsqrt(mean(x^2) + eps) * x_gamma          (x_gamma None: n = x)
+        h = residual_scale * residual + scale * (gate * n)
+        y = h * rsqrt(mean(h^2) + eps) * gamma
+
+    x, residual [T, H]: CUDA tensors with unit stride within a row; the residual
+    of x's type or float32; x_gamma, gamma [H].  gate: [H] (one for all tokens),
+    [T, H], or [rows, H] with ``gate_index`` [T] int32 naming each token's row (a
+    token whose index is outside keeps its output rows and sets watchdog bit 4);
+    None: no gate.  h goes to ``residual_out``, or in place into the residual
+    where that is None.  ``out`` may be x.  Returns y."""
+    import torch
+    dev, dt = x.device, x.dtype
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    rx = _matrix("x", x, T, H, dt, dev)
+    rr = _matrix("residual", residual, T, H, residual.dtype, dev)
+    if residual_out is None or residual_out is residual:
+        rh = rr
+    else:
+        rh = _matrix("residual_out", residual_out, T, H, residual.dtype, dev)
+    if out is None:
+        out = torch.empty(T, H, dtype=dt, device=dev)
+    ry = _matrix("out", out, T, H, dt, dev)
+    xg, g = _gamma("x_gamma", x_gamma, H, dt, dev), _gamma("gamma", gamma, H, dt, dev)
+    pg = None
+    if gate is not None:
+        if gate.dim() == 1:
+            gate = gate[None]
+        n = gate.shape[0]
+        rg = _matrix("gate", gate, n, H, dt, dev)
+        if gate_index is None:
+            if n != 1 and n != T:
+                raise ValueError(f"gate must have one row or {T}, or a gate_index")
+            index = None
+        else:
+            index = _indices("gate_index", gate_index, torch.int32, T, dev)
+        pg = ctypes.byref(Gate(rg.data, rg.row_stride, n, index))
+    elif gate_index is not None:
+        raise ValueError("gate_index needs a gate")
+    _on(dev, "rarn_gated_add_rms_norm", library().rarn_gated_add_rms_norm, ry, rh, rx, rr, xg, g,
+        pg, scale, residual_scale, T, H, eps)
+    return out
+
+
 def _rotation(cos_sin, positions, style, T, device):
-    """The rarn_rotation of a call, or None without a table."""
+    """The rarn_rotation of a call, or None without a table; positions: the
+    tensor, or its address where the caller has checked it."""
     import torch
     code = ROTATION_STYLES.get(style)
     if code is None:
@@ -823,12 +920,57 @@ def _rotation(cos_sin, positions, style, T, device):
         raise ValueError("cos_sin must be [positions, rot_dim]")
     if positions is None:
         raise ValueError("cos_sin needs positions")
-    return Rotation(cos_sin.data_ptr(), _indices("positions", positions, torch.int64, T, device),
-                    shape[0], shape[1], code)
+    if type(positions) is not int:
+        positions = _indices("positions", positions, torch.int64, T, device)
+    return Rotation(cos_sin.data_ptr(), positions, shape[0], shape[1], code)
+
+
+# axis_of_pair of a model's sections, as the C ABI takes it
+_axis_maps = {}   # (pairs, sections, order) -> ctypes array
+
+
+def _axis_map(pairs, sections, order):
+    key = (pairs, sections, order)
+    got = _axis_maps.get(key)
+    if got is None:
+        if order not in SECTION_ORDERS:
+            raise ValueError(f"section_order must be one of {SECTION_ORDERS}")
+        left = [int(n) for n in sections]
+        if not left or min(left) < 0 or sum(left) != pairs:
+            raise ValueError(f"sections must be pairs of each axis, {pairs} in all")
+        if order == "blocks":
+            axes = [a for a, n in enumerate(left) for _ in range(n)]
+        else:
+            axes = []
+            while len(axes) < pairs:
+                for a, n in enumerate(left):
+                    if n:
+                        axes.append(a)
+                        left[a] = n - 1
+        got = _axis_maps[key] = (ctypes.c_uint8 * max(pairs, 1))(*axes)
+    return got
+
+
+def _rotation_axes(cos_sin, positions, style, sections, order, T, device):
+    """The rarn_rotation_axes of a call."""
+    import torch
+    if cos_sin is None or positions is None:
+        raise ValueError("sections need cos_sin and positions")
+    sections = sections if type(sections) is tuple else tuple(sections)
+    A = len(sections)
+    if positions.dtype is not torch.int64 or positions.device != device or not positions.is_cuda:
+        raise TypeError(f"positions must be an int64 CUDA tensor on {device}")
+    shape, stride = positions.shape, positions.stride()
+    if len(shape) != 2 or shape[0] != A or shape[1] != T or (T > 1 and stride[1] != 1):
+        raise ValueError(f"positions must be [{A}, {T}] with unit stride along the tokens")
+    rot = _rotation(cos_sin, positions.data_ptr(), style, T, device)
+    amap = _axis_map(rot.rot_dim // 2, sections, order)
+    return RotationAxes(rot, A, stride[0], ctypes.addressof(amap))
 
 
 def qk_norm_rope(q, k, q_gamma, k_gamma, eps: float, cos_sin=None, positions=None,
-                 style: str = "half", q_out=None, k_out=None):
+                 style: str = "half", q_out=None, k_out=None, sections=None,
+                 section_order: str = "blocks"):
     """RMSNorm of every query and key head over its D elements, times gamma,
     then the position rotation; returns (q_out, k_out).
 
@@ -839,7 +981,14 @@ def qk_norm_rope(q, k, q_gamma, k_gamma, eps: float, cos_sin=None, positions=Non
     None for no rotation; positions: [T] int64; style: "half" rotates elements
     (i, i + rot_dim / 2), "interleaved" (2i, 2i + 1).  q_out may be q, k_out k.
     A token whose position is outside the table keeps its output rows and sets
-    watchdog bit 4."""
+    watchdog bit 4.
+
+    Positions of several axes (time, height, width): positions [axes, T] (unit
+    stride along the tokens) and ``sections``, the rotation's pairs of each of up
+    to four axes (a tuple; rot_dim / 2 in all).  section_order "blocks": the
+    first axis's pairs, then the second's and so on; "cyclic": the axes in turn,
+    one that has used its pairs up left out.  Pair i turns by column i of the
+    table at its axis's position."""
     import torch
     dev, dt = q.device, q.dtype
     if q.dim() != 3:
@@ -851,10 +1000,15 @@ def qk_norm_rope(q, k, q_gamma, k_gamma, eps: float, cos_sin=None, positions=Non
         q_out = torch.empty(q.shape, dtype=dt, device=dev)
     if k_out is None:
         k_out = torch.empty(k.shape, dtype=dt, device=dev)
-    _on(dev, "rarn_qk_norm_rope", library().rarn_qk_norm_rope,
-        _heads("q_out", q_out, T, Hq, D, dt, dev), _heads("k_out", k_out, T, hk.heads, D, dt, dev),
-        hq, hk, _gamma("q_gamma", q_gamma, D, dt, dev), _gamma("k_gamma", k_gamma, D, dt, dev),
-        _rotation(cos_sin, positions, style, T, dev), T, D, eps)
+    if sections is None:
+        what, rot = "rarn_qk_norm_rope", _rotation(cos_sin, positions, style, T, dev)
+    else:
+        what = "rarn_qk_norm_rope_axes"
+        rot = _rotation_axes(cos_sin, positions, style, sections, section_order, T, dev)
+    _on(dev, what, getattr(library(), what), _heads("q_out", q_out, T, Hq, D, dt, dev),
+        _heads("k_out", k_out, T, hk.heads, D, dt, dev), hq, hk,
+        _gamma("q_gamma", q_gamma, D, dt, dev), _gamma("k_gamma", k_gamma, D, dt, dev), rot, T, D,
+        eps)
     return q_out, k_out
 
 
@@ -936,21 +1090,26 @@ def kv_cache_write(k, v, cache: KVCache, slots) -> None:
 
 
 def qk_norm_rope_kv_write(q, k, v, q_gamma, k_gamma, eps: float, cos_sin, positions,
-                          cache: KVCache, slots, style: str = "half", q_out=None):
+                          cache: KVCache, slots, style: str = "half", q_out=None, sections=None,
+                          section_order: str = "blocks"):
     """qk_norm_rope and kv_cache_write in one pass: returns the normalised,
     rotated queries; the keys (quantised from their binary32 values) and values
-    go to the cache."""
+    go to the cache.  ``sections``, ``section_order``: positions of several axes,
+    as in qk_norm_rope."""
     import torch
     dev, dt, H, D = cache.device, q.dtype, cache.heads, cache.head_dim
     T = q.shape[0]
     hq = _heads("q", q, T, None, D, dt, dev)
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=dt, device=dev)
-    _on(dev, "rarn_qk_norm_rope_kv_write", library().rarn_qk_norm_rope_kv_write,
-        _heads("q_out", q_out, T, hq.heads, D, dt, dev), cache._ref, hq,
-        _heads("k", k, T, H, D, dt, dev), _heads("v", v, T, H, D, dt, dev),
-        _gamma("q_gamma", q_gamma, D, dt, dev), _gamma("k_gamma", k_gamma, D, dt, dev),
-        _rotation(cos_sin, positions, style, T, dev),
+    if sections is None:
+        what, rot = "rarn_qk_norm_rope_kv_write", _rotation(cos_sin, positions, style, T, dev)
+    else:
+        what = "rarn_qk_norm_rope_axes_kv_write"
+        rot = _rotation_axes(cos_sin, positions, style, sections, section_order, T, dev)
+    _on(dev, what, getattr(library(), what), _heads("q_out", q_out, T, hq.heads, D, dt, dev),
+        cache._ref, hq, _heads("k", k, T, H, D, dt, dev), _heads("v", v, T, H, D, dt, dev),
+        _gamma("q_gamma", q_gamma, D, dt, dev), _gamma("k_gamma", k_gamma, D, dt, dev), rot,
         _indices("slots", slots, torch.int64, T, dev), T, eps)
     return q_out
 

@@ -43,6 +43,11 @@ struct RowParams {
     int64_t table_rows;
     int rot;
     int interleaved;
+    // several axes: axis a's position of token t is positions[a * axis_stride + t],
+    // pair i turns by axis_of's bits 2i and 2i + 1; axes == 0: one position a token
+    int axes;
+    int64_t axis_stride;
+    uint32_t axis_of[32];
     const int64_t *slots;   // cache slot of each token, < 0: not written
     Cache cache;            // cache.k == nullptr: none
     int64_t T;
@@ -119,6 +124,55 @@ __device__ __forceinline__ const float *table_row(const RowParams &p, int64_t po
     return p.table + pos * p.rot;
 }
 
+// Where a token's angles stand: a row of the table, or one for each axis.
+constexpr int kMaxAxes = 4;
+
+template <bool kAxes>
+struct Angles {
+    const float *row[kAxes ? kMaxAxes : 1];
+
+    // From the token's positions; *ok = false when one lies outside the table.
+    __device__ __forceinline__ void find(const RowParams &p, const int64_t (&pos)[kMaxAxes],
+                                         bool reporter, bool *ok) {
+        *ok = true;
+        if constexpr (kAxes) {
+#pragma unroll
+            for (int a = 0; a < kMaxAxes; ++a) {
+                bool in = true;
+                row[a] = a < p.axes ? table_row(p, pos[a], reporter, &in) : nullptr;
+                *ok = *ok && in;
+            }
+        } else {
+            row[0] = table_row(p, pos[0], reporter, ok);
+        }
+    }
+
+    __device__ __forceinline__ const float *of(unsigned axis) const {
+        if constexpr (kAxes)
+            return axis == 0 ? row[0] : axis == 1 ? row[1] : axis == 2 ? row[2] : row[3];
+        else
+            return row[0];
+    }
+};
+
+// Token t's positions, one or one for each axis.
+template <bool kAxes>
+__device__ __forceinline__ void load_positions(const RowParams &p, int64_t t,
+                                               int64_t (&pos)[kMaxAxes]) {
+    if constexpr (kAxes) {
+#pragma unroll
+        for (int a = 0; a < kMaxAxes; ++a)
+            pos[a] = a < p.axes ? p.positions[a * p.axis_stride + t] : 0;
+    } else {
+        pos[0] = p.table ? p.positions[t] : 0;
+    }
+}
+
+// The axes of pairs i .. (16 to a word, i a multiple of four).
+__device__ __forceinline__ unsigned axes_from(const RowParams &p, int i) {
+    return p.axis_of[i >> 4] >> (2 * (i & 15));
+}
+
 template <int LG>
 __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
@@ -193,7 +247,9 @@ constexpr int kRowCtas = 5;
 // A warp: one token, `per` heads of one tensor for each group of LG lanes.
 // The work items of a token are its tensors' chunks of per * 32 / LG heads,
 // `chunks` in all (nq of q, then nk of k, then those of v).
-template <typename T, int LG, bool kInter>
+// With several axes a lane's pairs may turn by different rows of the table: four
+// neighbouring pairs of one axis are read together, others one by one.
+template <typename T, int LG, bool kInter, bool kAxes>
 __global__ void __launch_bounds__(128, kRowCtas)
     k_head_rows(const RowParams p, int per, int nq, int nk, int chunks) {
     constexpr int E = DT<T>::EPV;  // elements per pack
@@ -220,7 +276,8 @@ __global__ void __launch_bounds__(128, kRowCtas)
     const int eb = turns && !kInter ? p.rot / 2 + l * E : ea + E;
 
     // first what the other loads wait for
-    const int64_t pos = p.table ? p.positions[t] : 0;
+    int64_t pos[kMaxAxes];
+    load_positions<kAxes>(p, t, pos);
     const int64_t slot = r.codes ? p.slots[t] : -1;
     const T *src = reinterpret_cast<const T *>(r.src);
     auto load = [&](int h, uint4 &a, uint4 &b) {
@@ -237,7 +294,8 @@ __global__ void __launch_bounds__(128, kRowCtas)
     for (int u = 0; u < U; ++u) load(h0 + u * GPW, xa[u], xb[u]);
 
     bool ok;
-    const float *tr = table_row(p, pos, lane == 0, &ok);
+    Angles<kAxes> at;
+    at.find(p, pos, lane == 0, &ok);
     if (!ok) return;  // the whole warp: one token
     const Place pl = place_of(p, slot, lane == 0);
     // gamma, and its products with the cosines and sines
@@ -252,9 +310,20 @@ __global__ void __launch_bounds__(128, kRowCtas)
         if (turns) {
 #pragma unroll
             for (int j = 0; j < E; j += 4) {
-                const float4 c = __ldg(reinterpret_cast<const float4 *>(tr + l * E + j));
-                const float4 s =
-                    __ldg(reinterpret_cast<const float4 *>(tr + p.rot / 2 + l * E + j));
+                float4 c, s;
+                const unsigned four = kAxes ? axes_from(p, l * E + j) & 0xffu : 0u;
+                const float *tr = at.of(four & 3u) + l * E + j;
+                if (!kAxes || four == (four & 3u) * 0x55u) {
+                    c = __ldg(reinterpret_cast<const float4 *>(tr));
+                    s = __ldg(reinterpret_cast<const float4 *>(tr + p.rot / 2));
+                } else {
+                    const float *t1 = at.of(four >> 2 & 3u) + l * E + j + 1;
+                    const float *t2 = at.of(four >> 4 & 3u) + l * E + j + 2;
+                    const float *t3 = at.of(four >> 6) + l * E + j + 3;
+                    c = make_float4(__ldg(tr), __ldg(t1), __ldg(t2), __ldg(t3));
+                    s = make_float4(__ldg(tr + p.rot / 2), __ldg(t1 + p.rot / 2),
+                                    __ldg(t2 + p.rot / 2), __ldg(t3 + p.rot / 2));
+                }
                 const float cj[4] = {c.x, c.y, c.z, c.w}, sj[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
@@ -357,7 +426,7 @@ __global__ void __launch_bounds__(128, kRowCtas)
 // Any head size, rotation width, stride and alignment: a warp per head, a
 // lane per rotation pair (then per unrotated element), the row re-read from
 // L1 for each of its passes.
-template <typename T>
+template <typename T, bool kAxes>
 __global__ void __launch_bounds__(128) k_head_rows_any(const RowParams p, int heads) {
     grid_dependency_wait();
     grid_launch_dependents();
@@ -377,7 +446,10 @@ __global__ void __launch_bounds__(128) k_head_rows_any(const RowParams p, int he
     }
     const Role r = role_of<T>(p, t, which);
     bool ok;
-    const float *tr = table_row(p, p.table ? p.positions[t] : 0, lane == 0, &ok);
+    int64_t pos[kMaxAxes];
+    load_positions<kAxes>(p, t, pos);
+    Angles<kAxes> at;
+    at.find(p, pos, lane == 0, &ok);
     if (!ok) return;
     const Place pl = place_of(p, r.codes ? p.slots[t] : -1, lane == 0);
     const T *src = reinterpret_cast<const T *>(r.src) + h * r.src_hs;
@@ -390,7 +462,7 @@ __global__ void __launch_bounds__(128) k_head_rows_any(const RowParams p, int he
         }
         inv = rsqrtf(fmaf(warp_sum(ss), 1.f / static_cast<float>(p.D), p.eps));
     }
-    const bool turn = r.rotate && tr;
+    const bool turn = r.rotate && at.row[0];
     const int half = turn ? p.rot / 2 : 0;
     const int work = half + (p.D - 2 * half);  // pairs, then single elements
     auto normed = [&](int e) {
@@ -403,6 +475,7 @@ __global__ void __launch_bounds__(128) k_head_rows_any(const RowParams p, int he
             e0 = p.interleaved ? 2 * i : i;
             e1 = p.interleaved ? 2 * i + 1 : half + i;
             const float x = normed(e0), y = normed(e1);
+            const float *tr = at.of(kAxes ? axes_from(p, i & ~3) >> (2 * (i & 3)) & 3u : 0u);
             const float c = __ldg(tr + i), s = __ldg(tr + half + i);
             a = x * c - y * s;
             b = y * c + x * s;

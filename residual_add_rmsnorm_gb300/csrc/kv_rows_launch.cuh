@@ -13,7 +13,7 @@ namespace kv {
 constexpr int kRowHeads = 8;
 constexpr int kRowWarps = 16;
 
-template <typename T, int LG, bool kInter>
+template <typename T, int LG, bool kInter, bool kAxes>
 inline cudaError_t launch_head_group(const RowParams &p, int num_sms, bool pdl, cudaStream_t st) {
     constexpr int gpw = 32 / LG;
     auto chunks_of = [](int heads, int per) { return (heads + per * gpw - 1) / (per * gpw); };
@@ -28,14 +28,17 @@ inline cudaError_t launch_head_group(const RowParams &p, int num_sms, bool pdl, 
         if (per == 1 || p.T * (nq + nk + nv) >= (int64_t)num_sms * kRowWarps) break;
     }
     const int chunks = nq + nk + nv;
-    return launch_kernel(k_head_rows<T, LG, kInter>, dim3((unsigned)((p.T + 3) / 4 * chunks)),
-                         dim3(128), 0, st, pdl, 1, p, per, nq, nk, chunks);
+    return launch_kernel(k_head_rows<T, LG, kInter, kAxes>,
+                         dim3((unsigned)((p.T + 3) / 4 * chunks)), dim3(128), 0, st, pdl, 1, p, per, nq, nk, chunks);
 }
 
 template <typename T, int LG>
 inline cudaError_t launch_head_style(const RowParams &p, int num_sms, bool pdl, cudaStream_t st) {
-    return p.interleaved ? launch_head_group<T, LG, true>(p, num_sms, pdl, st)
-                         : launch_head_group<T, LG, false>(p, num_sms, pdl, st);
+    if (p.axes)
+        return p.interleaved ? launch_head_group<T, LG, true, true>(p, num_sms, pdl, st)
+                             : launch_head_group<T, LG, false, true>(p, num_sms, pdl, st);
+    return p.interleaved ? launch_head_group<T, LG, true, false>(p, num_sms, pdl, st)
+                         : launch_head_group<T, LG, false, false>(p, num_sms, pdl, st);
 }
 
 template <typename T>
@@ -43,8 +46,11 @@ cudaError_t launch_head_rows(const RowParams &p, bool vec, int num_sms, bool pdl
                              cudaStream_t st) {
     if (!vec) {
         const int heads = p.q.heads + p.k.heads + p.v.heads;
-        return launch_kernel(k_head_rows_any<T>, dim3((unsigned)((p.T * heads + 3) / 4)),
-                             dim3(128), 0, st, pdl, 1, p, heads);
+        const dim3 grid((unsigned)((p.T * heads + 3) / 4));
+        return p.axes ? launch_kernel(k_head_rows_any<T, true>, grid, dim3(128), 0, st, pdl, 1, p,
+                                      heads)
+                      : launch_kernel(k_head_rows_any<T, false>, grid, dim3(128), 0, st, pdl, 1, p,
+                                      heads);
     }
     const int lanes = p.D / (2 * DT<T>::EPV);
     if (lanes <= 4) return launch_head_style<T, 4>(p, num_sms, pdl, st);

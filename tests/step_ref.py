@@ -1,0 +1,62 @@
+"""Binary64 definitions of a step's operators on CPU tensors, and the error
+bounds that their GPU tests use.
+
+Bounds (h(t) = eps(t) / 2, a type's half step; u = 2^-24):
+  * gated norms.  A row sum of squares: a thread's run of k = ceil(H / 32) terms at
+    most, a tree of at most 10 levels, one product and one sum: (k + 14) u; its
+    reciprocal root half of that and 2^-22; the products with x, gamma, gate and
+    scale, residual_scale's and the sum 8 u.  In all E = (k / 2 + 24) u times the
+    magnitudes |residual_scale r| + |scale gate n|, then one rounding to the
+    residual's type.  y is compared with the norm of the h that the kernel stored:
+    E |y|, then one rounding.
+"""
+from __future__ import annotations
+
+import torch
+
+F64 = torch.float64
+
+
+def half(dt):
+    return torch.finfo(dt).eps / 2
+
+
+def tiny(dt):
+    """Half the smallest subnormal step."""
+    return torch.finfo(dt).smallest_normal * torch.finfo(dt).eps / 2
+
+
+def norm(x, gamma, eps):
+    x = x.to(F64)
+    return x / torch.sqrt((x * x).mean(-1, keepdim=True) + eps) * gamma.to(F64)
+
+
+def row_error(H):
+    return ((H + 31) // 32 / 2 + 24) * 2.0 ** -24
+
+
+def check_block(y, h, x, residual, x_gamma, gamma, eps, gate=None, scale=1.0, residual_scale=1.0,
+                what=""):
+    """y and h (what came of the call, on the host) against the formulas; gate: [T, H] or None."""
+    H = x.shape[1]
+    n = x.to(F64) if x_gamma is None else norm(x, x_gamma, eps)
+    if gate is not None:
+        n = n * gate.to(F64)
+    a, b = residual_scale * residual.to(F64), scale * n
+    want, err = a + b, row_error(H)
+    bound = half(h.dtype) * (want.abs() + err * (a.abs() + b.abs())) + \
+        err * (a.abs() + b.abs()) + tiny(h.dtype)
+    within(h, want, bound, f"{what} h")
+    want = norm(h, gamma, eps)
+    within(y, want, half(y.dtype) * want.abs() * (1 + err) + err * want.abs() + tiny(y.dtype),
+           f"{what} y")
+
+
+def within(got, want, bound, what):
+    got = got.to(F64)
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), f"{what}: NaN pattern"
+    err = torch.where(torch.isnan(want) | (got == want), torch.zeros_like(want),
+                      (got - want).abs())
+    bad = ~(err <= torch.nan_to_num(bound, posinf=float("inf")))
+    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} off, worst "
+                           f"{float((err / bound).nan_to_num().max()):.3g} of the bound")
