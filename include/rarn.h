@@ -800,6 +800,77 @@ int64_t rarn_tree_attention_workspace_bytes(int64_t tokens, int64_t B, int64_t q
 rarn_status rarn_plan_tree_attention(int64_t tokens, int64_t B, int64_t q_heads, int64_t kv_heads,
                                      int64_t D, int64_t page_size, char *out, size_t cap);
 
+/*
+ * A step's pages, slots and positions, made on the device from the sequences'
+ * lengths, so that one captured step serves all later lengths.
+ *
+ * A rarn_kv_pages holds which pages of a cache are free and which each sequence
+ * has: sequence b (a row of page_table, as the calls above take it) holds the
+ * pages page_table[b * table_stride + i], i < held[b], in the order of its
+ * tokens; free_pages[0 .. free_count[0] - 1] are free.  All of it is the
+ * caller's device memory, updated in place by the two calls: at the start held
+ * is zero and free_pages any order of all pages; ticket is one word of the
+ * calls' own, zero at the start.  A page belongs to one sequence at a time.
+ * Calls on the same pages must be ordered.  sequences: at most
+ * RARN_MAX_STEP_SEQUENCES; table_width * page_size at most 2^31 - 1.
+ */
+#define RARN_MAX_STEP_SEQUENCES 8192
+
+typedef struct rarn_kv_pages {
+    int32_t *page_table;   /* [sequences, table_width] */
+    int64_t table_stride, table_width;
+    int32_t *held;         /* [sequences] */
+    int32_t *free_pages;   /* [num_pages] */
+    int32_t *free_count;   /* [1] */
+    uint32_t *ticket;      /* [1] */
+    int64_t sequences, num_pages;
+    int32_t page_size;
+} rarn_kv_pages;
+
+/*
+ * new_lens[b] new tokens of sequence b behind its context_lens[b] cached ones: the
+ * pages that they need and the sequence does not hold are taken from the end
+ * of the free ones, in order of sequences and tokens.  Then
+ *   starts[b]     rows of the sequences before b (B + 1 values);
+ *   positions[r]  context_lens[b] + r - starts[b], for row r of sequence b;
+ *   slots[r]      page * page_size + slot of that token, as
+ *                 rarn_kv_cache_write takes it;
+ * rows starts[B] .. tokens - 1 get slot -1 and position 0 (padding that the
+ * writes leave out).  A sequence with new_lens 0 has no rows and keeps its pages.
+ * served[0]: how many sequences were served.  It is B unless rows or pages run
+ * out: the first sequence whose rows would pass `tokens` or whose pages the free
+ * ones, and all behind it, get no rows and no pages.  A sequence whose lengths
+ * are negative or need more than table_width pages, or that holds fewer pages
+ * than its cached tokens fill, has no rows; that, and a page outside 0 ..
+ * num_pages - 1 (slot -1), sets bit 4 of the watchdog word.
+ */
+rarn_status rarn_kv_step(const rarn_kv_pages *pages, const int32_t *context_lens,
+                         const int32_t *new_lens, int32_t *starts, int64_t *slots,
+                         int64_t *positions, int32_t *served, int64_t tokens, void *stream);
+
+/*
+ * Every sequence keeps the pages of its first lens[b] tokens (0: a finished
+ * sequence) and gives back the others, whose table entries become -1: pages of
+ * refused drafts return in the order from which rarn_kv_step takes the same
+ * ones again.  A negative length keeps its pages; that, a page outside, or more
+ * pages than there are (nothing is then done) set bit 4.
+ */
+rarn_status rarn_kv_trim(const rarn_kv_pages *pages, const int32_t *lens, void *stream);
+
+/*
+ * The tokens of an accepted path moved together: token context_lens[b] +
+ * path[b, j] of sequence b goes to context_lens[b] + j, codes and scales of all
+ * heads, j = 1 .. lengths[b] - 1; path (dense [B, path_width]) and lengths as
+ * rarn_verify_drafts writes them.  A path must rise from path[b, 0] >= 0: from an
+ * entry that does not, the sequence's tokens stay; they stay, too, where a page
+ * is missing.  Either, and a length over path_width (taken as that), sets bit 4.
+ */
+rarn_status rarn_kv_cache_compact(const rarn_kv_cache *cache, const int32_t *page_table,
+                                  int64_t table_stride, int64_t table_width,
+                                  const int32_t *context_lens, const int32_t *path,
+                                  const int32_t *lengths, int64_t B, int64_t path_width,
+                                  void *stream);
+
 /* Rows that one launch sequence of rarn_gemm_add_rms_norm_noalloc covers for
  * a row length H: floor(floor((2^20 - 16) / (H / 128 + 1)) / 128) * 128
  * (16128 at H = 8192, 8064 at H = 16384); -1 if H is not supported. */

@@ -22,6 +22,14 @@ attention of drafted tokens over it):
     kv_cache_read(cache, page_table, starts, k_out, v_out)
     tree_attention(q, cache, page_table, context_lens, starts, mask=mask)
 
+A step of drafted tokens (pages, slots and positions from the sequences' lengths;
+the drafts' verification; the cache's tidying after it):
+
+    pages = KVPages.empty(sequences, width, num_pages, page_size)
+    starts, slots, positions, served = kv_step(pages, context_lens, new_lens, tokens)
+    kv_cache_compact(cache, pages.page_table, context_lens, path, lengths)
+    kv_trim(pages, kept_lens)
+
 8-bit output (e4m3 / e5m2 codes with a per-tensor or per-row scale):
 
     rms_norm_fp8(x, gamma, eps, out, scale, fmt="e4m3", scale_mode="tensor")
@@ -50,7 +58,8 @@ __all__ = ["rms_norm", "fused_add_rms_norm", "reduce_add_rms_norm", "rms_norm_ho
            "IPC_HANDLE_BYTES", "qk_norm_rope", "KVCache", "kv_cache_write",
            "qk_norm_rope_kv_write", "kv_cache_read", "tree_attention",
            "tree_attention_workspace_bytes", "plan_tree_attention", "ROTATION_STYLES",
-           "SECTION_ORDERS", "gated_add_rms_norm"]
+           "SECTION_ORDERS", "gated_add_rms_norm", "KVPages", "kv_step", "kv_trim",
+           "kv_cache_compact", "MAX_STEP_SEQUENCES"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "librarn.so")
@@ -90,6 +99,7 @@ class Rows(ctypes.Structure):
                 ("dtype", ctypes.c_int)]
 
 
+MAX_STEP_SEQUENCES = 8192
 TP_MAX_RANKS = 8
 TP_SIGNAL_BYTES = 1024 * TP_MAX_RANKS * 4
 IPC_HANDLE_BYTES = 96
@@ -149,6 +159,15 @@ class KvCacheDesc(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("format", ctypes.c_int),
                 ("scale_mode", ctypes.c_int)]
+
+
+class KvPagesDesc(ctypes.Structure):
+    """``rarn_kv_pages``."""
+    _fields_ = [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("table_width", ctypes.c_int64), ("held", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p),
+                ("ticket", ctypes.c_void_p), ("sequences", ctypes.c_int64),
+                ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32)]
 
 
 _lib = None
@@ -282,6 +301,12 @@ def library() -> ctypes.CDLL:
     for f in (lib.rarn_qk_norm_rope, lib.rarn_kv_cache_write, lib.rarn_qk_norm_rope_kv_write,
               lib.rarn_qk_norm_rope_axes, lib.rarn_qk_norm_rope_axes_kv_write,
               lib.rarn_kv_cache_read, lib.rarn_tree_attention):
+        f.restype = c_int
+    kp = ctypes.POINTER(KvPagesDesc)
+    lib.rarn_kv_step.argtypes = [kp, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.rarn_kv_trim.argtypes = [kp, vp, vp]
+    lib.rarn_kv_cache_compact.argtypes = [kc, vp, i64, i64, vp, vp, vp, i64, i64, vp]
+    for f in (lib.rarn_kv_step, lib.rarn_kv_trim, lib.rarn_kv_cache_compact):
         f.restype = c_int
     lib.rarn_tree_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
     lib.rarn_tree_attention_workspace_bytes.restype = i64
@@ -1198,6 +1223,95 @@ def tree_attention(q, cache: KVCache, page_table, context_lens, starts, mask=Non
         stride, width, ctx, st, pm, words, B, N, D ** -0.5 if scale is None else scale,
         workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
+
+
+class KVPages:
+    """Which pages of a cache each sequence holds and which are free: the state that
+    kv_step and kv_trim update in place.  Int32 CUDA tensors of the caller's:
+    page_table [sequences, width] (unit stride along a row; what tree_attention and
+    kv_cache_read take), held [sequences], free_pages [num_pages], free_count [1].
+    A page belongs to one sequence at a time; calls on one object must be
+    ordered."""
+
+    def __init__(self, page_table, held, free_pages, free_count, page_size: int):
+        import torch
+        dev = page_table.device
+        table, stride, B, width = _page_table(page_table, dev)
+        self.page_table, self.held = page_table, held
+        self.free_pages, self.free_count = free_pages, free_count
+        self.device, self.page_size = dev, page_size
+        self.sequences, self.num_pages = B, free_pages.numel()
+        self._ticket = torch.zeros(1, dtype=torch.int32, device=dev)
+        i32 = torch.int32
+        self._desc = KvPagesDesc(table, stride, width, _indices("held", held, i32, B, dev),
+                                 _indices("free_pages", free_pages, i32, self.num_pages, dev),
+                                 _indices("free_count", free_count, i32, 1, dev),
+                                 self._ticket.data_ptr(), B, self.num_pages, page_size)
+        self._ref = ctypes.byref(self._desc)
+
+    @classmethod
+    def empty(cls, sequences: int, width: int, num_pages: int, page_size: int, device="cuda"):
+        """Tensors of its own: no sequence holds a page, page 0 is the first taken."""
+        import torch
+        kw = dict(dtype=torch.int32, device=device)
+        return cls(torch.full((sequences, width), -1, **kw), torch.zeros(sequences, **kw),
+                   torch.arange(num_pages - 1, -1, -1, **kw), torch.full((1,), num_pages, **kw),
+                   page_size)
+
+
+def kv_step(pages: KVPages, context_lens, new_lens, tokens: int, starts=None, slots=None,
+            positions=None, served=None):
+    """Pages, slots and positions of a step: sequence b adds new_lens[b] tokens
+    behind its context_lens[b] (int32 CUDA tensors of pages.sequences values), and
+    gets the pages that they need.  Returns (starts [B + 1] int32, slots [tokens]
+    int64, positions [tokens] int64, served [1] int32): row r of sequence b is r -
+    starts[b] tokens behind its context; rows past the last sequence get slot -1 and
+    position 0.  served < B: rows (``tokens``) or free pages ran out at that
+    sequence, and it and those behind it got none.  Lengths that make no sense
+    leave their sequence without rows and set watchdog bit 4."""
+    import torch
+    dev, B = pages.device, pages.sequences
+    if starts is None:
+        starts = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    if slots is None:
+        slots = torch.empty(tokens, dtype=torch.int64, device=dev)
+    if positions is None:
+        positions = torch.empty(tokens, dtype=torch.int64, device=dev)
+    if served is None:
+        served = torch.empty(1, dtype=torch.int32, device=dev)
+    i32, i64 = torch.int32, torch.int64
+    _on(dev, "rarn_kv_step", library().rarn_kv_step, pages._ref,
+        _indices("context_lens", context_lens, i32, B, dev),
+        _indices("new_lens", new_lens, i32, B, dev), _indices("starts", starts, i32, B + 1, dev),
+        _indices("slots", slots, i64, tokens, dev),
+        _indices("positions", positions, i64, tokens, dev),
+        _indices("served", served, i32, 1, dev), tokens)
+    return starts, slots, positions, served
+
+
+def kv_trim(pages: KVPages, lens) -> None:
+    """Every sequence keeps the pages of its first lens[b] tokens (int32 CUDA
+    tensor; 0: a finished sequence) and gives the others back."""
+    import torch
+    _on(pages.device, "rarn_kv_trim", library().rarn_kv_trim, pages._ref,
+        _indices("lens", lens, torch.int32, pages.sequences, pages.device))
+
+
+def kv_cache_compact(cache: KVCache, page_table, context_lens, path, lengths) -> None:
+    """The tokens of an accepted path moved together: token context_lens[b] +
+    path[b, j] goes to context_lens[b] + j, j = 1 .. lengths[b] - 1, with its scales.
+    path: [B, width] int32, rising along a row; lengths: [B] int32 (as
+    verify_drafts returns them)."""
+    import torch
+    dev = cache.device
+    table, stride, B, width = _page_table(page_table, dev)
+    if path.dim() != 2 or path.shape[0] != B:
+        raise ValueError(f"path must be [{B}, width]")
+    W = path.shape[1]
+    _on(dev, "rarn_kv_cache_compact", library().rarn_kv_cache_compact, cache._ref, table, stride,
+        width, _indices("context_lens", context_lens, torch.int32, B, dev),
+        _indices("path", path, torch.int32, B * W, dev),
+        _indices("lengths", lengths, torch.int32, B, dev), B, W)
 
 
 def launch_floor(grid: int, block: int, rows=None, row_bytes: int = 0) -> None:

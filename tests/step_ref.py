@@ -60,3 +60,53 @@ def within(got, want, bound, what):
     bad = ~(err <= torch.nan_to_num(bound, posinf=float("inf")))
     assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} off, worst "
                            f"{float((err / bound).nan_to_num().max()):.3g} of the bound")
+
+
+class Pages:
+    """The pages of a step, sequence by sequence: a model of KVPages on the host."""
+
+    def __init__(self, sequences, width, num_pages, page_size, free=None):
+        self.width, self.num, self.page = width, num_pages, page_size
+        self.has = [[] for _ in range(sequences)]
+        self.free = list(range(num_pages - 1, -1, -1)) if free is None else list(free)
+
+    def step(self, context, new, tokens):
+        """(starts, slots, positions, served, whether a sequence made no sense)."""
+        starts, slots, positions, bad = [0], [], [], False
+        served = len(self.has)
+        plan = []
+        rows = pages = 0
+        for b, (c, n) in enumerate(zip(context, new)):
+            need = 0
+            if n != 0 and (n < 0 or c < 0 or len(self.has[b]) * self.page < c or
+                           c + n > self.width * self.page):
+                bad, n = True, 0
+            if n:
+                need = max(0, -(-(c + n) // self.page) - len(self.has[b]))
+            plan.append((n, need))
+            rows, pages = rows + n, pages + need
+            if (rows > tokens or pages > len(self.free)) and served == len(self.has):
+                served = b
+        for b, (n, need) in enumerate(plan):
+            if b < served:
+                self.has[b] += [self.free.pop() for _ in range(need)]
+                for t in range(context[b], context[b] + n):
+                    page = self.has[b][t // self.page]
+                    slots.append(page * self.page + t % self.page)
+                    positions.append(t)
+            starts.append(len(slots))
+        pad = tokens - len(slots)
+        return starts, slots + [-1] * pad, positions + [0] * pad, served, bad
+
+    def trim(self, lens):
+        back = []
+        for b, n in enumerate(lens):
+            if n < 0:
+                continue
+            keep = min(len(self.has[b]), -(-n // self.page))
+            back += self.has[b][keep:]
+            del self.has[b][keep:]
+        self.free += back[::-1]
+
+    def table(self):
+        return [h + [-1] * (self.width - len(h)) for h in self.has]

@@ -49,7 +49,8 @@ CASES = [
     (9, 3, 3, 80, 80, (10, 15, 15), 0), (6, 4, 2, 96, 64, (0, 20, 12), 0),
     (5, 2, 1, 64, 32, (4, 4, 4, 4), 0), (7, 2, 1, 129, 126, (13, 30, 20), 0),
     (11, 4, 2, 128, 128, (16, 24, 24), 3), (3, 2, 2, 1000, 1000, (100, 200, 200), 0),
-    (2, 1, 1, 2, 2, (1, 0), 0), (4, 3, 1, 256, 256, (1, 126, 1), 0), (3, 2, 1, 512, 512, (56, 200), 0),
+    (2, 1, 1, 2, 2, (1, 0), 0), (4, 3, 1, 256, 256, (1, 126, 1), 0),
+    (3, 2, 1, 512, 512, (56, 200), 0),
 ]
 
 
