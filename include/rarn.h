@@ -858,6 +858,54 @@ rarn_status rarn_kv_step(const rarn_kv_pages *pages, const int32_t *context_lens
 rarn_status rarn_kv_trim(const rarn_kv_pages *pages, const int32_t *lens, void *stream);
 
 /*
+ * Verification of drafted tokens against the target model's probabilities, from
+ * given random numbers, and the draw of the token behind the accepted ones.
+ *
+ * Sequence b's rows are starts[b] .. starts[b + 1] - 1 of probs [rows, vocab], as
+ * in rarn_tree_attention: row 0 is its last known token, the others are drafts.
+ * Row r is the target's distribution behind that row's token; tokens[r] is row
+ * r's token; its parent is row parents[r] of its sequence (parents[r] < r, not
+ * read for row 0), or the row before without parents (a chain).  With p a row's
+ * probabilities and u = uniforms[row] in [0, 1), the draft r below it with
+ * token x is accepted where
+ *   u * q(x) < p(x)         with draft_probs, row r of which is the distribution q
+ *                           that x was drawn from (chains only);
+ *   s <= u < s + p(x)       without: s the sum of p over the other tokens of its
+ *                           earlier siblings (a token drafted twice: the first
+ *                           time counts), so that at most one sibling is.
+ * From row 0 the accepted drafts make a path of at most `most` drafts.  The next
+ * token is drawn at its last row: the smallest x for which w(0) + .. + w(x) is
+ * more than final_uniforms[b] times w's sum, where w is max(p - q, 0) of the
+ * refused draft, or p without the refused children's tokens; p itself where none
+ * was refused (the drafts end, or the path has `most` of them) or where that
+ * leaves nothing.  Tokens so drawn are distributed as the target's own.
+ *
+ * lengths[b]: rows of the path, 1 + accepted drafts; path[b, 0 .. lengths[b] - 1]:
+ * these rows (path[b, 0] = 0); new_tokens[b, 0 .. lengths[b] - 1]: the accepted
+ * drafts' tokens and the drawn one.  Both dense [B, most + 1]; entries behind are
+ * -1.  A sequence without rows has length 0.
+ *
+ * probs and draft_probs have one type, any of the three, and any row stride;
+ * values are taken as 0 .. 1 (NaN as 0) and rounded to multiples of 2^-46 for
+ * the sums, which are exact from there on.  A row whose weights sum to 0, or to
+ * 2 or more, gives the token -1 and sets bit 4 of the watchdog word, as do
+ * tokens outside 0 .. vocab - 1 and parents outside 0 .. r - 1 (such a draft is
+ * refused and takes nothing), starts that fall or lie outside and trees of more
+ * than RARN_MAX_VERIFY_TREE rows (length 0).  vocab is at most
+ * RARN_MAX_VERIFY_VOCAB; draft_probs together with parents:
+ * RARN_ERR_UNSUPPORTED.  Any overlap of an output: RARN_ERR_ALIAS.
+ */
+#define RARN_MAX_VERIFY_VOCAB (1 << 20)
+#define RARN_MAX_VERIFY_TREE 1024
+
+rarn_status rarn_verify_drafts(int64_t *new_tokens, int32_t *path, int32_t *lengths,
+                               rarn_rows probs, const rarn_rows *draft_probs,
+                               const int64_t *tokens, const int32_t *parents,
+                               const int32_t *starts, const float *uniforms,
+                               const float *final_uniforms, int64_t B, int64_t rows,
+                               int64_t vocab, int64_t most, void *stream);
+
+/*
  * The tokens of an accepted path moved together: token context_lens[b] +
  * path[b, j] of sequence b goes to context_lens[b] + j, codes and scales of all
  * heads, j = 1 .. lengths[b] - 1; path (dense [B, path_width]) and lengths as

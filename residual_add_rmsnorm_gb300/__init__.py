@@ -27,6 +27,7 @@ the drafts' verification; the cache's tidying after it):
 
     pages = KVPages.empty(sequences, width, num_pages, page_size)
     starts, slots, positions, served = kv_step(pages, context_lens, new_lens, tokens)
+    new_tokens, path, lengths = verify_drafts(probs, tokens, starts, uniforms, final_uniforms, most)
     kv_cache_compact(cache, pages.page_table, context_lens, path, lengths)
     kv_trim(pages, kept_lens)
 
@@ -59,7 +60,7 @@ __all__ = ["rms_norm", "fused_add_rms_norm", "reduce_add_rms_norm", "rms_norm_ho
            "qk_norm_rope_kv_write", "kv_cache_read", "tree_attention",
            "tree_attention_workspace_bytes", "plan_tree_attention", "ROTATION_STYLES",
            "SECTION_ORDERS", "gated_add_rms_norm", "KVPages", "kv_step", "kv_trim",
-           "kv_cache_compact", "MAX_STEP_SEQUENCES"]
+           "kv_cache_compact", "MAX_STEP_SEQUENCES", "verify_drafts"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "librarn.so")
@@ -306,7 +307,10 @@ def library() -> ctypes.CDLL:
     lib.rarn_kv_step.argtypes = [kp, vp, vp, vp, vp, vp, vp, i64, vp]
     lib.rarn_kv_trim.argtypes = [kp, vp, vp]
     lib.rarn_kv_cache_compact.argtypes = [kc, vp, i64, i64, vp, vp, vp, i64, i64, vp]
-    for f in (lib.rarn_kv_step, lib.rarn_kv_trim, lib.rarn_kv_cache_compact):
+    lib.rarn_verify_drafts.argtypes = [vp, vp, vp, Rows, ctypes.POINTER(Rows), vp, vp, vp, vp, vp,
+                                       i64, i64, i64, i64, vp]
+    for f in (lib.rarn_kv_step, lib.rarn_kv_trim, lib.rarn_kv_cache_compact,
+              lib.rarn_verify_drafts):
         f.restype = c_int
     lib.rarn_tree_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
     lib.rarn_tree_attention_workspace_bytes.restype = i64
@@ -1295,6 +1299,58 @@ def kv_trim(pages: KVPages, lens) -> None:
     import torch
     _on(pages.device, "rarn_kv_trim", library().rarn_kv_trim, pages._ref,
         _indices("lens", lens, torch.int32, pages.sequences, pages.device))
+
+
+def verify_drafts(probs, tokens, starts, uniforms, final_uniforms, most: int, draft_probs=None,
+                  parents=None, new_tokens=None, path=None, lengths=None):
+    """Drafted tokens verified against the target's probabilities, and the token
+    behind the accepted ones drawn: what comes out is distributed as the target's
+    own tokens.
+
+    Sequence b's rows are starts[b] .. starts[b + 1] - 1 (int32, [B + 1]) of probs
+    [rows, vocab] (float32 / float16 / bfloat16, unit stride along a row): row 0 its
+    last known token, the others drafts; a row holds the target's distribution
+    behind its token.  tokens: [rows] int64; parents: [rows] int32, each draft's
+    parent row within its sequence (a tree), or None: the row before (a chain).
+    uniforms: [rows] float32 in [0, 1), the number that decides among a row's drafts;
+    final_uniforms: [B] float32, those of the drawn tokens.  draft_probs: like probs,
+    row r the distribution that draft r was drawn from (chains only); None: drafts
+    that were chosen without chance.  At most ``most`` drafts are accepted.
+
+    Returns (new_tokens [B, most + 1] int64, path [B, most + 1] int32, lengths [B]
+    int32): lengths[b] - 1 accepted drafts; path their rows behind row 0; new_tokens
+    their tokens and the drawn one; -1 behind those.  A row without a distribution
+    (a sum of 0, or of 2 and more) draws -1; that, and indices outside, set watchdog
+    bit 4."""
+    import torch
+    dev, dt = probs.device, probs.dtype
+    if probs.dim() != 2:
+        raise ValueError("probs must be [rows, vocab]")
+    N, V = probs.shape
+    rp = _matrix("probs", probs, N, V, dt, dev)
+    rq = None
+    if draft_probs is not None:
+        if parents is not None:
+            raise ValueError("draft_probs go with chains only: parents must be None")
+        rq = ctypes.byref(_matrix("draft_probs", draft_probs, N, V, dt, dev))
+    B, W = starts.numel() - 1, most + 1
+    i32, i64, f32 = torch.int32, torch.int64, torch.float32
+    if B < 0 or most < 0:
+        raise ValueError("starts must hold a value more than there are sequences, most be >= 0")
+    if new_tokens is None:
+        new_tokens = torch.empty(B, W, dtype=i64, device=dev)
+    if path is None:
+        path = torch.empty(B, W, dtype=i32, device=dev)
+    if lengths is None:
+        lengths = torch.empty(B, dtype=i32, device=dev)
+    _on(dev, "rarn_verify_drafts", library().rarn_verify_drafts,
+        _indices("new_tokens", new_tokens, i64, B * W, dev),
+        _indices("path", path, i32, B * W, dev),
+        _indices("lengths", lengths, i32, B, dev), rp, rq, _indices("tokens", tokens, i64, N, dev),
+        None if parents is None else _indices("parents", parents, i32, N, dev),
+        _indices("starts", starts, i32, B + 1, dev), _indices("uniforms", uniforms, f32, N, dev),
+        _indices("final_uniforms", final_uniforms, f32, B, dev), B, N, V, most)
+    return new_tokens, path, lengths
 
 
 def kv_cache_compact(cache: KVCache, page_table, context_lens, path, lengths) -> None:

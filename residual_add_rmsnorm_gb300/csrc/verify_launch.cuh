@@ -1,0 +1,18 @@
+// verify_launch.cuh -- host side of verify.cuh: how many CTAs take a sequence.
+#pragma once
+
+#include "verify.cuh"
+
+namespace rarn {
+namespace verify {
+
+template <typename T>
+cudaError_t launch_verify(const Params &p, int num_sms, bool pdl, cudaStream_t st) {
+    int cluster = kMaxCluster;
+    while (cluster > 1 && (int64_t)p.B * cluster > 2 * num_sms) cluster /= 2;
+    return launch_kernel(k_verify<T>, dim3((unsigned)(p.B * cluster)), dim3(kThreads), 0, st, pdl,
+                         cluster, p, cluster);
+}
+
+}  // namespace verify
+}  // namespace rarn

@@ -110,3 +110,56 @@ class Pages:
 
     def table(self):
         return [h + [-1] * (self.width - len(h)) for h in self.has]
+
+
+def verify(probs, tokens, starts, u, v, most, draft_probs=None, parents=None):
+    """(new_tokens, path, lengths) as lists, sequence by sequence in binary64: sums of
+    up to 10^5 terms are off by 2^-53 of the total a term, so that a draw differs from the
+    exact one where v lies that near to a border."""
+    W, V = most + 1, probs.shape[1]
+    new, paths, lengths = [], [], []
+    for b in range(len(starts) - 1):
+        lo, n = starts[b], starts[b + 1] - starts[b]
+        if n == 0:
+            new.append([-1] * W)
+            paths.append([-1] * W)
+            lengths.append(0)
+            continue
+        at, path = 0, [0]
+        while True:
+            p = probs[lo + at].to(F64)
+            left, low, took = p.clone(), 0.0, None
+            kids = [] if len(path) == W else \
+                [r for r in range(at + 1, n) if (parents[lo + r] if parents else r - 1) == at]
+            for r in kids:
+                x, number = tokens[lo + r], float(u[lo + at])
+                if not 0 <= x < V:
+                    if draft_probs is not None:
+                        left = (p - draft_probs[lo + r].to(F64)).clamp_min(0)
+                    continue
+                if draft_probs is not None:
+                    q = draft_probs[lo + r].to(F64)
+                    good = number * float(q[x]) < float(p[x])
+                    left = (p - q).clamp_min(0)
+                else:
+                    mass = float(left[x])
+                    good = low <= number < low + mass
+                    low += mass
+                    left[x] = 0
+                if good:
+                    took = r
+                    break
+            if took is None:
+                break
+            at = took
+            path.append(at)
+        if not kids or float(left.sum()) == 0:
+            left = p
+        total = left.cumsum(0)
+        drawn = -1 if float(total[-1]) == 0 else \
+            int(torch.searchsorted(total, total[-1] * float(v[b]), right=True))
+        pad = [-1] * (W - len(path))
+        new.append([tokens[lo + r] for r in path[1:]] + [drawn] + pad)
+        paths.append(path + pad)
+        lengths.append(len(path))
+    return new, paths, lengths
