@@ -10,6 +10,7 @@
 #pragma once
 
 #include "kv.cuh"
+#include "rows.cuh"
 
 namespace rarn {
 namespace block {
@@ -32,6 +33,200 @@ __device__ __forceinline__ int64_t gate_row(const Params &p, int64_t t) {
     if (!p.index) return p.gates == 1 ? 0 : t;
     const int64_t g = p.index[t];
     return g >= 0 && g < p.gates ? g : -1;
+}
+
+// Rows in registers, 16-byte packs: a warp per row, or a CTA.  Between the sums a
+// thread keeps its packs of x and r as they came and then of h as it is stored, so
+// that nothing is read twice; the gammas and shared gates come from L1.  kPipe: the next
+// row's loads are under way while a row is summed and written.
+template <typename T, typename TR, int VPT>
+struct RowPacks {
+    uint4 x[VPT], r[VPT][Res<T, TR>::N];
+};
+
+template <typename T, typename TR, int VPT>
+__device__ __forceinline__ void load_row(const Params &p, int64_t t, int j0, int js, int nv,
+                                         RowPacks<T, TR, VPT> &b) {
+    using RS = Res<T, TR>;
+    const T *x = static_cast<const T *>(p.x) + t * p.ldx;
+    const TR *r = static_cast<const TR *>(p.residual) + t * p.ldr;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int j = j0 + k * js;
+        if (j < nv) {
+            b.x[k] = ld_stream(x + j * RS::EPV);
+#pragma unroll
+            for (int q = 0; q < RS::N; ++q)
+                b.r[k][q] = ld_stream(r + j * RS::EPV + q * RS::EPW);
+        }
+    }
+}
+
+// Threads that a CTA of the kernel may have: with eight packs a thread 128 registers hold
+// x, r and h of one row, with four or fewer the next row's too.
+template <int VPT, bool kWarp>
+constexpr int kMaxThreads = kWarp ? 256 : VPT == 1 ? 1024 : 512;
+
+// Packs as pairs, for arithmetic two elements to an instruction.
+template <typename T>
+__device__ __forceinline__ void unpack2(const uint4 &p, float2 (&f)[DT<T>::EPV / 2]) {
+    if constexpr (sizeof(T) == 4) {
+        f[0] = float2{__uint_as_float(p.x), __uint_as_float(p.y)};
+        f[1] = float2{__uint_as_float(p.z), __uint_as_float(p.w)};
+    } else {
+        f[0] = DT<T>::w2f(p.x);
+        f[1] = DT<T>::w2f(p.y);
+        f[2] = DT<T>::w2f(p.z);
+        f[3] = DT<T>::w2f(p.w);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack2(const float2 (&f)[DT<T>::EPV / 2]) {
+    if constexpr (sizeof(T) == 4)
+        return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y),
+                          __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+    else
+        return make_uint4(DT<T>::f2w(f[0].x, f[0].y), DT<T>::f2w(f[1].x, f[1].y),
+                          DT<T>::f2w(f[2].x, f[2].y), DT<T>::f2w(f[3].x, f[3].y));
+}
+
+// The residual's words of one pack of T.
+template <typename T, typename TR>
+__device__ __forceinline__ void res_unpack2(const uint4 (&v)[Res<T, TR>::N],
+                                            float2 (&f)[DT<T>::EPV / 2]) {
+    if constexpr (Res<T, TR>::SAME) {
+        unpack2<T>(v[0], f);
+    } else {
+#pragma unroll
+        for (int q = 0; q < Res<T, TR>::N; ++q) {
+            f[2 * q] = float2{__uint_as_float(v[q].x), __uint_as_float(v[q].y)};
+            f[2 * q + 1] = float2{__uint_as_float(v[q].z), __uint_as_float(v[q].w)};
+        }
+    }
+}
+
+template <typename T, typename TR>
+__device__ __forceinline__ void res_pack2(const float2 (&f)[DT<T>::EPV / 2],
+                                          uint4 (&v)[Res<T, TR>::N]) {
+    if constexpr (Res<T, TR>::SAME) {
+        v[0] = pack2<T>(f);
+    } else {
+#pragma unroll
+        for (int q = 0; q < Res<T, TR>::N; ++q)
+            v[q] = make_uint4(__float_as_uint(f[2 * q].x), __float_as_uint(f[2 * q].y),
+                              __float_as_uint(f[2 * q + 1].x), __float_as_uint(f[2 * q + 1].y));
+    }
+}
+
+template <typename T, typename TR, int VPT, bool kGate, bool kWarp, bool kPipe>
+__global__ void __launch_bounds__(kMaxThreads<VPT, kWarp>) k_block_vec(const Params p) {
+    using RS = Res<T, TR>;
+    constexpr int E = RS::EPV;
+    __shared__ float red[kWarp ? 1 : 4][32];
+    const int nv = p.H / E;
+    const int j0 = kWarp ? threadIdx.x & 31 : threadIdx.x, js = kWarp ? 32 : blockDim.x;
+    const int per = kWarp ? blockDim.x >> 5 : 1;
+    const int64_t step = (int64_t)gridDim.x * per;
+    int64_t t = (int64_t)blockIdx.x * per + (kWarp ? threadIdx.x >> 5 : 0);
+    const float inv_h = 1.f / static_cast<float>(p.H);
+    const T *xg = static_cast<const T *>(p.x_gamma), *gm = static_cast<const T *>(p.gamma);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    // two sums a row, each in a buffer that the row before did not use
+    int par = 0;
+    auto row_sum = [&](float v, int which) {
+        if constexpr (kWarp) return warp_sum(v);
+        else return block_sum(v, red[2 * par + which]);
+    };
+    RowPacks<T, TR, VPT> next;
+    if (kPipe && t < p.T) load_row<T, TR, VPT>(p, t, j0, js, nv, next);
+    for (; t < p.T; t += step, par ^= 1) {
+        RowPacks<T, TR, VPT> cur;
+        if constexpr (kPipe) cur = next;
+        else load_row<T, TR, VPT>(p, t, j0, js, nv, cur);
+        uint4 gate[kGate ? VPT : 1];
+        bool live = true;
+        if constexpr (kGate) {
+            const int64_t g = gate_row(p, t);
+            live = g >= 0;  // else the row is only gone through
+            const T *row = static_cast<const T *>(p.gate) + (live ? g : 0) * p.ldg;
+            if (!live && j0 == 0) atomicOr(p.watchdog, kv::kWatchIndex);
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int j = j0 + k * js;
+                if (j < nv) gate[k] = ld_stream(row + j * E);
+            }
+        }
+        if constexpr (kPipe)
+            if (t + step < p.T) load_row<T, TR, VPT>(p, t + step, j0, js, nv, next);
+        float inv = 1.f;
+        if (xg) {
+            float2 ss = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                if (j0 + k * js < nv) {
+                    float2 x[E / 2];
+                    unpack2<T>(cur.x[k], x);
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) ss = __ffma2_rn(x[e], x[e], ss);
+                }
+            }
+            inv = rsqrtf(fmaf(row_sum(ss.x + ss.y, 0), inv_h, p.eps));
+        }
+        TR *h = static_cast<TR *>(p.h) + t * p.ldh;
+        const float2 by = {inv, inv}, scale = {p.scale, p.scale};
+        const float2 keep = {p.residual_scale, p.residual_scale};
+        float2 ss = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int j = j0 + k * js;
+            if (j < nv) {
+                float2 n[E / 2], w[E / 2], s[E / 2];
+                unpack2<T>(cur.x[k], n);
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) n[e] = __fmul2_rn(n[e], by);
+                if (xg) {
+                    unpack2<T>(ld_keep(xg + j * E), w);
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) n[e] = __fmul2_rn(n[e], w[e]);
+                }
+                if constexpr (kGate) {
+                    unpack2<T>(gate[k], w);
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) n[e] = __fmul2_rn(n[e], w[e]);
+                }
+                res_unpack2<T, TR>(cur.r[k], s);
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e)
+                    s[e] = __ffma2_rn(keep, s[e], __fmul2_rn(scale, n[e]));
+                res_pack2<T, TR>(s, cur.r[k]);
+                if (live) {
+#pragma unroll
+                    for (int q = 0; q < RS::N; ++q)
+                        st_global(h + j * E + q * RS::EPW, cur.r[k][q]);
+                }
+                res_unpack2<T, TR>(cur.r[k], s);
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) ss = __ffma2_rn(s[e], s[e], ss);
+            }
+        }
+        const float inv2 = rsqrtf(fmaf(row_sum(ss.x + ss.y, 1), inv_h, p.eps));
+        T *y = static_cast<T *>(p.y) + t * p.ldy;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int j = j0 + k * js;
+            if (j < nv) {
+                float2 s[E / 2], w[E / 2];
+                res_unpack2<T, TR>(cur.r[k], s);
+                unpack2<T>(ld_keep(gm + j * E), w);
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e)
+                    s[e] = __fmul2_rn(__fmul2_rn(s[e], float2{inv2, inv2}), w[e]);
+                if (live) st_global(y + j * E, pack2<T>(s));
+            }
+        }
+    }
 }
 
 // Any row length, stride and alignment: a CTA per row, element by element, x and
