@@ -57,25 +57,31 @@ struct Params {
 enum Weights : int { W_ALL = 0, W_REST = 1, W_WITHOUT = 2 };
 
 // 0 .. 1, NaN as 0.
-__device__ __forceinline__ float unit(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
+__device__ __forceinline__ float unit(float x) { return __saturatef(x); }
 
-// The two halves of F(x) added to hi (units of 2^-23) and lo (2^-46), 0 <= x <= 1: x + 1
-// has x's first half in its bits above those of 1; the rest, exact and at most 2^-24,
-// comes out of a sum with 1.5 * 2^-23 alike.
+// The two halves of F(x) as bits above those of two constants, two elements at a time,
+// 0 <= x <= 1: x + 1 has x's first half in its bits above those of 1; the rest,
+// exact and at most 2^-24, comes out of a sum with 1.5 * 2^-23 alike.
 constexpr uint32_t kOne = 0x3f800000u;      // bits of 1
 constexpr uint32_t kSmall = 0x34400000u;    // bits of 1.5 * 2^-23
 
-__device__ __forceinline__ void halves(float x, uint32_t &hi, uint32_t &lo) {
-    const float y = __fadd_rn(x, 1.f);
-    const float rest = __fsub_rn(x, __fsub_rn(y, 1.f));
-    hi = __float_as_uint(y);
-    lo = __float_as_uint(__fadd_rn(rest, __uint_as_float(kSmall)));
+__device__ __forceinline__ void halves(float2 x, float2 &hi, float2 &lo) {
+    const float s = __uint_as_float(kSmall);
+    hi = __fadd2_rn(x, float2{1.f, 1.f});
+    const float2 first = __fadd2_rn(hi, float2{-1.f, -1.f});
+    lo = __fadd2_rn(__fadd2_rn(x, float2{-first.x, -first.y}), float2{s, s});
 }
 
 __device__ __forceinline__ int64_t fixed(float x) {
-    uint32_t hi, lo;
-    halves(unit(x), hi, lo);
-    return ((int64_t)(int32_t)(hi - kOne) << 23) + (int32_t)(lo - kSmall);
+    float2 hi, lo;
+    halves(float2{unit(x), 0.f}, hi, lo);
+    return ((int64_t)(int32_t)(__float_as_uint(hi.x) - kOne) << 23) +
+           (int32_t)(__float_as_uint(lo.x) - kSmall);
+}
+
+// max(p - q, 0): F(p) - F(min(p, q)), F being monotone.
+__device__ __forceinline__ int64_t weight(float p, float q, bool rest) {
+    return rest ? fixed(p) - fixed(fminf(unit(p), unit(q))) : fixed(p);
 }
 
 // A lane's sum of up to 32 weights.
@@ -83,33 +89,28 @@ struct Lane {
     uint32_t hi = 0, lo = 0;
 
     template <bool kRest>
-    __device__ __forceinline__ void add(float p, float q) {
-        uint32_t h, l;
-        p = unit(p);
+    __device__ __forceinline__ void add(float2 p, float2 q) {
+        float2 h, l;
+        p = float2{unit(p.x), unit(p.y)};
+        halves(p, h, l);
         if constexpr (kRest) {
-            q = unit(q);
-            const bool left = p > q;
-            uint32_t h2, l2;
-            halves(left ? p : 0.f, h, l);
-            halves(left ? q : 0.f, h2, l2);
-            hi += h - h2;
-            lo += l - l2;
+            float2 h2, l2;
+            halves(float2{fminf(p.x, unit(q.x)), fminf(p.y, unit(q.y))}, h2, l2);
+            hi += __float_as_uint(h.x) - __float_as_uint(h2.x);
+            hi += __float_as_uint(h.y) - __float_as_uint(h2.y);
+            lo += __float_as_uint(l.x) - __float_as_uint(l2.x);
+            lo += __float_as_uint(l.y) - __float_as_uint(l2.y);
         } else {
-            halves(p, h, l);
-            hi += h - kOne;
-            lo += l - kSmall;
+            hi += __float_as_uint(h.x) - kOne;
+            hi += __float_as_uint(h.y) - kOne;
+            lo += __float_as_uint(l.x) - kSmall;
+            lo += __float_as_uint(l.y) - kSmall;
         }
     }
     __device__ __forceinline__ int64_t sum() const {
         return ((int64_t)(int32_t)hi << 23) + (int32_t)lo;
     }
 };
-
-__device__ __forceinline__ int64_t weight(float p, float q, bool rest) {
-    if (!rest) return fixed(p);
-    const int64_t d = fixed(p) - fixed(q);
-    return unit(p) > unit(q) ? d : 0;
-}
 
 __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
 #pragma unroll
@@ -139,35 +140,52 @@ __device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t *red, int64_t
     return before + in - v;
 }
 
-// The sum of a group's weights, in every lane.
+// The sum of a group's weights, in every lane.  Loads come in batches of 32 registers
+// (64 bytes of p and of q a lane), which four CTAs to an SM have room for.
 template <typename T, bool kRest>
 __device__ __forceinline__ int64_t group_sum64(const T *p, const T *q, int g, int V, bool vec) {
     constexpr int E = DT<T>::EPV;
     const int lane = threadIdx.x & 31, at = g * kGroup;
     Lane s;
     if (vec && at + kGroup <= V) {
-        constexpr int N = kGroup / (32 * E);
-        uint4 a[N], b[N];
+        constexpr int N = 4;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            a[i] = ld_stream(p + at + (i * 32 + lane) * E);
-            if constexpr (kRest) b[i] = ld_stream(q + at + (i * 32 + lane) * E);
-        }
+        for (int i0 = 0; i0 < kGroup / (32 * E); i0 += N) {
+            uint4 a[N], b[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float x[E], y[E];
-            DT<T>::unpack(a[i], x);
-            if constexpr (kRest) DT<T>::unpack(b[i], y);
+            for (int i = 0; i < N; ++i) {
+                a[i] = ld_stream(p + at + ((i0 + i) * 32 + lane) * E);
+                if constexpr (kRest) b[i] = ld_stream(q + at + ((i0 + i) * 32 + lane) * E);
+            }
 #pragma unroll
-            for (int e = 0; e < E; ++e) s.add<kRest>(x[e], kRest ? y[e] : 0.f);
+            for (int i = 0; i < N; ++i) {
+                float x[E], y[E];
+                DT<T>::unpack(a[i], x);
+                if constexpr (kRest) DT<T>::unpack(b[i], y);
+#pragma unroll
+                for (int e = 0; e < E; e += 2)
+                    s.add<kRest>(float2{x[e], x[e + 1]},
+                                 kRest ? float2{y[e], y[e + 1]} : float2{0.f, 0.f});
+            }
         }
     } else {
-#pragma unroll 8
-        for (int i = lane; i < kGroup; i += 32) {
-            const bool in = at + i < V;
-            const float x = in ? DT<T>::to_f(p[at + i]) : 0.f;
-            const float y = in && kRest ? DT<T>::to_f(q[at + i]) : 0.f;
-            s.add<kRest>(x, y);
+        constexpr int N = 16;
+#pragma unroll 1
+        for (int i0 = at + lane; i0 < min(at + kGroup, V); i0 += N * 32) {
+            T a[N], b[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int x = i0 + i * 32;
+                a[i] = b[i] = DT<T>::from_f(0.f);
+                if (x < V) {
+                    a[i] = p[x];
+                    if constexpr (kRest) b[i] = q[x];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < N; i += 2)
+                s.add<kRest>(float2{DT<T>::to_f(a[i]), DT<T>::to_f(a[i + 1])},
+                             float2{DT<T>::to_f(b[i]), DT<T>::to_f(b[i + 1])});
         }
     }
     return warp_sum64(s.sum());
@@ -192,13 +210,14 @@ __device__ __forceinline__ void store_peer(int64_t *place, int rank, int64_t v) 
 // A cluster of CTAs per sequence; every CTA finds the accepted rows by itself, then
 // sums its part of the last one's weights.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_verify(const Params p, int cluster) {
+__global__ void __launch_bounds__(kThreads, 4) k_verify(const Params p, int cluster) {
     __shared__ int64_t s_group[kMaxGroups];      // weights of this CTA's groups
     __shared__ int64_t s_mass[kMaxTree];         // F(p) of each draft; 0: its token came before
     __shared__ int s_parent[kMaxTree], s_next[kMaxTree];
     __shared__ int s_token[kMaxTree], s_walk[kMaxTree];
     __shared__ int64_t red[kWarps], s_part[2][kMaxCluster];
-    __shared__ int s_stop, s_length, s_deep, s_found;
+    __shared__ int64_t s_u[kMaxTree];
+    __shared__ int s_stop, s_length, s_deep, s_found, s_gone;
     grid_dependency_wait();
     grid_launch_dependents();
     cluster_arrive();  // waited for before a peer's shared memory is written
@@ -243,6 +262,7 @@ __global__ void __launch_bounds__(kThreads) k_verify(const Params p, int cluster
         for (int r = 1 + tid; r < most; r += kThreads) {
             const int x = token_of(r);
             bool ok = false;
+            if (r < kMaxTree) s_token[r] = x;
             if (x >= 0) {
                 const float u = p.u[lo + r - 1], px = DT<T>::to_f(probs[(r - 1) * p.ldp + x]);
                 if (drafts)  // exact in binary64
@@ -275,6 +295,7 @@ __global__ void __launch_bounds__(kThreads) k_verify(const Params p, int cluster
             s_token[r] = x;
             s_mass[r] = mass;
             s_next[r] = -1;
+            s_u[r] = fixed(p.u[lo + r]);
         }
         __syncthreads();
         for (int r = 1 + tid; r < n; r += kThreads) {
@@ -291,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) k_verify(const Params p, int cluster
             int64_t low = 0;
             for (int s = up + 1; s < r; ++s)
                 if (s_parent[s] == up) low += s_mass[s];
-            const int64_t u = fixed(p.u[lo + up]);
+            const int64_t u = s_u[up];
             if (low <= u && u < low + s_mass[r]) s_next[up] = r;  // one child at most
         }
         __syncthreads();
@@ -311,8 +332,12 @@ __global__ void __launch_bounds__(kThreads) k_verify(const Params p, int cluster
         if (bad) atomicOr(p.watchdog, kv::kWatchIndex);
         for (int j = tid; j < W; j += kThreads) {
             path[j] = j < length ? (tree ? s_walk[j] : j) : -1;
-            if (j != length - 1)
-                tokens[j] = j < length ? p.tokens[lo + (tree ? s_walk[j + 1] : j + 1)] : -1;
+            if (j < length - 1) {
+                const int r = tree ? s_walk[j + 1] : j + 1;
+                tokens[j] = r < kMaxTree ? s_token[r] : p.tokens[lo + r];
+            } else if (j >= length) {
+                tokens[j] = -1;
+            }
         }
         if (tid == 0) p.lengths[b] = length;
     }
@@ -321,13 +346,21 @@ __global__ void __launch_bounds__(kThreads) k_verify(const Params p, int cluster
     const T *pr = probs + last * p.ldp;
     const T *qr = drafts && refused ? drafts + (last + 1) * p.ldq : nullptr;
     int mode = !refused ? W_ALL : drafts ? W_REST : W_WITHOUT;
-    // without q a chain's refused draft is its only child
-    auto gone = [&](int x) {
-        if (!tree) return x == token_of(last + 1);
-        for (int s = last + 1; s < n; ++s)
-            if (s_parent[s] == last && s_token[s] == x) return true;
-        return false;
-    };
+    const float v = fminf(unit(p.v[b]), 0.99999994f);
+    // the refused children's tokens, in s_next
+    if (tid == 0) s_gone = 0;
+    __syncthreads();
+    if (mode == W_WITHOUT) {
+        auto refuse = [&](int x) { s_next[atomicAdd(&s_gone, 1)] = x; };
+        if (tree) {
+            for (int s = last + 1 + tid; s < n; s += kThreads)
+                if (s_parent[s] == last && s_mass[s] > 0) refuse(s_token[s]);
+        } else if (tid == 0) {  // a chain's only child
+            const int x = last + 1 < kMaxTree ? s_token[last + 1] : token_of(last + 1);
+            if (x >= 0) refuse(x);
+        }
+    }
+    __syncthreads();
     const int groups = (p.V + kGroup - 1) / kGroup;
     const int g0 = (int)((int64_t)groups * rank / cluster);
     const int g1 = (int)((int64_t)groups * (rank + 1) / cluster);
@@ -340,19 +373,12 @@ __global__ void __launch_bounds__(kThreads) k_verify(const Params p, int cluster
             if ((tid & 31) == 0) s_group[g - g0] = s;
         }
         __syncthreads();
-        if (mode == W_WITHOUT) {
-            auto take = [&](int x, int64_t mass) {
-                const int g = x / kGroup;
+        if (mode == W_WITHOUT) {  // each of them once
+            for (int i = tid; i < s_gone; i += kThreads) {
+                const int x = s_next[i], g = x / kGroup;
                 if (g >= g0 && g < g1)
                     atomicAdd(reinterpret_cast<unsigned long long *>(&s_group[g - g0]),
-                              (unsigned long long)-mass);
-            };
-            if (tree) {
-                for (int s = last + 1 + tid; s < n; s += kThreads)
-                    if (s_parent[s] == last) take(s_token[s], s_mass[s]);
-            } else if (tid == 0) {
-                const int x = token_of(last + 1);
-                if (x >= 0) take(x, fixed(DT<T>::to_f(pr[x])));
+                              (unsigned long long)-fixed(DT<T>::to_f(pr[x])));
             }
             __syncthreads();
         }
@@ -384,7 +410,6 @@ __global__ void __launch_bounds__(kThreads) k_verify(const Params p, int cluster
             }
             return;
         }
-        const float v = fminf(unit(p.v[b]), 0.99999994f);
         const int64_t target = (int64_t)((double)v * (double)all) - ahead;  // rounded down
         if (target < 0 || target >= total) return;  // another CTA's
         if (target >= before && target < before + mine) {
@@ -417,10 +442,18 @@ __global__ void __launch_bounds__(kThreads) k_verify(const Params p, int cluster
             if (x < p.V) {
                 w[i] = weight(DT<T>::to_f(pr[x]), mode == W_REST ? DT<T>::to_f(qr[x]) : 0.f,
                               mode == W_REST);
-                if (mode == W_WITHOUT && w[i] > 0 && gone(x)) w[i] = 0;
             }
-            own += w[i];
         }
+        if (mode == W_WITHOUT) {
+            for (int k = 0; k < s_gone; ++k) {
+                const int i = s_next[k] - x0;
+#pragma unroll
+                for (int m = 0; m < kMine; ++m)
+                    if (i == m) w[m] = 0;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) own += w[i];
         int64_t sum = block_scan64(own, red, &ignored);
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
