@@ -810,15 +810,16 @@ def _on(device, what, fn, *args):
     """fn(*args, stream) on ``device`` and its current stream; raises on a
     status other than OK."""
     global _get_device, _raw_stream
-    import torch
     if _get_device is None:
-        _get_device = torch.cuda.current_device
+        import torch
+        _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda i: torch.cuda.current_stream(i).cuda_stream)
     i = device.index
     if _get_device() == i:
         status = fn(*args, _raw_stream(i))
     else:
+        import torch
         with torch.cuda.device(i):
             status = fn(*args, _raw_stream(i))
     if status:
@@ -835,7 +836,7 @@ def _heads(name, t, T, heads, D, dtype, device):
                          f"{list(shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.device != device or not t.is_cuda:
+    if t.get_device() != device.index:  # -1 and None for the CPU
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
     if stride[2] != 1 and D > 1:
         raise ValueError(f"{name} must have unit stride inside a head")
@@ -847,7 +848,7 @@ def _heads(name, t, T, heads, D, dtype, device):
 
 def _indices(name, t, dtype, n, device):
     """A contiguous CUDA index tensor of n values."""
-    if t.dtype is not dtype or t.device != device or not t.is_cuda:
+    if t.dtype is not dtype or t.get_device() != device.index:
         raise TypeError(f"{name} must be a {dtype} CUDA tensor on {device}")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {n} values")
@@ -857,7 +858,7 @@ def _indices(name, t, dtype, n, device):
 def _gamma(name, g, D, dtype, device):
     if g is None:
         return None
-    if g.dtype is not dtype or g.device != device or not g.is_contiguous():
+    if g.dtype is not dtype or g.get_device() != device.index or not g.is_contiguous():
         _check_tensor(name, g, dtype, device)
     if g.numel() != D:
         raise ValueError(f"{name} has {g.numel()} elements, expected {D}")
@@ -871,7 +872,7 @@ def _matrix(name, t, T, H, dtype, device):
         raise ValueError(f"{name} must be [{T}, {H}], got {list(shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.device != device or not t.is_cuda:
+    if t.get_device() != device.index:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
     if stride[1] != 1 and H > 1:
         raise ValueError(f"{name} must have unit stride within a row")
@@ -941,7 +942,7 @@ def _rotation(cos_sin, positions, style, T, device):
         raise ValueError(f"style must be one of {sorted(ROTATION_STYLES)}")
     if cos_sin is None:
         return None
-    if cos_sin.dtype is not torch.float32 or cos_sin.device != device or \
+    if cos_sin.dtype is not torch.float32 or cos_sin.get_device() != device.index or \
             not cos_sin.is_contiguous():
         _check_tensor("cos_sin", cos_sin, torch.float32, device)
     shape = cos_sin.shape
@@ -987,7 +988,7 @@ def _rotation_axes(cos_sin, positions, style, sections, order, T, device):
         raise ValueError("sections need cos_sin and positions")
     sections = sections if type(sections) is tuple else tuple(sections)
     A = len(sections)
-    if positions.dtype is not torch.int64 or positions.device != device or not positions.is_cuda:
+    if positions.dtype is not torch.int64 or positions.get_device() != device.index:
         raise TypeError(f"positions must be an int64 CUDA tensor on {device}")
     shape, stride = positions.shape, positions.stride()
     if len(shape) != 2 or shape[0] != A or shape[1] != T or (T > 1 and stride[1] != 1):
@@ -1146,7 +1147,7 @@ def qk_norm_rope_kv_write(q, k, v, q_gamma, k_gamma, eps: float, cos_sin, positi
 def _page_table(t, device):
     """Address, row stride, sequences and width of a page table."""
     import torch
-    if t.dtype is not torch.int32 or t.device != device or not t.is_cuda:
+    if t.dtype is not torch.int32 or t.get_device() != device.index:
         raise TypeError(f"page_table must be an int32 CUDA tensor on {device}")
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):

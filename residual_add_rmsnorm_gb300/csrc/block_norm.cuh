@@ -229,53 +229,88 @@ __global__ void __launch_bounds__(kMaxThreads<VPT, kWarp>) k_block_vec(const Par
     }
 }
 
-// Any row length, stride and alignment: a CTA per row, element by element, x and
-// the new residual read again for the passes behind the sums (each thread what it
-// read or wrote itself).
-template <typename T, typename TR>
+// Any row length, stride and alignment: a CTA per row, element by element.  With NE > 0
+// a thread holds its NE elements from the first load on; NE == 0, rows longer than
+// that: x and the new residual are read again for the passes behind the sums (each
+// thread what it read or wrote itself).
+template <typename T, typename TR, int NE>
 __global__ void __launch_bounds__(1024) k_block_any(const Params p) {
-    __shared__ float red[2][32];
+    __shared__ float red[2][2][32];
+    constexpr int N = NE > 0 ? NE : 1;
     grid_dependency_wait();
     grid_launch_dependents();
     const float inv_h = 1.f / static_cast<float>(p.H);
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+    const int js = blockDim.x;
+    int par = 0;
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, par ^= 1) {
         const T *x = static_cast<const T *>(p.x) + t * p.ldx;
         const TR *r = static_cast<const TR *>(p.residual) + t * p.ldr;
         TR *h = static_cast<TR *>(p.h) + t * p.ldh;
         T *y = static_cast<T *>(p.y) + t * p.ldy;
         const T *gate = nullptr;
+        bool live = true;
         if (p.gate) {
             const int64_t g = gate_row(p, t);
-            if (g < 0) {  // the whole CTA
-                if (threadIdx.x == 0) atomicOr(p.watchdog, kv::kWatchIndex);
-                continue;
+            live = g >= 0;
+            gate = static_cast<const T *>(p.gate) + (live ? g : 0) * p.ldg;
+            if (!live && threadIdx.x == 0) atomicOr(p.watchdog, kv::kWatchIndex);
+        }
+        float n[N], s[N];
+        if constexpr (NE > 0) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int i = threadIdx.x + k * js;
+                n[k] = i < p.H ? DT<T>::to_f(x[i]) : 0.f;
+                s[k] = i < p.H ? DT<TR>::to_f(r[i]) : 0.f;
             }
-            gate = static_cast<const T *>(p.gate) + g * p.ldg;
         }
         float inv = 1.f;
         if (p.x_gamma) {
             float ss = 0.f;
-            for (int i = threadIdx.x; i < p.H; i += blockDim.x) {
-                const float v = DT<T>::to_f(x[i]);
-                ss = fmaf(v, v, ss);
+            if constexpr (NE > 0) {
+#pragma unroll
+                for (int k = 0; k < N; ++k) ss = fmaf(n[k], n[k], ss);
+            } else {
+                for (int i = threadIdx.x; i < p.H; i += js) {
+                    const float v = DT<T>::to_f(x[i]);
+                    ss = fmaf(v, v, ss);
+                }
             }
-            inv = rsqrtf(fmaf(block_sum(ss, red[0]), inv_h, p.eps));
+            inv = rsqrtf(fmaf(block_sum(ss, red[par][0]), inv_h, p.eps));
         }
         float ss = 0.f;
-        for (int i = threadIdx.x; i < p.H; i += blockDim.x) {
-            float n = DT<T>::to_f(x[i]);
-            if (p.x_gamma) n = n * inv * ld_elem<T>(p.x_gamma, i);
-            if (gate) n *= DT<T>::to_f(gate[i]);
-            const TR s =
-                DT<TR>::from_f(fmaf(p.residual_scale, DT<TR>::to_f(r[i]), p.scale * n));
-            h[i] = s;
-            const float v = DT<TR>::to_f(s);
-            ss = fmaf(v, v, ss);
+        // element i of the stream, from x and r
+        auto stream = [&](int i, float v, float was) {
+            if (p.x_gamma) v = v * inv * ld_elem<T>(p.x_gamma, i);
+            if (gate) v *= DT<T>::to_f(gate[i]);
+            const TR now = DT<TR>::from_f(fmaf(p.residual_scale, was, p.scale * v));
+            if (live) h[i] = now;
+            const float f = DT<TR>::to_f(now);
+            ss = fmaf(f, f, ss);
+            return f;
+        };
+        if constexpr (NE > 0) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int i = threadIdx.x + k * js;
+                if (i < p.H) s[k] = stream(i, n[k], s[k]);
+            }
+        } else {
+            for (int i = threadIdx.x; i < p.H; i += js)
+                stream(i, DT<T>::to_f(x[i]), DT<TR>::to_f(r[i]));
         }
-        const float inv2 = rsqrtf(fmaf(block_sum(ss, red[1]), inv_h, p.eps));
-        for (int i = threadIdx.x; i < p.H; i += blockDim.x)
-            y[i] = DT<T>::from_f(DT<TR>::to_f(h[i]) * inv2 * ld_elem<T>(p.gamma, i));
-        __syncthreads();  // red is written again for the next row
+        const float inv2 = rsqrtf(fmaf(block_sum(ss, red[par][1]), inv_h, p.eps));
+        if (!live) continue;  // the whole CTA
+        if constexpr (NE > 0) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int i = threadIdx.x + k * js;
+                if (i < p.H) y[i] = DT<T>::from_f(s[k] * inv2 * ld_elem<T>(p.gamma, i));
+            }
+        } else {
+            for (int i = threadIdx.x; i < p.H; i += js)
+                y[i] = DT<T>::from_f(DT<TR>::to_f(h[i]) * inv2 * ld_elem<T>(p.gamma, i));
+        }
     }
 }
 
