@@ -229,18 +229,30 @@ __global__ void __launch_bounds__(kMaxThreads<VPT, kWarp>) k_block_vec(const Par
     }
 }
 
+// An element of a gamma or gate, which no output overlaps: a load that stores do not
+// hold back.
+template <typename T>
+__device__ __forceinline__ float ld_const(const void *base, int i) {
+    if constexpr (sizeof(T) == 4) {
+        return __ldg(static_cast<const float *>(base) + i);
+    } else {
+        const unsigned short w = __ldg(static_cast<const unsigned short *>(base) + i);
+        return DT<T>::to_f(*reinterpret_cast<const T *>(&w));
+    }
+}
+
 // Any row length, stride and alignment: a CTA per row, element by element.  With NE > 0
 // a thread holds its NE elements from the first load on; NE == 0, rows longer than
 // that: x and the new residual are read again for the passes behind the sums (each
 // thread what it read or wrote itself).
 template <typename T, typename TR, int NE>
-__global__ void __launch_bounds__(1024) k_block_any(const Params p) {
+__global__ void __launch_bounds__(NE > 0 ? 512 : 1024, NE > 0 ? 2 : 1)
+    k_block_any(const Params p) {
     __shared__ float red[2][2][32];
-    constexpr int N = NE > 0 ? NE : 1;
     grid_dependency_wait();
     grid_launch_dependents();
     const float inv_h = 1.f / static_cast<float>(p.H);
-    const int js = blockDim.x;
+    const int js = blockDim.x, j0 = threadIdx.x;
     int par = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, par ^= 1) {
         const T *x = static_cast<const T *>(p.x) + t * p.ldx;
@@ -253,63 +265,77 @@ __global__ void __launch_bounds__(1024) k_block_any(const Params p) {
             const int64_t g = gate_row(p, t);
             live = g >= 0;
             gate = static_cast<const T *>(p.gate) + (live ? g : 0) * p.ldg;
-            if (!live && threadIdx.x == 0) atomicOr(p.watchdog, kv::kWatchIndex);
+            if (!live && j0 == 0) atomicOr(p.watchdog, kv::kWatchIndex);
         }
-        float n[N], s[N];
+        float ss = 0.f, inv = 1.f;
         if constexpr (NE > 0) {
+            // this thread's elements j0 + k * js; beyond the row its first one is read in
+            // their place (of a thread that has none the row's first gamma) and weighs nothing
+            int at[NE];
+            float n[NE], s[NE], w[NE];
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const int i = threadIdx.x + k * js;
-                n[k] = i < p.H ? DT<T>::to_f(x[i]) : 0.f;
-                s[k] = i < p.H ? DT<TR>::to_f(r[i]) : 0.f;
+            for (int k = 0; k < NE; ++k)
+                at[k] = j0 + k * js < p.H ? j0 + k * js : j0 < p.H ? j0 : 0;
+#pragma unroll
+            for (int k = 0; k < NE; ++k) n[k] = s[k] = 0.f;
+            if (j0 < p.H) {
+#pragma unroll
+                for (int k = 0; k < NE; ++k) n[k] = DT<T>::to_f(x[at[k]]);
+#pragma unroll
+                for (int k = 0; k < NE; ++k) s[k] = DT<TR>::to_f(r[at[k]]);
             }
-        }
-        float inv = 1.f;
-        if (p.x_gamma) {
-            float ss = 0.f;
-            if constexpr (NE > 0) {
+            if (p.x_gamma) {
 #pragma unroll
-                for (int k = 0; k < N; ++k) ss = fmaf(n[k], n[k], ss);
-            } else {
-                for (int i = threadIdx.x; i < p.H; i += js) {
+                for (int k = 0; k < NE; ++k) w[k] = ld_const<T>(p.x_gamma, at[k]);
+#pragma unroll
+                for (int k = 0; k < NE; ++k) ss += j0 + k * js < p.H ? n[k] * n[k] : 0.f;
+                inv = rsqrtf(fmaf(block_sum(ss, red[par][0]), inv_h, p.eps));
+#pragma unroll
+                for (int k = 0; k < NE; ++k) n[k] = n[k] * inv * w[k];
+            }
+            if (gate) {
+#pragma unroll
+                for (int k = 0; k < NE; ++k) w[k] = ld_const<T>(gate, at[k]);
+#pragma unroll
+                for (int k = 0; k < NE; ++k) n[k] *= w[k];
+            }
+#pragma unroll
+            for (int k = 0; k < NE; ++k) w[k] = ld_const<T>(p.gamma, at[k]);
+            ss = 0.f;
+#pragma unroll
+            for (int k = 0; k < NE; ++k) {
+                s[k] = DT<TR>::round(fmaf(p.residual_scale, s[k], p.scale * n[k]));
+                ss += j0 + k * js < p.H ? s[k] * s[k] : 0.f;
+            }
+            const int end = live ? p.H : 0;
+#pragma unroll
+            for (int k = 0; k < NE; ++k)
+                if (j0 + k * js < end) h[at[k]] = DT<TR>::from_f(s[k]);
+            const float inv2 = rsqrtf(fmaf(block_sum(ss, red[par][1]), inv_h, p.eps));
+#pragma unroll
+            for (int k = 0; k < NE; ++k)
+                if (j0 + k * js < end) y[at[k]] = DT<T>::from_f(s[k] * inv2 * w[k]);
+        } else {
+            if (p.x_gamma) {
+                for (int i = j0; i < p.H; i += js) {
                     const float v = DT<T>::to_f(x[i]);
                     ss = fmaf(v, v, ss);
                 }
+                inv = rsqrtf(fmaf(block_sum(ss, red[par][0]), inv_h, p.eps));
             }
-            inv = rsqrtf(fmaf(block_sum(ss, red[par][0]), inv_h, p.eps));
-        }
-        float ss = 0.f;
-        // element i of the stream, from x and r
-        auto stream = [&](int i, float v, float was) {
-            if (p.x_gamma) v = v * inv * ld_elem<T>(p.x_gamma, i);
-            if (gate) v *= DT<T>::to_f(gate[i]);
-            const TR now = DT<TR>::from_f(fmaf(p.residual_scale, was, p.scale * v));
-            if (live) h[i] = now;
-            const float f = DT<TR>::to_f(now);
-            ss = fmaf(f, f, ss);
-            return f;
-        };
-        if constexpr (NE > 0) {
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const int i = threadIdx.x + k * js;
-                if (i < p.H) s[k] = stream(i, n[k], s[k]);
+            ss = 0.f;
+            for (int i = j0; i < p.H; i += js) {
+                float v = DT<T>::to_f(x[i]);
+                if (p.x_gamma) v = v * inv * ld_const<T>(p.x_gamma, i);
+                if (gate) v *= ld_const<T>(gate, i);
+                v = DT<TR>::round(fmaf(p.residual_scale, DT<TR>::to_f(r[i]), p.scale * v));
+                if (live) h[i] = DT<TR>::from_f(v);
+                ss = fmaf(v, v, ss);
             }
-        } else {
-            for (int i = threadIdx.x; i < p.H; i += js)
-                stream(i, DT<T>::to_f(x[i]), DT<TR>::to_f(r[i]));
-        }
-        const float inv2 = rsqrtf(fmaf(block_sum(ss, red[par][1]), inv_h, p.eps));
-        if (!live) continue;  // the whole CTA
-        if constexpr (NE > 0) {
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const int i = threadIdx.x + k * js;
-                if (i < p.H) y[i] = DT<T>::from_f(s[k] * inv2 * ld_elem<T>(p.gamma, i));
-            }
-        } else {
-            for (int i = threadIdx.x; i < p.H; i += js)
-                y[i] = DT<T>::from_f(DT<TR>::to_f(h[i]) * inv2 * ld_elem<T>(p.gamma, i));
+            const float inv2 = rsqrtf(fmaf(block_sum(ss, red[par][1]), inv_h, p.eps));
+            if (!live) continue;  // the whole CTA
+            for (int i = j0; i < p.H; i += js)
+                y[i] = DT<T>::from_f(DT<TR>::to_f(h[i]) * inv2 * ld_const<T>(p.gamma, i));
         }
     }
 }

@@ -50,17 +50,17 @@ cudaError_t launch_block(const Params &p, bool vec, int num_sms, bool pdl, cudaS
         if (n <= 2048) return launch_cta<T, TR, 4>(p, num_sms, pdl, st);
         return launch_vec<T, TR, 8, false, false>(p, num_sms, (n + 255) / 256 * 32, pdl, st);
     }
-    // single elements: 4 or 16 to a thread while a row fits
-    auto any = [&](auto kernel, int each) {
-        const int threads = std::min(1024, ((p.H + each - 1) / each + 31) / 32 * 32);
+    // single elements: 8 or 16 to a thread while a row fits 512 threads
+    auto any = [&](auto kernel, int each, int most) {
+        const int threads = std::min(most, ((p.H + each - 1) / each + 31) / 32 * 32);
         const int64_t slots = (int64_t)num_sms * (2048 / threads);
         const int64_t rounds = (p.T + slots - 1) / slots;
         return launch_kernel(kernel, dim3((unsigned)((p.T + rounds - 1) / rounds)), dim3(threads),
                              0, st, pdl, 1, p);
     };
-    if (p.H <= 4 * 1024) return any(k_block_any<T, TR, 4>, 4);
-    if (p.H <= 16 * 1024) return any(k_block_any<T, TR, 16>, 16);
-    return any(k_block_any<T, TR, 0>, 1);
+    if (p.H <= 8 * 512) return any(k_block_any<T, TR, 8>, 8, 512);
+    if (p.H <= 16 * 512) return any(k_block_any<T, TR, 16>, 16, 512);
+    return any(k_block_any<T, TR, 0>, 1, 1024);
 }
 
 }  // namespace block
