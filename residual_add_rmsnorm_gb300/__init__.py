@@ -1246,7 +1246,10 @@ class KVPages:
         self.free_pages, self.free_count = free_pages, free_count
         self.device, self.page_size = dev, page_size
         self.sequences, self.num_pages = B, free_pages.numel()
+        # the calls' own word; its zero has to be there for a call on any stream
         self._ticket = torch.zeros(1, dtype=torch.int32, device=dev)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(dev).synchronize()
         i32 = torch.int32
         self._desc = KvPagesDesc(table, stride, width, _indices("held", held, i32, B, dev),
                                  _indices("free_pages", free_pages, i32, self.num_pages, dev),

@@ -1602,6 +1602,6 @@ rarn_status rarn_launch_floor(const void *rows, int64_t row_bytes, int32_t grid,
     return RARN_OK;
 }
 
-int rarn_version(void) { return (1 << 16) | 2; }
+int rarn_version(void) { return (1 << 16) | 3; }
 
 }  // extern "C"

@@ -160,6 +160,14 @@ __global__ void __launch_bounds__(kMaxThreads<VPT, kWarp>) k_block_vec(const Par
         }
         if constexpr (kPipe)
             if (t + step < p.T) load_row<T, TR, VPT>(p, t + step, j0, js, nv, next);
+        if constexpr (!kPipe && !kWarp) {  // the next row into L2 (2000 rows of 16384: 133 -> 126 us)
+            if (threadIdx.x == 0 && t + step < p.T) {
+                prefetch_l2(static_cast<const T *>(p.x) + (t + step) * p.ldx,
+                            (uint32_t)(p.H * sizeof(T)));
+                prefetch_l2(static_cast<const TR *>(p.residual) + (t + step) * p.ldr,
+                            (uint32_t)(p.H * sizeof(TR)));
+            }
+        }
         float inv = 1.f;
         if (xg) {
             float2 ss = {0.f, 0.f};

@@ -249,9 +249,10 @@ __global__ void __launch_bounds__(kThreads) k_trim(const TrimParams p) {
     __syncthreads();
     const int gone = (int)total.a;
     bool missing = false;
-    for (int x = blockIdx.x * kThreads + threadIdx.x; x < gone; x += gridDim.x * kThreads) {
-        const int b = find(pre, B, x);
-        const int entry = kept(b, p.pool.held[b]) + (x - pre[b]);
+    for (int64_t x = (int64_t)blockIdx.x * kThreads + threadIdx.x; x < gone;
+         x += (int64_t)gridDim.x * kThreads) {
+        const int b = find(pre, B, (int)x);
+        const int entry = kept(b, p.pool.held[b]) + ((int)x - pre[b]);
         int32_t *e = p.pool.table + b * p.pool.table_stride + entry;
         const int page = *e;
         missing |= page < 0 || page >= p.pool.num;

@@ -175,3 +175,37 @@ def test_the_same_bits_every_time_on_streams_and_in_graphs(T, H):
     torch.cuda.synchronize()
     rarn.gated_add_rms_norm(y, h, xg, gm, EPS, out=y)
     assert torch.equal(h, h2) and torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("H", [4096, 999])
+def test_rows_far_apart(H):
+    """Rows whose offsets pass 2^31 elements."""
+    T, ld, dt = 3, (1 << 30) + 8, torch.bfloat16
+    x, r, xg, gm, gate = inputs(T, H, dt, False, T, H)
+    far = []
+    for v in (x, r, gate, torch.zeros_like(x)):
+        d = torch.empty((T - 1) * ld + H, dtype=dt, device="cuda").as_strided((T, H), (ld, 1))
+        d.copy_(v)
+        far.append(d)
+    rarn.gated_add_rms_norm(far[0], far[1], xg.cuda(), gm.cuda(), EPS, gate=far[2], out=far[3])
+    R.check_block(far[3].cpu(), far[1].cpu(), x, r, xg, gm, EPS, gate)
+
+
+def test_two_streams_at_once():
+    T, H = 3000, 4096
+    ins = [[v.cuda() for v in inputs(T, H, torch.bfloat16, False, T, s)] for s in (1, 2)]
+    want = []
+    for x, r, xg, gm, gate in ins:
+        h = torch.empty_like(r)
+        want.append((rarn.gated_add_rms_norm(x, r, xg, gm, EPS, gate=gate, residual_out=h), h))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ins]
+    got = [(torch.empty_like(y), torch.empty_like(h)) for y, h in want]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, (x, r, xg, gm, gate), (y, h) in zip(streams, ins, got):
+            with torch.cuda.stream(s):
+                rarn.gated_add_rms_norm(x, r, xg, gm, EPS, gate=gate, residual_out=h, out=y)
+    torch.cuda.synchronize()
+    for (y, h), (y2, h2) in zip(want, got):
+        assert torch.equal(y, y2) and torch.equal(h, h2)

@@ -301,3 +301,39 @@ def test_compact_without_work():
     rarn.kv_cache_compact(cache, t, c, p[:, :1].contiguous(), torch.ones_like(n))
     rarn.kv_cache_compact(cache, t[:0], c[:0], p[:0], n[:0])
     assert torch.equal(before, cache.k) and rarn.watchdog() == 0
+
+
+def test_compact_pages_far_apart():
+    """Pages whose offsets pass 2^31 bytes."""
+    pages, H, page, D, ld = 3, 2, 4, 32, (1 << 30) + 16
+    g = torch.Generator().manual_seed(1)
+    kv = []
+    for _ in range(2):
+        d = torch.empty((pages - 1) * ld + H * page * D, dtype=torch.uint8, device="cuda")
+        d = d.as_strided((pages, H, page, D), (ld, page * D, D, 1))
+        d.copy_(torch.randint(0, 256, (pages, H, page, D), generator=g, dtype=torch.uint8))
+        kv.append(d)
+    s = [torch.rand(pages, H, page, generator=g).cuda() for _ in range(2)]
+    cache = rarn.KVCache(*kv, *s)
+    want = moved(cache, [[0, 2, 1]], [1], [[0, 3, 5, 10]])
+    rarn.kv_cache_compact(cache, ints([[0, 2, 1]]), ints([1]), ints([[0, 3, 5, 10]]), ints([4]))
+    for name, w in want.items():
+        assert torch.equal(getattr(cache, name).cpu(), w), name
+    assert rarn.watchdog() == 0
+
+
+def test_pages_made_on_one_stream_are_used_on_another():
+    s = torch.cuda.Stream()
+    for _ in range(20):
+        pages, model = make(300, 12, 3600, 16)
+        torch.cuda.synchronize()
+        held = torch.full((300,), 100, dtype=torch.int32, device="cuda")
+        zero = torch.zeros_like(held)
+        s.wait_stream(torch.cuda.current_stream())
+        pages = rarn.KVPages(pages.page_table, pages.held, pages.free_pages, pages.free_count, 16)
+        with torch.cuda.stream(s):
+            out = rarn.kv_step(pages, zero, held, 30000)
+        s.synchronize()
+        want = model.step([0] * 300, [100] * 300, 30000)
+        assert out[0].tolist() == want[0] and out[1].tolist() == want[1]
+        same_state(pages, model)

@@ -276,3 +276,40 @@ def test_in_a_graph_and_on_a_stream():
         x.copy_(y)
     graph.replay()
     assert tuple(x.tolist() for x in out) == R.verify(*b[:5], 4, b[5])
+
+
+def test_rows_far_apart():
+    """Probabilities whose offsets pass 2^31 elements, of p and of q."""
+    rows, V, ld = [3], 5000, (1 << 30) + 8
+    for kind in ("drawn", "tree"):
+        probs, tokens, starts, u, v, q, parents = inputs(rows, V, torch.bfloat16, kind, 3)
+        want = R.verify(probs, tokens, starts, u, v, 2, q, parents)
+        far = []
+        for x in (probs, q):
+            if x is None:
+                far.append(None)
+                continue
+            d = torch.empty(2 * ld + V, dtype=x.dtype, device="cuda").as_strided((3, V), (ld, 1))
+            d.copy_(x)
+            far.append(d)
+        assert run(far[0], tokens, starts, u, v, 2, far[1], parents) == want
+        del far
+
+
+def test_two_streams_at_once():
+    ins = [inputs([4] * 40, 20000, torch.float32, "drawn", s) for s in (1, 2)]
+    dev = [[x.cuda() if torch.is_tensor(x) else torch.tensor(x, device="cuda") for x in
+            (i[0], i[1], i[3], i[4], i[5])] for i in ins]
+    st = torch.tensor(ins[0][2], dtype=torch.int32, device="cuda")
+    streams = [torch.cuda.Stream() for _ in ins]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(3):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                d = dev[k]
+                outs[k].append(rarn.verify_drafts(d[0], d[1], st, d[2], d[3], 3, draft_probs=d[4]))
+    torch.cuda.synchronize()
+    for i, got in zip(ins, outs):
+        want = R.verify(*i[:5], 3, i[5])
+        assert all(tuple(x.tolist() for x in g) == want for g in got)
