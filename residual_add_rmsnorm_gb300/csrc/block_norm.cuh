@@ -35,8 +35,8 @@ __device__ __forceinline__ int64_t gate_row(const Params &p, int64_t t) {
     return g >= 0 && g < p.gates ? g : -1;
 }
 
-// Rows in registers, 16-byte packs: a warp per row, or a CTA.  Between the sums a
-// thread keeps its packs of x and r as they came and then of h as it is stored, so
+// Rows in registers, 16-byte packs: a CTA of n / 4 threads per row, down to one warp.
+// Between the sums a thread keeps its packs of x and r as they came and then of h as it is stored, so
 // that nothing is read twice; the gammas and shared gates come from L1.  kPipe: the next
 // row's loads are under way while a row is summed and written.
 template <typename T, typename TR, int VPT>
@@ -44,7 +44,7 @@ struct RowPacks {
     uint4 x[VPT], r[VPT][Res<T, TR>::N];
 };
 
-template <typename T, typename TR, int VPT>
+template <typename T, typename TR, int VPT, bool kFull>
 __device__ __forceinline__ void load_row(const Params &p, int64_t t, int j0, int js, int nv,
                                          RowPacks<T, TR, VPT> &b) {
     using RS = Res<T, TR>;
@@ -53,7 +53,7 @@ __device__ __forceinline__ void load_row(const Params &p, int64_t t, int j0, int
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int j = j0 + k * js;
-        if (j < nv) {
+        if (kFull || j < nv) {
             b.x[k] = ld_stream(x + j * RS::EPV);
 #pragma unroll
             for (int q = 0; q < RS::N; ++q)
@@ -62,10 +62,14 @@ __device__ __forceinline__ void load_row(const Params &p, int64_t t, int j0, int
     }
 }
 
-// Threads that a CTA of the kernel may have: with eight packs a thread 128 registers hold
-// x, r and h of one row, with four or fewer the next row's too.
-template <int VPT, bool kWarp>
-constexpr int kMaxThreads = kWarp ? 256 : VPT == 1 ? 1024 : 512;
+// Threads that a CTA of the kernel may have and CTAs to an SM, which set its registers.
+// Four packs a thread and the next row's take 128, and fewer cost more than the warps
+// that they would leave room for (16384 rows of 5120, binary32 residual: 155 us with
+// 128, 195 with 102, 250 with 85); a row alone leaves room for four CTAs of 160.
+template <int VPT, bool kPipe, bool kFull>
+constexpr int kMaxThreads = VPT == 1 ? 1024 : VPT == 4 && !kPipe && kFull ? 320 : 512;
+template <int VPT, bool kPipe, bool kFull>
+constexpr int kMinCtas = VPT == 4 && !kPipe && kFull ? 2 : 1;
 
 // Packs as pairs, for arithmetic two elements to an instruction.
 template <typename T>
@@ -119,32 +123,29 @@ __device__ __forceinline__ void res_pack2(const float2 (&f)[DT<T>::EPV / 2],
     }
 }
 
-template <typename T, typename TR, int VPT, bool kGate, bool kWarp, bool kPipe>
-__global__ void __launch_bounds__(kMaxThreads<VPT, kWarp>) k_block_vec(const Params p) {
+// kFull: every thread has VPT packs, none is checked against the row's end.
+template <typename T, typename TR, int VPT, bool kGate, bool kPipe, bool kFull>
+__global__ void __launch_bounds__(kMaxThreads<VPT, kPipe, kFull>, kMinCtas<VPT, kPipe, kFull>)
+    k_block_vec(const Params p) {
     using RS = Res<T, TR>;
     constexpr int E = RS::EPV;
-    __shared__ float red[kWarp ? 1 : 4][32];
-    const int nv = p.H / E;
-    const int j0 = kWarp ? threadIdx.x & 31 : threadIdx.x, js = kWarp ? 32 : blockDim.x;
-    const int per = kWarp ? blockDim.x >> 5 : 1;
-    const int64_t step = (int64_t)gridDim.x * per;
-    int64_t t = (int64_t)blockIdx.x * per + (kWarp ? threadIdx.x >> 5 : 0);
+    __shared__ float red[4][32];
+    const int nv = p.H / E, j0 = threadIdx.x, js = blockDim.x;
+    const int64_t step = gridDim.x;
+    int64_t t = blockIdx.x;
     const float inv_h = 1.f / static_cast<float>(p.H);
     const T *xg = static_cast<const T *>(p.x_gamma), *gm = static_cast<const T *>(p.gamma);
     grid_dependency_wait();
     grid_launch_dependents();
     // two sums a row, each in a buffer that the row before did not use
     int par = 0;
-    auto row_sum = [&](float v, int which) {
-        if constexpr (kWarp) return warp_sum(v);
-        else return block_sum(v, red[2 * par + which]);
-    };
+    auto row_sum = [&](float v, int which) { return block_sum(v, red[2 * par + which]); };
     RowPacks<T, TR, VPT> next;
-    if (kPipe && t < p.T) load_row<T, TR, VPT>(p, t, j0, js, nv, next);
+    if (kPipe && t < p.T) load_row<T, TR, VPT, kFull>(p, t, j0, js, nv, next);
     for (; t < p.T; t += step, par ^= 1) {
         RowPacks<T, TR, VPT> cur;
         if constexpr (kPipe) cur = next;
-        else load_row<T, TR, VPT>(p, t, j0, js, nv, cur);
+        else load_row<T, TR, VPT, kFull>(p, t, j0, js, nv, cur);
         uint4 gate[kGate ? VPT : 1];
         bool live = true;
         if constexpr (kGate) {
@@ -155,13 +156,13 @@ __global__ void __launch_bounds__(kMaxThreads<VPT, kWarp>) k_block_vec(const Par
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int j = j0 + k * js;
-                if (j < nv) gate[k] = ld_stream(row + j * E);
+                if (kFull || j < nv) gate[k] = ld_stream(row + j * E);
             }
         }
         if constexpr (kPipe)
-            if (t + step < p.T) load_row<T, TR, VPT>(p, t + step, j0, js, nv, next);
-        if constexpr (!kPipe && !kWarp) {  // the next row into L2 (2000 rows of 16384: 133 -> 126 us)
-            if (threadIdx.x == 0 && t + step < p.T) {
+            if (t + step < p.T) load_row<T, TR, VPT, kFull>(p, t + step, j0, js, nv, next);
+        if constexpr (!kPipe) {  // the next row into L2 (2000 rows of 16384: 133 -> 126 us)
+            if (j0 == 0 && t + step < p.T) {
                 prefetch_l2(static_cast<const T *>(p.x) + (t + step) * p.ldx,
                             (uint32_t)(p.H * sizeof(T)));
                 prefetch_l2(static_cast<const TR *>(p.residual) + (t + step) * p.ldr,
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kMaxThreads<VPT, kWarp>) k_block_vec(const Par
             float2 ss = {0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                if (j0 + k * js < nv) {
+                if (kFull || j0 + k * js < nv) {
                     float2 x[E / 2];
                     unpack2<T>(cur.x[k], x);
 #pragma unroll
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kMaxThreads<VPT, kWarp>) k_block_vec(const Par
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int j = j0 + k * js;
-            if (j < nv) {
+            if (kFull || j < nv) {
                 float2 n[E / 2], w[E / 2], s[E / 2];
                 unpack2<T>(cur.x[k], n);
 #pragma unroll
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kMaxThreads<VPT, kWarp>) k_block_vec(const Par
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int j = j0 + k * js;
-            if (j < nv) {
+            if (kFull || j < nv) {
                 float2 s[E / 2], w[E / 2];
                 res_unpack2<T, TR>(cur.r[k], s);
                 unpack2<T>(ld_keep(gm + j * E), w);
