@@ -9,19 +9,31 @@ namespace rarn {
 namespace block {
 
 // Every CTA has the same number of rows or one less.
-inline dim3 balanced(int64_t T, int num_sms, int threads) {
-    const int64_t slots = (int64_t)num_sms * std::min(32, std::max(1, 2048 / threads));
+inline dim3 balanced(int64_t T, int num_sms, int threads, int resident = 2048) {
+    const int64_t slots = (int64_t)num_sms * std::min(32, std::max(1, resident / threads));
     const int64_t rounds = (T + slots - 1) / slots;
     return dim3((unsigned)((T + rounds - 1) / rounds));
+}
+
+// With four packs a thread and the next row an SM holds 512 threads.  Rows of up to ten
+// rounds of these go round by round (1000 rows of 8192: 13.2 us, in CTAs for 2048
+// threads an SM, most of which wait, 16.1); more rows keep the SMs busier when a CTA that
+// ends makes room for another (8192 rows of 8192: 81 us, round by round 90).
+constexpr int kPipeThreads = 512, kRounds = 10;
+
+inline dim3 piped(int64_t T, int num_sms, int threads) {
+    const int64_t slots = (int64_t)num_sms * std::min(32, std::max(1, kPipeThreads / threads));
+    return balanced(T, num_sms, threads, T <= kRounds * slots ? kPipeThreads : 2048);
 }
 
 template <typename T, typename TR, int VPT, bool kPipe>
 cudaError_t launch_vec(const Params &p, int num_sms, int threads, bool pdl, cudaStream_t st) {
     // no thread without a pack: no bounds to check (8192 rows of 8192: 86 -> 82 us)
     const bool full = p.H / DT<T>::EPV == VPT * threads && threads <= kMaxThreads<VPT, kPipe, true>;
+    const dim3 grid = kPipe && VPT == 4 ? piped(p.T, num_sms, threads)
+                                        : balanced(p.T, num_sms, threads);
     auto go = [&](auto kernel) {
-        return launch_kernel(kernel, balanced(p.T, num_sms, threads), dim3(threads), 0, st, pdl, 1,
-                             p);
+        return launch_kernel(kernel, grid, dim3(threads), 0, st, pdl, 1, p);
     };
     if (p.gate)
         return full ? go(k_block_vec<T, TR, VPT, true, kPipe, true>)
