@@ -118,7 +118,8 @@ __device__ __forceinline__ Sums demand(const StepParams &p, int b) {
     if (n < 0 || ctx < 0 || held < 0 || held > p.pool.width || held * ps < ctx ||
         ctx + n > p.pool.width * ps)
         return Sums{-1, 0};
-    const int64_t need = (ctx + n + ps - 1) / ps - held;
+    // below 2^31 + 2^20 by now
+    const int need = (int)((uint32_t)(ctx + n + ps - 1) / (uint32_t)ps) - (int)held;
     return Sums{n, need > 0 ? need : 0};
 }
 
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kThreads) k_trim(const TrimParams p) {
     auto kept = [&](int b, int held) {
         const int n = p.lens[b];
         if (n < 0 || held < 0 || held > p.pool.width) return -1;
-        return min(held, (int)(((int64_t)n + ps - 1) / ps));
+        return min(held, (int)(((uint32_t)n + (uint32_t)ps - 1) / (uint32_t)ps));
     };
     Sums mine{0, 0}, total;
     for (int b = b0; b < b1; ++b) {
@@ -326,11 +327,11 @@ __global__ void __launch_bounds__(kMoveThreads) k_compact(const CompactParams p,
                 rises = before >= j - 1 && at > before;
                 if (rises && at > j) {
                     auto place = [&](int64_t t, int64_t *code_at, int64_t *scale_at) {
-                        const int64_t entry = t / p.cache.page_size;
-                        if (entry >= p.width) return false;
+                        const uint32_t entry = (uint32_t)t / (uint32_t)p.cache.page_size;
+                        if (entry >= (uint32_t)p.width) return false;
                         const int page = table[entry];
                         if (page < 0 || page >= p.cache.pages) return false;
-                        const int64_t in = t - entry * p.cache.page_size;
+                        const int64_t in = (uint32_t)t - entry * (uint32_t)p.cache.page_size;
                         *code_at = page * p.cache.page_stride + in * p.cache.slot_stride;
                         *scale_at = page * p.cache.s_page + in * p.cache.s_slot;
                         return true;
