@@ -1031,11 +1031,12 @@ def qk_norm_rope(q, k, q_gamma, k_gamma, eps: float, cos_sin=None, positions=Non
     if k_out is None:
         k_out = torch.empty(k.shape, dtype=dt, device=dev)
     if sections is None:
-        what, rot = "rarn_qk_norm_rope", _rotation(cos_sin, positions, style, T, dev)
+        what, fn = "rarn_qk_norm_rope", library().rarn_qk_norm_rope
+        rot = _rotation(cos_sin, positions, style, T, dev)
     else:
-        what = "rarn_qk_norm_rope_axes"
+        what, fn = "rarn_qk_norm_rope_axes", library().rarn_qk_norm_rope_axes
         rot = _rotation_axes(cos_sin, positions, style, sections, section_order, T, dev)
-    _on(dev, what, getattr(library(), what), _heads("q_out", q_out, T, Hq, D, dt, dev),
+    _on(dev, what, fn, _heads("q_out", q_out, T, Hq, D, dt, dev),
         _heads("k_out", k_out, T, hk.heads, D, dt, dev), hq, hk,
         _gamma("q_gamma", q_gamma, D, dt, dev), _gamma("k_gamma", k_gamma, D, dt, dev), rot, T, D,
         eps)
@@ -1133,11 +1134,12 @@ def qk_norm_rope_kv_write(q, k, v, q_gamma, k_gamma, eps: float, cos_sin, positi
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=dt, device=dev)
     if sections is None:
-        what, rot = "rarn_qk_norm_rope_kv_write", _rotation(cos_sin, positions, style, T, dev)
+        what, fn = "rarn_qk_norm_rope_kv_write", library().rarn_qk_norm_rope_kv_write
+        rot = _rotation(cos_sin, positions, style, T, dev)
     else:
-        what = "rarn_qk_norm_rope_axes_kv_write"
+        what, fn = "rarn_qk_norm_rope_axes_kv_write", library().rarn_qk_norm_rope_axes_kv_write
         rot = _rotation_axes(cos_sin, positions, style, sections, section_order, T, dev)
-    _on(dev, what, getattr(library(), what), _heads("q_out", q_out, T, hq.heads, D, dt, dev),
+    _on(dev, what, fn, _heads("q_out", q_out, T, hq.heads, D, dt, dev),
         cache._ref, hq, _heads("k", k, T, H, D, dt, dev), _heads("v", v, T, H, D, dt, dev),
         _gamma("q_gamma", q_gamma, D, dt, dev), _gamma("k_gamma", k_gamma, D, dt, dev), rot,
         _indices("slots", slots, torch.int64, T, dev), T, eps)

@@ -42,9 +42,9 @@ __device__ __forceinline__ int64_t gate_row(const Params &p, int64_t t) {
 }
 
 // Rows in registers, 16-byte packs: a CTA of n / 4 threads per row, down to one warp.
-// Between the sums a thread keeps its packs of x and r as they came and then of h as it is stored, so
-// that nothing is read twice; the gammas and shared gates come from L1.  kPipe: the next
-// row's loads are under way while a row is summed and written.
+// Between the sums a thread keeps its packs of x and r as they came and then of h as
+// it is stored, so that nothing is read twice; the gammas and shared gates come from
+// L1.  kPipe: the next row's loads are under way while a row is summed and written.
 template <typename T, typename TR, int VPT>
 struct RowPacks {
     uint4 x[VPT], r[VPT][Res<T, TR>::N];

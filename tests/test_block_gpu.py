@@ -30,7 +30,8 @@ def inputs(T, H, dt, wide, gates, seed, pad=0):
 # rows of a warp, a CTA, several rounds of CTAs, longer than registers, odd, one element
 SHAPES = [(1, 4096), (1, 1), (3, 7), (2, 256), (700, 512), (5, 1000), (33, 1024), (19, 1591),
           (300, 1592), (4, 2048), (700, 4096), (17, 5120), (1300, 5120), (9, 8192), (400, 8192),
-          (2, 16384), (320, 16384), (2, 20000), (3, 40000), (1, 131072), (2500, 64), (5000, 128)]
+          (2, 16384), (320, 16384), (2, 20000), (3, 40000), (1, 131072), (2500, 64), (5000, 128),
+          (320, 32768), (13000, 2048), (3000, 1024)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "bf16w", "f16", "f16w", "f32"])
