@@ -840,10 +840,7 @@ def _heads(name, t, T, heads, D, dtype, device):
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
     if stride[2] != 1 and D > 1:
         raise ValueError(f"{name} must have unit stride inside a head")
-    code = _codes.get(dtype)
-    if code is None:
-        code = _codes[dtype] = _dtype_code(t)
-    return Heads(t.data_ptr(), stride[0], stride[1], shape[1], code)
+    return Heads(t.data_ptr(), stride[0], stride[1], shape[1], _codes.get(dtype) or _code(t))
 
 
 def _indices(name, t, dtype, n, device):
@@ -865,21 +862,28 @@ def _gamma(name, g, D, dtype, device):
     return g.data_ptr()
 
 
-def _matrix(name, t, T, H, dtype, device):
-    """A [T, H] CUDA tensor with unit stride within a row as a rarn_rows."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or shape[0] != T or shape[1] != H:
-        raise ValueError(f"{name} must be [{T}, {H}], got {list(shape)}")
+def _code(t) -> int:
+    """The rarn_dtype of a tensor."""
+    dtype = t.dtype
+    code = _codes.get(dtype)
+    if code is None:
+        code = _codes[dtype] = _dtype_code(t)
+    return code
+
+
+def _matrix(name, t, shape, dtype, code, device):
+    """A CUDA tensor of ``shape`` [T, H] with unit stride within a row as a
+    rarn_rows."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.get_device() != device.index:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if stride[1] != 1 and H > 1:
+    row, one = t.stride()
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have unit stride within a row")
-    code = _codes.get(dtype)
-    if code is None:
-        code = _codes[dtype] = _dtype_code(t)
-    return Rows(t.data_ptr(), stride[0], code)
+    return Rows(t.data_ptr(), row, code)
 
 
 def gated_add_rms_norm(x, residual, x_gamma, gamma, eps: float, gate=None, gate_index=None,
@@ -898,32 +902,32 @@ def gated_add_rms_norm(x, residual, x_gamma, gamma, eps: float, gate=None, gate_
     token whose index is outside keeps its output rows and sets watchdog bit 4);
     None: no gate.  h goes to ``residual_out``, or in place into the residual
     where that is None.  ``out`` may be x.  Returns y."""
-    import torch
-    dev, dt = x.device, x.dtype
-    if x.dim() != 2:
+    dev, dt, shape = x.device, x.dtype, x.shape
+    if len(shape) != 2:
         raise ValueError("x must be [T, H]")
-    T, H = x.shape
-    rx = _matrix("x", x, T, H, dt, dev)
-    rr = _matrix("residual", residual, T, H, residual.dtype, dev)
-    if residual_out is None or residual_out is residual:
-        rh = rr
-    else:
-        rh = _matrix("residual_out", residual_out, T, H, residual.dtype, dev)
+    T, H = shape
+    code, rt = _code(x), residual.dtype
+    rx = _matrix("x", x, shape, dt, code, dev)
+    rr = rh = _matrix("residual", residual, shape, rt, _code(residual), dev)
+    if residual_out is not None and residual_out is not residual:
+        rh = _matrix("residual_out", residual_out, shape, rt, rr.dtype, dev)
     if out is None:
-        out = torch.empty(T, H, dtype=dt, device=dev)
-    ry = _matrix("out", out, T, H, dt, dev)
+        import torch
+        out = torch.empty(shape, dtype=dt, device=dev)
+    ry = _matrix("out", out, shape, dt, code, dev)
     xg, g = _gamma("x_gamma", x_gamma, H, dt, dev), _gamma("gamma", gamma, H, dt, dev)
     pg = None
     if gate is not None:
         if gate.dim() == 1:
             gate = gate[None]
         n = gate.shape[0]
-        rg = _matrix("gate", gate, n, H, dt, dev)
+        rg = _matrix("gate", gate, (n, H), dt, code, dev)
         if gate_index is None:
             if n != 1 and n != T:
                 raise ValueError(f"gate must have one row or {T}, or a gate_index")
             index = None
         else:
+            import torch
             index = _indices("gate_index", gate_index, torch.int32, T, dev)
         pg = ctypes.byref(Gate(rg.data, rg.row_stride, n, index))
     elif gate_index is not None:
@@ -1332,13 +1336,14 @@ def verify_drafts(probs, tokens, starts, uniforms, final_uniforms, most: int, dr
     dev, dt = probs.device, probs.dtype
     if probs.dim() != 2:
         raise ValueError("probs must be [rows, vocab]")
-    N, V = probs.shape
-    rp = _matrix("probs", probs, N, V, dt, dev)
+    shape, code = probs.shape, _code(probs)
+    N, V = shape
+    rp = _matrix("probs", probs, shape, dt, code, dev)
     rq = None
     if draft_probs is not None:
         if parents is not None:
             raise ValueError("draft_probs go with chains only: parents must be None")
-        rq = ctypes.byref(_matrix("draft_probs", draft_probs, N, V, dt, dev))
+        rq = ctypes.byref(_matrix("draft_probs", draft_probs, shape, dt, code, dev))
     B, W = starts.numel() - 1, most + 1
     i32, i64, f32 = torch.int32, torch.int64, torch.float32
     if B < 0 or most < 0:
