@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(kMaxThreads<VPT, kPipe, kFull>, kMinCtas<VPT, 
     }
 }
 
-// An element of a gamma or gate, which no output overlaps: a load that stores do not
-// hold back.
+// An element of a gamma, which no output overlaps: a load that stores do not hold back
+// (a gate may come from the kernel just before: plain loads).
 template <typename T>
 __device__ __forceinline__ float ld_const(const void *base, int i) {
     if constexpr (sizeof(T) == 4) {
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(NE > 0 ? 512 : 1024, NE > 0 ? 2 : 1)
             }
             if (gate) {
 #pragma unroll
-                for (int k = 0; k < NE; ++k) w[k] = ld_const<T>(gate, at[k]);
+                for (int k = 0; k < NE; ++k) w[k] = DT<T>::to_f(gate[at[k]]);
 #pragma unroll
                 for (int k = 0; k < NE; ++k) n[k] *= w[k];
             }
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(NE > 0 ? 512 : 1024, NE > 0 ? 2 : 1)
             for (int i = j0; i < p.H; i += js) {
                 float v = DT<T>::to_f(x[i]);
                 if (p.x_gamma) v = v * inv * ld_const<T>(p.x_gamma, i);
-                if (gate) v *= ld_const<T>(gate, i);
+                if (gate) v *= DT<T>::to_f(gate[i]);
                 v = DT<TR>::round(fmaf(p.residual_scale, DT<TR>::to_f(r[i]), p.scale * v));
                 if (live) h[i] = DT<TR>::from_f(v);
                 ss = fmaf(v, v, ss);
