@@ -887,11 +887,11 @@ rarn_status rarn_kv_trim(const rarn_kv_pages *pages, const int32_t *lens, void *
  *
  * probs and draft_probs have one type, any of the three, and any row stride;
  * values are taken as 0 .. 1 (NaN as 0) and rounded to multiples of 2^-46 (not for
- * u * q < p, which is exact); sums are exact from there on.  A row whose weights sum to 0, or to
- * 2 or more, gives the token -1 and sets bit 4 of the watchdog word, as do
- * tokens outside 0 .. vocab - 1 and parents outside 0 .. r - 1 (such a draft is
- * refused and takes nothing), starts that fall or lie outside and trees of more
- * than RARN_MAX_VERIFY_TREE rows (length 0).  vocab is at most
+ * u * q < p, which is exact); sums are exact from there on.  A row whose weights
+ * sum to 0, or to 2 or more, gives the token -1 and sets bit 4 of the watchdog
+ * word, as do tokens outside 0 .. vocab - 1 and parents outside 0 .. r - 1 (such
+ * a draft is refused and takes nothing), starts that fall or lie outside and
+ * trees of more than RARN_MAX_VERIFY_TREE rows (length 0).  vocab is at most
  * RARN_MAX_VERIFY_VOCAB; draft_probs together with parents:
  * RARN_ERR_UNSUPPORTED.  Any overlap of an output: RARN_ERR_ALIAS.
  */
@@ -1054,7 +1054,8 @@ rarn_status rarn_plan_fp8(rarn_op op, int64_t T, int64_t H, int32_t R, rarn_dtyp
  * wait; bit 2: a wait in a GEMM-form kernel; bit 3: a wait of the
  * tensor-parallel form's barrier between ranks.  Bit 4 is no timeout: an index
  * in device memory lay outside its table (see the attention side and a step's
- * calls), and what it named was left out, or a row drawn from was no distribution.  Bit 5: a wait of rarn_tree_attention.  Synchronises the
+ * calls), and what it named was left out, or a row drawn from was no
+ * distribution.  Bit 5: a wait of rarn_tree_attention.  Synchronises the
  * device.  If `clear` is nonzero the word is reset to 0 after reading.
  */
 rarn_status rarn_watchdog(uint32_t *flags, int clear);

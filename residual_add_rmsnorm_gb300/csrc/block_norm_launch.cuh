@@ -16,21 +16,23 @@ inline dim3 balanced(int64_t T, int num_sms, int threads, int resident = 2048) {
 }
 
 // With four packs a thread and the next row an SM holds 512 threads.  Rows of up to ten
-// rounds of these go round by round (1000 rows of 8192: 13.2 us, in CTAs for 2048
+// rounds of these go round by round (1000 rows of 8192: 13.0 us, in CTAs for 2048
 // threads an SM, most of which wait, 16.1); more rows keep the SMs busier when a CTA that
-// ends makes room for another (8192 rows of 8192: 81 us, round by round 90).
+// ends makes room for another (8192 rows of 8192: 81 us, round by round 90), but with a
+// gate do not (16384 rows of 4096: 83.7 us, round by round 82.7; 2000 of 16384 with a
+// binary32 residual 80.5, 71.3).
 constexpr int kPipeThreads = 512, kRounds = 10;
 
-inline dim3 piped(int64_t T, int num_sms, int threads) {
+inline dim3 piped(int64_t T, bool gate, int num_sms, int threads) {
     const int64_t slots = (int64_t)num_sms * std::min(32, std::max(1, kPipeThreads / threads));
-    return balanced(T, num_sms, threads, T <= kRounds * slots ? kPipeThreads : 2048);
+    return balanced(T, num_sms, threads, gate || T <= kRounds * slots ? kPipeThreads : 2048);
 }
 
 template <typename T, typename TR, int VPT, bool kPipe>
 cudaError_t launch_vec(const Params &p, int num_sms, int threads, bool pdl, cudaStream_t st) {
     // no thread without a pack: no bounds to check (8192 rows of 8192: 86 -> 82 us)
     const bool full = p.H / DT<T>::EPV == VPT * threads && threads <= kMaxThreads<VPT, kPipe, true>;
-    const dim3 grid = kPipe && VPT == 4 ? piped(p.T, num_sms, threads)
+    const dim3 grid = kPipe && VPT == 4 ? piped(p.T, p.gate != nullptr, num_sms, threads)
                                         : balanced(p.T, num_sms, threads);
     auto go = [&](auto kernel) {
         return launch_kernel(kernel, grid, dim3(threads), 0, st, pdl, 1, p);
