@@ -938,8 +938,20 @@ def gated_add_rms_norm(x, residual, x_gamma, gamma, eps: float, gate=None, gate_
 
 
 def _rotation(cos_sin, positions, style, T, device):
-    """The rarn_rotation of a call, or None without a table; positions: the
-    tensor, or its address where the caller has checked it."""
+    """The rarn_rotation of a call, or None without a table."""
+    import torch
+    if cos_sin is None:
+        return _rotation_at(cos_sin, None, style, device)
+    if positions is None:
+        raise ValueError("cos_sin needs positions")
+    if not isinstance(positions, torch.Tensor):
+        raise TypeError(f"positions must be an int64 CUDA tensor on {device}")
+    return _rotation_at(cos_sin, _indices("positions", positions, torch.int64, T, device), style,
+                        device)
+
+
+def _rotation_at(cos_sin, address, style, device):
+    """The same for positions that the caller has checked, by their address."""
     import torch
     code = ROTATION_STYLES.get(style)
     if code is None:
@@ -952,11 +964,7 @@ def _rotation(cos_sin, positions, style, T, device):
     shape = cos_sin.shape
     if len(shape) != 2:
         raise ValueError("cos_sin must be [positions, rot_dim]")
-    if positions is None:
-        raise ValueError("cos_sin needs positions")
-    if type(positions) is not int:
-        positions = _indices("positions", positions, torch.int64, T, device)
-    return Rotation(cos_sin.data_ptr(), positions, shape[0], shape[1], code)
+    return Rotation(cos_sin.data_ptr(), address, shape[0], shape[1], code)
 
 
 # axis_of_pair of a model's sections, as the C ABI takes it
@@ -992,12 +1000,13 @@ def _rotation_axes(cos_sin, positions, style, sections, order, T, device):
         raise ValueError("sections need cos_sin and positions")
     sections = sections if type(sections) is tuple else tuple(sections)
     A = len(sections)
-    if positions.dtype is not torch.int64 or positions.get_device() != device.index:
+    if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int64 or \
+            positions.get_device() != device.index:
         raise TypeError(f"positions must be an int64 CUDA tensor on {device}")
     shape, stride = positions.shape, positions.stride()
     if len(shape) != 2 or shape[0] != A or shape[1] != T or (T > 1 and stride[1] != 1):
         raise ValueError(f"positions must be [{A}, {T}] with unit stride along the tokens")
-    rot = _rotation(cos_sin, positions.data_ptr(), style, T, device)
+    rot = _rotation_at(cos_sin, positions.data_ptr(), style, device)
     amap = _axis_map(rot.rot_dim // 2, sections, order)
     return RotationAxes(rot, A, stride[0], ctypes.addressof(amap))
 
