@@ -64,11 +64,16 @@ bool apart(const Range *r, int outs, int n) {
     return true;
 }
 
+// The most dynamic shared memory of a call: k_step's two sums of every sequence.
+constexpr int kMostSums = 2 * (RARN_MAX_STEP_SEQUENCES + 1) * 4;
+
 template <typename P>
 rarn_status launch(void (*kernel)(P), unsigned grid, size_t smem, const P &p, void *stream) {
     cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // The 48 KB that any kernel may have hold its static part too (some hundred bytes here).
+    // The limit is always raised to the same value, so that no call lowers another's.
+    if (smem > 47 * 1024)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSums);
     if (e == cudaSuccess)
         e = launch_kernel(kernel, dim3(grid), dim3(pages::kThreads), smem,
                           static_cast<cudaStream_t>(stream), host::pdl_enabled(), 1, p);
