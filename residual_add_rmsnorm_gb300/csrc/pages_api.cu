@@ -22,10 +22,12 @@ rarn_status check_pages(const rarn_kv_pages *g) {
         g->page_size > RARN_MAX_PAGE_SIZE || !reaches(g->table_stride, g->sequences) ||
         g->table_width > ((int64_t(1) << 31) - 1) / g->page_size)
         return RARN_ERR_UNSUPPORTED;
-    for (const void *p : {(const void *)g->page_table, (const void *)g->held,
-                          (const void *)g->free_pages, (const void *)g->free_count,
+    for (const void *p : {(const void *)g->free_pages, (const void *)g->free_count,
                           (const void *)g->ticket})
         if (!p || !on(p, 4)) return RARN_ERR_INVALID_ARG;
+    // empty without sequences, and then often without an address
+    for (const void *p : {(const void *)g->page_table, (const void *)g->held})
+        if ((!p && g->sequences > 0) || !on(p, 4)) return RARN_ERR_INVALID_ARG;
     return RARN_OK;
 }
 
