@@ -308,13 +308,14 @@ rarn_status rarn_reduce_add_rms_norm_fp8in(void *y, const void *partials, int32_
  * one: that or RARN_F32.  gate (NULL: none): `rows` rows of H elements, one
  * for all tokens (rows == 1), one per token (rows == T), or any number with
  * index[t] naming token t's row; a token whose index is outside keeps its rows
- * of y and residual_out as they were (bit 4 of the watchdog word).  scale and
- * residual_scale must be finite.  y may equal x and residual_out the residual
- * (same data and row stride); any other overlap of an output returns
- * RARN_ERR_ALIAS, judged on the row spans.  With every base, stride and H a
- * multiple of 16 bytes kernels with 16-byte accesses run, otherwise one that
- * goes element by element.  A stride times its rows is at most
- * RARN_MAX_STRIDE; everything else is as for the general forms.
+ * of y and residual_out as they were (bit 4 of the watchdog word).  Without
+ * tokens (T == 0) the gate may have no rows.  scale and residual_scale must be
+ * finite.  y may equal x and residual_out the residual (same data and row
+ * stride); any other overlap of an output returns RARN_ERR_ALIAS, judged on the
+ * row spans.  With every base, stride and H a multiple of 16 bytes kernels with
+ * 16-byte accesses run, otherwise one that goes element by element.  A stride
+ * times its rows is at most RARN_MAX_STRIDE; everything else is as for the general
+ * forms.
  */
 typedef struct rarn_gate {
     const void *data;

@@ -60,7 +60,10 @@ extern "C" rarn_status rarn_gated_add_rms_norm(rarn_rows y, rarn_rows residual_o
         !std::isfinite(residual_scale))
         return RARN_ERR_INVALID_ARG;
     if (H > RARN_MAX_H || T > RARN_MAX_T) return RARN_ERR_UNSUPPORTED;
-    if (gate && (gate->rows < 1 || (!gate->index && gate->rows != 1 && gate->rows != T)))
+    if (gate && gate->rows < 0) return RARN_ERR_INVALID_ARG;
+    // without tokens a gate for each has no rows, and their indices no address
+    if (gate && T > 0 &&
+        (gate->rows < 1 || (!gate->index && gate->rows != 1 && gate->rows != T)))
         return RARN_ERR_INVALID_ARG;
     if (y.dtype != x.dtype || residual_out.dtype != residual.dtype ||
         (residual.dtype != x.dtype && residual.dtype != RARN_F32))
