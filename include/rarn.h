@@ -833,7 +833,9 @@ typedef struct rarn_kv_pages {
  * pages that they need and the sequence does not hold are taken from the end
  * of the free ones, in order of sequences and tokens.  Then
  *   starts[b]     rows of the sequences before b (B + 1 values);
- *   positions[r]  context_lens[b] + r - starts[b], for row r of sequence b;
+ *   positions[r]  context_lens[b] + r - starts[b], for row r of sequence b: those of
+ *                 a chain.  In a tree a row's position is context_lens[b] plus its
+ *                 depth below row 0: the caller adds depth - (r - starts[b]);
  *   slots[r]      page * page_size + slot of that token, as
  *                 rarn_kv_cache_write takes it;
  * rows starts[B] .. tokens - 1 get slot -1 and position 0 (padding that the

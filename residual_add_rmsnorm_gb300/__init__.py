@@ -27,6 +27,7 @@ the drafts' verification; the cache's tidying after it):
 
     pages = KVPages.empty(sequences, width, num_pages, page_size)
     starts, slots, positions, served = kv_step(pages, context_lens, new_lens, tokens)
+    positions += (depths - rows) * (slots >= 0)     # a tree's; a chain's as they are
     new_tokens, path, lengths = verify_drafts(probs, tokens, starts, uniforms, final_uniforms, most)
     kv_cache_compact(cache, pages.page_table, context_lens, path, lengths)
     kv_trim(pages, kept_lens)
@@ -1288,10 +1289,14 @@ def kv_step(pages: KVPages, context_lens, new_lens, tokens: int, starts=None, sl
     behind its context_lens[b] (int32 CUDA tensors of pages.sequences values), and
     gets the pages that they need.  Returns (starts [B + 1] int32, slots [tokens]
     int64, positions [tokens] int64, served [1] int32): row r of sequence b is r -
-    starts[b] tokens behind its context; rows past the last sequence get slot -1 and
-    position 0.  served < B: rows (``tokens``) or free pages ran out at that
-    sequence, and it and those behind it got none.  Lengths that make no sense
-    leave their sequence without rows and set watchdog bit 4."""
+    starts[b] tokens behind its context, in slot and position; rows past the last
+    sequence get slot -1 and position 0.  That is a chain's position; a tree's row
+    lies as many tokens behind the context as it is deep, so for trees add each
+    row's depth less its number in its sequence before the rows are turned (keys
+    that kv_cache_compact moves stay turned as they were).  served < B: rows
+    (``tokens``) or free pages ran out at that sequence, and it and those behind it
+    got none.  Lengths that make no sense leave their sequence without rows and set
+    watchdog bit 4."""
     import torch
     dev, B = pages.device, pages.sequences
     if starts is None:
