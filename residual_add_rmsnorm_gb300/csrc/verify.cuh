@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify(const Params p, int clus
             }
             return;
         }
-        const int64_t target = (int64_t)((double)v * (double)all) - ahead;  // rounded down
+        // the whole part: the product has up to 71 bits, rounded down as the cut is
+        const int64_t target = (int64_t)__dmul_rd((double)v, (double)all) - ahead;
         if (target < 0 || target >= total) return;  // another CTA's
         if (target >= before && target < before + mine) {
             int64_t sum = before;

@@ -1,0 +1,51 @@
+"""GPU tests of the verification at the edges of its definition: draws that end exactly on a
+border."""
+import random
+
+import pytest
+import torch
+
+import residual_add_rmsnorm_gb300 as rarn
+from test_verify_gpu import run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _watchdog():
+    rarn.watchdog(clear=True)
+    yield
+
+
+def halves(units):
+    """A weight of `units` 2^-46 as two binary32 numbers, both not zero."""
+    low = units & (1 << 22) - 1
+    return [(units - low) * 2.0 ** -46, low * 2.0 ** -46]
+
+
+def borders(count, seed):
+    """(u, total, the whole part of u total) whose product a binary64 multiplication that
+    rounds to nearest lifts to the next whole number; in units of 2^-24 and 2^-46."""
+    r, got = random.Random(seed), [(10402440, 60473987187256)]
+    while len(got) < count:
+        u, total = r.randrange(1 << 23, 1 << 24), r.randrange(1 << 45, 1 << 46)
+        if int(u * 2.0 ** -24 * float(total)) > u * total >> 24:
+            got.append((u, total))
+    return [(u, t, u * t >> 24) for u, t in got]
+
+
+def test_a_draw_that_ends_on_a_border():
+    rows, want, numbers = [], [], []
+    for u, total, whole in borders(150, 1):
+        # the first two tokens' weight is just more than u total, or just not
+        for first, token in ((whole + 1, 1), (whole, 2)):
+            if first % (1 << 22) == 0 or (total - first) % (1 << 22) == 0:
+                continue
+            rows.append(halves(first) + halves(total - first))
+            want.append(token)
+            numbers.append(u * 2.0 ** -24)
+    B = len(rows)
+    got = run(torch.tensor(rows), [0] * B, list(range(B + 1)), torch.zeros(B),
+              torch.tensor(numbers), 0)
+    assert got[0] == [[w] for w in want]
+    assert rarn.watchdog() == 0
