@@ -267,9 +267,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify(const Params p, int clus
             bool ok = false;
             if (r < kMaxTree) s_token[r] = x;
             if (x >= 0) {
-                const float u = p.u[lo + r - 1], px = DT<T>::to_f(probs[(r - 1) * p.ldp + x]);
+                const float u = p.u[lo + r - 1], px = unit(DT<T>::to_f(probs[(r - 1) * p.ldp + x]));
                 if (drafts)  // exact in binary64
-                    ok = (double)u * (double)DT<T>::to_f(drafts[r * p.ldq + x]) < (double)px;
+                    ok = (double)u * (double)unit(DT<T>::to_f(drafts[r * p.ldq + x])) < (double)px;
                 else
                     ok = fixed(u) < fixed(px);
             }

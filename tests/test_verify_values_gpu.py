@@ -1,5 +1,5 @@
 """GPU tests of the verification at the edges of its definition: draws that end exactly on a
-border."""
+border, probabilities outside 0 .. 1 in the tests of drafts."""
 import random
 
 import pytest
@@ -9,6 +9,8 @@ import residual_add_rmsnorm_gb300 as rarn
 from test_verify_gpu import run
 
 pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
 
 
 @pytest.fixture(autouse=True)
@@ -49,3 +51,23 @@ def test_a_draw_that_ends_on_a_border():
               torch.tensor(numbers), 0)
     assert got[0] == [[w] for w in want]
     assert rarn.watchdog() == 0
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16, torch.float16])
+def test_drafts_are_tested_by_values_of_0_to_1(dt):
+    """u q < p with both taken as 0 .. 1 and NaN as 0."""
+    cases = [(p, q, u) for p in (0.0, 0.25, 1.0, 2.0, -1.0, NAN, INF, -INF)
+             for q in (0.0, 0.5, 1.0, 3.0, -0.5, NAN, INF, -INF) for u in (0.0, 0.25, 0.75)]
+
+    def unit(x):
+        return min(max(x, 0.0), 1.0) if x == x else 0.0
+
+    # token 1 is drafted; token 0 can always be drawn
+    probs = torch.tensor([[0.5, p] if row == 0 else [0.5, 0.25]
+                          for p, q, u in cases for row in (0, 1)], dtype=dt)
+    drafts = torch.tensor([[0.0, q] for p, q, u in cases for row in (0, 1)], dtype=dt)
+    B = len(cases)
+    got = run(probs, [0, 1] * B, list(range(0, 2 * B + 1, 2)),
+              torch.tensor([u for p, q, u in cases for row in (0, 1)]), torch.zeros(B), 1, drafts)
+    for (p, q, u), n in zip(cases, got[2]):
+        assert n == (2 if u * unit(q) < unit(p) else 1), (p, q, u)
