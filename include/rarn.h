@@ -888,14 +888,14 @@ rarn_status rarn_kv_trim(const rarn_kv_pages *pages, const int32_t *lens, void *
  * drafts' tokens and the drawn one.  Both dense [B, most + 1]; entries behind are
  * -1.  A sequence without rows has length 0.
  *
- * probs and draft_probs have one type, any of the three, and any row stride;
- * values are taken as 0 .. 1 (NaN as 0) and rounded to multiples of 2^-46 (not for
- * u * q < p, which is exact); sums are exact from there on.  A row whose weights
- * sum to 0, or to 2 or more, gives the token -1 and sets bit 4 of the watchdog
- * word, as do tokens outside 0 .. vocab - 1 and parents outside 0 .. r - 1 (such
- * a draft is refused and takes nothing), starts that fall or lie outside and
- * trees of more than RARN_MAX_VERIFY_TREE rows (length 0).  vocab is at most
- * RARN_MAX_VERIFY_VOCAB; draft_probs together with parents:
+ * probs and draft_probs have one type, any of the three, and any row stride from
+ * vocab on; values are taken as 0 .. 1 (NaN as 0) and rounded to multiples of 2^-46
+ * (not for u * q < p, which is exact); sums and the draw are exact from there on.
+ * A row whose weights sum to 0, or to 2 or more, gives the token -1 and sets bit 4
+ * of the watchdog word, as do tokens outside 0 .. vocab - 1 and parents outside 0 ..
+ * r - 1 (such a draft is refused and takes nothing from what is drawn from), starts
+ * that fall or lie outside and trees of more than RARN_MAX_VERIFY_TREE rows (length
+ * 0).  vocab is at most RARN_MAX_VERIFY_VOCAB; draft_probs together with parents:
  * RARN_ERR_UNSUPPORTED.  Any overlap of an output: RARN_ERR_ALIAS.
  */
 #define RARN_MAX_VERIFY_VOCAB (1 << 20)

@@ -256,11 +256,12 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify(const Params p, int clus
     };
     bool bad = false;
     int length, last;
-    bool refused;  // whether drafts below the last accepted row were refused
+    bool refused;  // whether tokens drafted below the last accepted row were refused
     if (!tree) {
-        // the first refusal; rows from W on are not looked at
+        // the first refusal, its last bit whether a token was refused (what is none takes
+        // nothing); rows from W on are not looked at
         const int most = min(n, W);
-        if (tid == 0) s_stop = most;
+        if (tid == 0) s_stop = 2 * most;
         __syncthreads();
         for (int r = 1 + tid; r < most; r += kThreads) {
             const int x = token_of(r);
@@ -274,12 +275,12 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify(const Params p, int clus
                     ok = fixed(u) < fixed(px);
             }
             bad |= x < 0;
-            if (!ok) atomicMin(&s_stop, r);
+            if (!ok) atomicMin(&s_stop, 2 * r + (x >= 0));
         }
         __syncthreads();
-        length = s_stop;
+        length = s_stop >> 1;
         last = length - 1;
-        refused = length < W && length < n;
+        refused = s_stop & 1;
     } else {
         for (int r = tid; r < n; r += kThreads) {
             int up = -1, x = -1;
@@ -347,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify(const Params p, int clus
 
     // the draw
     const T *pr = probs + last * p.ldp;
-    const T *qr = drafts && refused ? drafts + (last + 1) * p.ldq : nullptr;
     int mode = !refused ? W_ALL : drafts ? W_REST : W_WITHOUT;
+    const T *qr = mode == W_REST ? drafts + (last + 1) * p.ldq : pr;
     const float v = fminf(unit(p.v[b]), 0.99999994f);
     // the refused children's tokens, in s_next
     if (tid == 0) s_gone = 0;
@@ -359,8 +360,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify(const Params p, int clus
             for (int s = last + 1 + tid; s < n; s += kThreads)
                 if (s_parent[s] == last && s_mass[s] > 0) refuse(s_token[s]);
         } else if (tid == 0) {  // a chain's only child
-            const int x = last + 1 < kMaxTree ? s_token[last + 1] : token_of(last + 1);
-            if (x >= 0) refuse(x);
+            refuse(last + 1 < kMaxTree ? s_token[last + 1] : token_of(last + 1));
         }
     }
     __syncthreads();

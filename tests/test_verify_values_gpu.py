@@ -1,5 +1,5 @@
 """GPU tests of the verification at the edges of its definition: draws that end exactly on a
-border, probabilities outside 0 .. 1 in the tests of drafts."""
+border, probabilities outside 0 .. 1 in the tests of drafts, drafts that are no tokens."""
 import random
 
 import pytest
@@ -10,6 +10,7 @@ from test_verify_gpu import run
 
 pytestmark = pytest.mark.gpu
 
+INDEX_BIT = 16
 NAN, INF = float("nan"), float("inf")
 
 
@@ -71,3 +72,21 @@ def test_drafts_are_tested_by_values_of_0_to_1(dt):
               torch.tensor([u for p, q, u in cases for row in (0, 1)]), torch.zeros(B), 1, drafts)
     for (p, q, u), n in zip(cases, got[2]):
         assert n == (2 if u * unit(q) < unit(p) else 1), (p, q, u)
+
+
+@pytest.mark.parametrize("token", [-1, 3, 2 ** 40])
+def test_a_draft_that_is_no_token_takes_nothing(token):
+    """Behind it the target's own row is drawn from, whatever the drafts were drawn from."""
+    p = torch.tensor([[0.5, 0.25, 0.25]] * 3)
+    q = torch.tensor([[1.0, 0.0, 0.0]] * 3)
+    for v, x in ((0.0, 0), (0.49, 0), (0.5, 1), (0.75, 2)):
+        v = torch.tensor([v])
+        for probs in (q, None):
+            # refused as the first draft, and behind an accepted one
+            got = run(p, [0, token, 0], [0, 3], torch.zeros(3), v, 2, probs)
+            assert got == ([[x, -1, -1]], [[0, -1, -1]], [1])
+            got = run(p, [0, 0, token], [0, 3], torch.zeros(3), v, 2, probs)
+            assert got == ([[0, x, -1]], [[0, 1, -1]], [2])
+        got = run(p, [0, token, token], [0, 3], torch.zeros(3), v, 2, None, [-1, 0, 0])
+        assert got == ([[x, -1, -1]], [[0, -1, -1]], [1])
+    assert rarn.watchdog() == INDEX_BIT
