@@ -102,6 +102,7 @@ class Rows(ctypes.Structure):
 
 
 MAX_STEP_SEQUENCES = 8192
+MAX_PAGE_SIZE = 1 << 20
 TP_MAX_RANKS = 8
 TP_SIGNAL_BYTES = 1024 * TP_MAX_RANKS * 4
 IPC_HANDLE_BYTES = 96
@@ -1256,6 +1257,8 @@ class KVPages:
 
     def __init__(self, page_table, held, free_pages, free_count, page_size: int):
         import torch
+        if not 1 <= page_size <= MAX_PAGE_SIZE:  # ctypes would cut it to 32 bits
+            raise ValueError(f"page_size must be 1 .. {MAX_PAGE_SIZE}")
         dev = page_table.device
         table, stride, B, width = _page_table(page_table, dev)
         self.page_table, self.held = page_table, held
