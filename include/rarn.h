@@ -856,7 +856,9 @@ rarn_status rarn_kv_step(const rarn_kv_pages *pages, const int32_t *context_lens
  * sequence) and gives back the others, whose table entries become -1: pages of
  * refused drafts return in the order from which rarn_kv_step takes the same
  * ones again.  A negative length keeps its pages; that, a page outside, or more
- * pages than there are (nothing is then done) set bit 4.
+ * pages than there are (nothing is then done) set bit 4.  A page outside goes back
+ * as it is, in its place among the free ones: the step that takes it finds it
+ * outside again (slot -1, bit 4).  Who wants it gone makes the pages anew.
  */
 rarn_status rarn_kv_trim(const rarn_kv_pages *pages, const int32_t *lens, void *stream);
 

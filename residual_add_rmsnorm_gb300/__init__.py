@@ -1322,7 +1322,9 @@ def kv_step(pages: KVPages, context_lens, new_lens, tokens: int, starts=None, sl
 
 def kv_trim(pages: KVPages, lens) -> None:
     """Every sequence keeps the pages of its first lens[b] tokens (int32 CUDA
-    tensor; 0: a finished sequence) and gives the others back."""
+    tensor; 0: a finished sequence) and gives the others back.  A negative length
+    keeps its pages; that, and a table entry that is no page (it goes back as it is,
+    and the step that takes it gets no slots in it), set watchdog bit 4."""
     import torch
     _on(pages.device, "rarn_kv_trim", library().rarn_kv_trim, pages._ref,
         _indices("lens", lens, torch.int32, pages.sequences, pages.device))
