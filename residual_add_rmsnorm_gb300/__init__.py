@@ -814,9 +814,10 @@ def _on(device, what, fn, *args):
     global _get_device, _raw_stream
     if _get_device is None:
         import torch
-        _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda i: torch.cuda.current_stream(i).cuda_stream)
+        # last: another thread that sees it uses both
+        _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     i = device.index
     if _get_device() == i:
         status = fn(*args, _raw_stream(i))
