@@ -839,12 +839,13 @@ typedef struct rarn_kv_pages {
  *   slots[r]      page * page_size + slot of that token, as
  *                 rarn_kv_cache_write takes it;
  * rows starts[B] .. tokens - 1 get slot -1 and position 0 (padding that the
- * writes leave out).  A sequence with new_lens 0 has no rows and keeps its pages.
+ * writes leave out).  A sequence with new_lens 0 has no rows and keeps its pages;
+ * its context is not looked at.
  * served[0]: how many sequences were served.  It is B unless rows or pages run
  * out: the first sequence whose rows would pass `tokens` or whose pages the free
- * ones, and all behind it, get no rows and no pages.  A sequence whose lengths
- * are negative or need more than table_width pages, or that holds fewer pages
- * than its cached tokens fill, has no rows; that, and a page outside 0 ..
+ * ones, and all behind it, get no rows and no pages.  Any other sequence whose
+ * lengths are negative or need more than table_width pages, or that holds fewer
+ * pages than its cached tokens fill, has no rows; that, and a page outside 0 ..
  * num_pages - 1 (slot -1), sets bit 4 of the watchdog word.
  */
 rarn_status rarn_kv_step(const rarn_kv_pages *pages, const int32_t *context_lens,

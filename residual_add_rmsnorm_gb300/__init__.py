@@ -1254,7 +1254,8 @@ class KVPages:
     page_table [sequences, width] (unit stride along a row; what tree_attention and
     kv_cache_read take), held [sequences], free_pages [num_pages], free_count [1].
     A page belongs to one sequence at a time; calls on one object must be
-    ordered."""
+    ordered.  One that is made while a graph is captured belongs to that graph's
+    replays: its word of the calls' own is zeroed there."""
 
     def __init__(self, page_table, held, free_pages, free_count, page_size: int):
         import torch

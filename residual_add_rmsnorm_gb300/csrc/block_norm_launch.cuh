@@ -18,9 +18,12 @@ inline dim3 balanced(int64_t T, int num_sms, int threads, int resident = 2048) {
 // With four packs a thread and the next row an SM holds 512 threads.  Rows of up to ten
 // rounds of these go round by round (1000 rows of 8192: 13.0 us, in CTAs for 2048
 // threads an SM, most of which wait, 16.1); more rows keep the SMs busier when a CTA that
-// ends makes room for another (8192 rows of 8192: 81 us, round by round 90), but with a
-// gate do not (16384 rows of 4096: 83.7 us, round by round 82.7; 2000 of 16384 with a
-// binary32 residual 80.5, 71.3).
+// ends makes room for another (8192 rows of 8192: 81 us, round by round 90).  With a gate
+// round by round is the better one or as good (bfloat16, one gate, without the rule and
+// with it: 8192 rows of 8192 86.8 and 85.7 us, with nine gates 102.2 and 90.0, a gate a row
+// 108.8 and 108.4; 16384 of 4096 83.5 and 82.7, of 5120 107.2 and 107.7, of 7168 160.5 and
+// 154.6; 2000 of 16384 53.2 and 49.1, with a binary32 residual 79.5 and 69.9) but for rows
+// of one warp (60000 of 1024 75.5 and 78.4, 30000 of 2048 77.4 and 75.6).
 constexpr int kPipeThreads = 512, kRounds = 10;
 
 inline dim3 piped(int64_t T, bool gate, int num_sms, int threads) {

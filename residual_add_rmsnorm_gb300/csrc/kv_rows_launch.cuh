@@ -29,7 +29,8 @@ inline cudaError_t launch_head_group(const RowParams &p, int num_sms, bool pdl, 
     }
     const int chunks = nq + nk + nv;
     return launch_kernel(k_head_rows<T, LG, kInter, kAxes>,
-                         dim3((unsigned)((p.T + 3) / 4 * chunks)), dim3(128), 0, st, pdl, 1, p, per, nq, nk, chunks);
+                         dim3((unsigned)((p.T + 3) / 4 * chunks)), dim3(128), 0, st, pdl, 1, p,
+                         per, nq, nk, chunks);
 }
 
 template <typename T, int LG>

@@ -23,7 +23,7 @@
 // is memory, or for few sequences the chain of launch, indices, the accepted row, its
 // sums and the draw: a cluster of CTAs takes a sequence, each a part of the row.
 // Measured: 64 chains of up to 6 rows with draft probabilities, 128256 tokens, binary32,
-// 13.5 us (9.7 at a copy's rate), 128 of them 20.8 us (19.3); one chain over 32000 tokens
+// 13.7 us (9.7 at a copy's rate), 128 of them 22.3 us (19.3); one chain over 32000 tokens
 // 5.6 us; 16 trees of up to 32 rows over 50257 tokens 7.5 us.
 #pragma once
 
